@@ -18,6 +18,11 @@
  *     (rk_reduce_all2), and scans, the prefix folds of PR #202 (rk_scan,
  *     rk_scan_dims).
  *
+ * Beside them stand the reductions and scans that a language model's serving
+ * step makes around its model: softmax of lines (rk_softmax), verification of
+ * drafted tokens (rk_draft_verify), block tables and slot maps
+ * (rk_block_tables, rk_slot_map); their arguments are described with them.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Arrays are column-major (Julia semantics).  `shape[d]` is the extent of
@@ -282,6 +287,131 @@ int rk_scan_dims(int op, int in_dtype, int acc_dtype, int out_dtype, const void 
 int rk_scan(int op, int in_dtype, int acc_dtype, int out_dtype, const void *ptr, int64_t n,
             const void *init, int inclusive, void *out, void *workspace, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Serving operators.  The reductions and scans around a language model's step:
+ * logits to probabilities, drafted tokens verified, and the lengths that
+ * result turned into block tables and slots, with no host in between.  Lines
+ * are contiguous, line l at base + l * stride (elements; a line may start at
+ * any element).  They are asynchronous, enqueue kernels only (so they may be
+ * captured into a HIP graph; captured calls use no per-stream slot, and a
+ * graph may be replayed on any stream, replays that share buffers ordered by
+ * the caller), and take the size of their workspace, which is checked.
+ * Device data that a host cannot check (offsets, token and block ids) is
+ * clamped or ignored where it is out of range, as said with each call; nothing
+ * outside the given buffers is read or written.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of device workspace rk_softmax needs on the current device (0 when
+ * the call takes one launch, and for invalid arguments). */
+size_t rk_softmax_workspace_size(int in_dtype, int out_dtype, int64_t n, int64_t lines);
+
+/*
+ * Softmax of `lines` lines of n entries:
+ *   out_i = exp((x_i - m) / t) / sum_j exp((x_j - m) / t),   m = max_j x_j
+ * with the line's temperature t = temperature[line] (device array; NULL: 1).
+ * Statistics are float32 and the result is rounded once to out_dtype; both
+ * dtypes are f32, bf16 or f16.  An entry of -inf is masked: 0 at every
+ * temperature; a line of nothing else gives zeros.  t <= 0 puts 1 on the
+ * first largest entry, 0 elsewhere.  A NaN in the line, a NaN temperature, or
+ * +inf with t > 0, makes the whole line NaN.  Results below 2^-126 are 0.
+ *   x_stride    elements between lines (>= 0; 0 reads one line for all)
+ *   out         device pointer; may be x itself with the same stride and
+ *               element size, or other columns of the same rows; any other
+ *               overlap is rejected.  Entries between lines are left alone.
+ *   workspace   device pointer to workspace_bytes >= rk_softmax_workspace_size
+ *               bytes, aligned to 8 (may be NULL only if that size is 0).
+ * Returns an rk_status.
+ */
+int rk_softmax(int in_dtype, int out_dtype, const void *x, int64_t n, int64_t lines, int64_t x_stride,
+               const float *temperature, void *out, int64_t out_stride, void *workspace, size_t workspace_bytes,
+               void *stream);
+
+/* Bytes of device workspace rk_draft_verify needs (0 for invalid arguments
+ * and for no requests). */
+size_t rk_draft_verify_workspace_size(int prob_dtype, int64_t vocab, int64_t n_req);
+
+/*
+ * Verification of drafted tokens.  Request b has drafts i in [starts[b],
+ * starts[b + 1]) (starts: n_req + 1 device int32; NULL: max_draft for every
+ * request, n_draft = n_req * max_draft), draft i the token drafted[i] with
+ * the draft's probabilities in line i of q, and the target's probabilities for
+ * it in line i + b of p; line starts[b + 1] + b of p is the target's for the
+ * token after the last draft.  In order, token x is kept while
+ *   u[i] * q_i(x) < p_i(x)          (evaluated exactly)
+ * At the first that is not, the next token is drawn from max(p_i - q_i, 0)
+ * (from p_i where that leaves nothing), after the last kept one from p: the
+ * first index whose running sum, in float64, passes r[b] times the whole sum
+ * (the last index of positive weight where rounding lets none pass).
+ *   q           NULL: the drafts have no probabilities (q_i is 1 at the token)
+ *   u, r        device float32, n_draft and n_req uniform numbers of [0, 1)
+ *   tokens      n_req lines of max_draft + 1: the kept tokens, the drawn one
+ *               (-1 where the target's line weighs nothing), -1 behind it
+ *   accepted    n_req int32: how many drafts each request kept
+ * prob_dtype: f32, bf16 or f16, of p and q; they need not sum to 1, and what
+ * is not a positive finite number weighs nothing.  token_dtype: i32 or i64, of drafted and
+ * tokens.  A drafted token outside [0, vocab) is turned down.  starts is
+ * clamped into [0, n_draft], and drafts beyond max_draft are ignored.  No
+ * output may overlap an input.  vocab >= 1.  workspace: workspace_bytes >=
+ * rk_draft_verify_workspace_size bytes, aligned to 8; calls that may overlap
+ * need one each.  Returns an rk_status.
+ */
+int rk_draft_verify(int prob_dtype, int token_dtype, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                    int64_t vocab, int64_t n_req, int64_t n_draft, int max_draft, const int32_t *starts,
+                    const void *drafted, const float *u, const float *r, void *tokens, int32_t *accepted,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace rk_block_tables needs (0 for invalid arguments). */
+size_t rk_block_tables_workspace_size(int64_t n_req);
+
+/*
+ * Brings block tables to the requests' lengths.  A request of len tokens needs
+ * ceil(len / block_size) blocks (at most max_blocks); table line b names the
+ * held[b] it has.  Free blocks wait in a ring of ring_size places, at places
+ * head .. tail - 1 (modulo ring_size).  Blocks a request has too many go, in
+ * order of request and position, to the ring's end; those it lacks are taken
+ * in the same order from the ring's front, blocks given back in this call
+ * last.  Where the free blocks run out, later ones are missing: held_out says
+ * what every request has, and a later call goes on from there.
+ *   lens        n_req int32 (negative: 0; 0 gives all blocks back)
+ *   held        n_req int32 (clamped into [0, max_blocks]); held_out may be held
+ *   table       n_req lines of max_blocks int32, in place; entries that are
+ *               not newly taken are left as they were
+ *   ring        ring_size int32, in place
+ *   state       2 int64: head, tail (0 <= tail - head <= ring_size).
+ *   state_out   4 int64: head and tail afterwards, blocks missing, and blocks
+ *               given back that found no place in the ring; may be state
+ * Everything else that is written may not overlap anything.  workspace:
+ * workspace_bytes >= rk_block_tables_workspace_size bytes, aligned to 8;
+ * calls that may overlap need one each.  Returns an rk_status.
+ */
+int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const int32_t *held, int32_t *held_out,
+                    int32_t *table, int64_t table_stride, int max_blocks, int32_t *ring, int64_t ring_size,
+                    const int64_t *state, int64_t *state_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Slots of the new tokens of a batch.  Request b has lens[b] tokens, the last
+ * fresh[b] of them new (clamped into [0, max(lens[b], 0)]); the batch is the
+ * requests' new tokens one after the other.  For token t of it, number i of
+ * request b:
+ *   requests[t]  = b
+ *   positions[t] = lens[b] - fresh[b] + i
+ *   slots[t]     = table[b][positions[t] / block_size] * block_size
+ *                  + positions[t] % block_size
+ * and starts[b] is the batch's tokens before request b (starts[n_req]: all;
+ * sums past 2^31 - 1 stay there).  A slot is -1 where the block lies behind
+ * held[b] or max_blocks, or its id outside [0, n_blocks).  Entries behind the
+ * batch, up to `capacity`, hold slot -1, position 0, request -1; tokens beyond
+ * capacity are left out.
+ *   slots        capacity elements of slot_dtype, i32 (n_blocks * block_size
+ *                <= 2^31) or i64
+ *   positions, requests  capacity int32 each, or NULL
+ *   starts       n_req + 1 int32
+ * No output may overlap an input or another.  Returns an rk_status.
+ */
+int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int block_size, const int32_t *table,
+                int64_t table_stride, int max_blocks, const int32_t *held, int64_t n_blocks, int slot_dtype,
+                int64_t capacity, void *slots, int32_t *positions, int32_t *requests, int32_t *starts, void *stream);
+
 /* Static, human-readable name of an rk_status value. */
 const char *rk_status_string(int status);
 
@@ -313,10 +443,12 @@ typedef enum {
     RK_KERNEL_SCAN_LINES = 11,  /* scan: one thread per line along a strided scan dim */
     RK_KERNEL_SCAN_COLUMNS = 12,/* scan: tiles of contiguous lines x scan positions, look-back along
                                    a strided scan dim (+ a clearing launch) */
-    RK_KERNEL_SCAN_TRANSPOSE = 13 /* scan: input and output contiguous along different axes (a
+    RK_KERNEL_SCAN_TRANSPOSE = 13, /* scan: input and output contiguous along different axes (a
                                    transposed or permuted view): tiles of lines x scan positions
                                    staged through LDS, look-back along the scan dim (+ a clearing
                                    launch) */
+    RK_KERNEL_SOFTMAX_SPLIT = 14, /* softmax: several blocks a line, statistics first, then the line */
+    RK_KERNEL_DRAFT_VERIFY = 15   /* draft verification: a wave per tile of a request's line */
 } rk_kernel;
 
 typedef struct {
@@ -351,6 +483,12 @@ int rk_plan_scan(int in_dtype, int acc_dtype, int out_dtype, const void *ptr, co
                  const int64_t *shape, const int64_t *strides, int dim, int num_cus,
                  rk_plan_info *info);
 
+/* Plans of rk_softmax (split: blocks per line) and rk_draft_verify (split:
+ * blocks per request; tile_outputs: vocabulary entries a wave sums; launches as
+ * outside a capture). */
+int rk_plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int num_cus, rk_plan_info *info);
+int rk_plan_draft_verify(int prob_dtype, int64_t vocab, int64_t n_req, int num_cus, rk_plan_info *info);
+
 /* Whether a split reduction may finish inside its first launch (block 0
  * collecting tagged partials, or the last block to arrive; the default)
  * instead of a second launch.  Both give the same
@@ -358,8 +496,8 @@ int rk_plan_scan(int in_dtype, int acc_dtype, int out_dtype, const void *ptr, co
  * wide.  Returns the previous setting (1 or 0). */
 int rk_debug_set_fused_finish(int enable);
 
-/* Benchmark hook: while both are non-NULL, every later rk_reduce_*, rk_scan*
- * and rk_debug_stream_read call made by this host thread records hipEvent_t
+/* Benchmark hook: while both are non-NULL, every later rk_reduce_*, rk_scan*,
+ * serving and rk_debug_stream_read call made by this host thread records hipEvent_t
  * `begin` when its first kernel starts and `end` when it ends, on the call's
  * stream (the events ride on that kernel's dispatch packet).  Pass NULLs to
  * stop.  Returns an rk_status. */
@@ -408,7 +546,7 @@ int rk_stream_timeouts(void *stream, uint64_t *count);
  * their waits for rk_stream_timeouts.  Process-wide.  Returns an rk_status. */
 int rk_debug_force_wait_timeout(int64_t polls);
 
-/* Test hook: the next `count` reduction or scan calls that pass validation
+/* Test hook: the next `count` reduction, scan or serving calls that pass validation
  * return RK_ERR_HIP where they would launch their first kernel, and launch
  * nothing (out and workspace untouched), as after a launch the runtime
  * rejected.  Process-wide; 0 switches it off.  Returns an rk_status. */

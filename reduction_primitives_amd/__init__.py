@@ -6,6 +6,9 @@ Python face of librk.so.  ``rk_reduce_all``, ``rk_reduce_all2``, ``rk_reduce_dim
 tensors into those calls (``reduce_all2`` for a two-input source) -- pick dtype codes, allocate the output and the
 workspace with torch, pass the current HIP stream.  All arithmetic happens
 in the library's kernels; there is no fallback path.
+
+``softmax``, ``draft_verify``, ``block_tables`` and ``slot_map`` (serving.py,
+loaded at their first use) are the serving operators' face in the same way.
 """
 from __future__ import annotations
 
@@ -18,16 +21,17 @@ from ._native import (  # noqa: F401
     RK_ERR_UNSUPPORTED, RK_F16, RK_F32, RK_F64, RK_I32, RK_I64, RK_KERNEL_ALL,
     RK_KERNEL_ALL2, RK_KERNEL_ALL_STRIDED, RK_KERNEL_COLUMNS, RK_KERNEL_GENERIC, RK_KERNEL_NONE,
     RK_KERNEL_ROW, RK_KERNEL_SCAN_COLUMNS, RK_KERNEL_SCAN_LINES, RK_KERNEL_SCAN_ROWWAVE, RK_KERNEL_SCAN_TILE,
-    RK_KERNEL_SCAN_TRANSPOSE, RK_KERNEL_THREAD,
+    RK_KERNEL_DRAFT_VERIFY, RK_KERNEL_SCAN_TRANSPOSE, RK_KERNEL_SOFTMAX_SPLIT, RK_KERNEL_THREAD,
     RK_KERNEL_TILED, RK_MAP2_ABSDIFF, RK_MAP2_MUL, RK_MAP2_SQDIFF,
     RK_MAP_ABS, RK_MAP_IDENTITY, RK_MAP_SQUARE,
     RK_MODE_FOLD, RK_MODE_HOST, RK_MODE_OVERWRITE, RK_OK, RK_OP_MAX, RK_OP_MIN, RK_OP_SUM,
-    RkError, load, rk_debug_device_info, rk_debug_fail_launches, rk_debug_force_wait_timeout,
+    RkError, load, rk_block_tables, rk_block_tables_workspace_size, rk_debug_device_info, rk_debug_fail_launches, rk_debug_force_wait_timeout,
     rk_debug_set_finish_tag, rk_debug_set_fused_finish, rk_debug_set_launch_events, rk_stream_timeouts,
-    rk_debug_stream_read, rk_plan_all, rk_plan_all2, rk_plan_dims,
-    rk_plan_info, rk_plan_scan, rk_reduce_all, rk_reduce_all2, rk_reduce_dims, rk_reduce_dims_no_workspace,
+    rk_debug_stream_read, rk_draft_verify, rk_draft_verify_workspace_size, rk_plan_all, rk_plan_all2, rk_plan_dims,
+    rk_plan_draft_verify,
+    rk_plan_info, rk_plan_scan, rk_plan_softmax, rk_reduce_all, rk_reduce_all2, rk_reduce_dims, rk_reduce_dims_no_workspace,
     rk_scan, rk_scan_dims,
-    rk_scan_workspace_size, rk_workspace_size, status_string)
+    rk_scan_workspace_size, rk_slot_map, rk_softmax, rk_softmax_workspace_size, rk_workspace_size, status_string)
 
 OPS = {"sum": RK_OP_SUM, "max": RK_OP_MAX, "min": RK_OP_MIN}
 MAPS = {"identity": RK_MAP_IDENTITY, "square": RK_MAP_SQUARE, "abs": RK_MAP_ABS}
@@ -294,3 +298,16 @@ def plan_dims(dtype, shape, strides, dims, acc=None, ptr=0, num_cus=0) -> dict:
     d = {f: getattr(info, f) for f, _ in rk_plan_info._fields_}
     d["kernel_name"] = KERNEL_NAMES[info.kernel]
     return d
+
+
+_SERVING = ("softmax", "draft_verify", "block_tables", "slot_map")
+
+
+def __getattr__(name):
+    # the serving operators' module needs torch when it loads; this package
+    # does not (the C ABI's bindings and plans work without a device)
+    if name in _SERVING:
+        from . import serving
+        globals().update({n: getattr(serving, n) for n in _SERVING})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -21,10 +21,12 @@ RK_F32, RK_BF16, RK_F16, RK_F64, RK_I32, RK_I64 = 0, 1, 2, 3, 4, 5
 RK_MODE_OVERWRITE, RK_MODE_FOLD, RK_MODE_HOST = 0, 1, 2
 (RK_KERNEL_NONE, RK_KERNEL_ALL, RK_KERNEL_ALL_STRIDED, RK_KERNEL_THREAD, RK_KERNEL_TILED,
  RK_KERNEL_COLUMNS, RK_KERNEL_ROW, RK_KERNEL_GENERIC, RK_KERNEL_ALL2, RK_KERNEL_SCAN_TILE,
- RK_KERNEL_SCAN_ROWWAVE, RK_KERNEL_SCAN_LINES, RK_KERNEL_SCAN_COLUMNS, RK_KERNEL_SCAN_TRANSPOSE) = range(14)
+ RK_KERNEL_SCAN_ROWWAVE, RK_KERNEL_SCAN_LINES, RK_KERNEL_SCAN_COLUMNS, RK_KERNEL_SCAN_TRANSPOSE,
+ RK_KERNEL_SOFTMAX_SPLIT, RK_KERNEL_DRAFT_VERIFY) = range(16)
 KERNEL_NAMES = {0: "none", 1: "all", 2: "all_strided", 3: "thread", 4: "tiled", 5: "columns",
                 6: "row", 7: "generic", 8: "all2", 9: "scan_tile", 10: "scan_rowwave",
-                11: "scan_lines", 12: "scan_columns", 13: "scan_transpose"}
+                11: "scan_lines", 12: "scan_columns", 13: "scan_transpose",
+                14: "softmax_split", 15: "draft_verify"}
 
 # every function include/rk.h declares
 EXPORTS = ("rk_workspace_size", "rk_reduce_all", "rk_reduce_all2", "rk_reduce_dims", "rk_status_string",
@@ -32,7 +34,10 @@ EXPORTS = ("rk_workspace_size", "rk_reduce_all", "rk_reduce_all2", "rk_reduce_di
            "rk_debug_set_launch_events", "rk_scan_workspace_size", "rk_scan", "rk_scan_dims",
            "rk_plan_scan", "rk_debug_stream_read", "rk_debug_device_info", "rk_debug_set_finish_tag",
            "rk_stream_timeouts", "rk_debug_force_wait_timeout", "rk_debug_fail_launches",
-           "rk_reduce_dims_no_workspace")
+           "rk_reduce_dims_no_workspace",
+           "rk_softmax_workspace_size", "rk_softmax", "rk_draft_verify_workspace_size", "rk_draft_verify",
+           "rk_block_tables_workspace_size", "rk_block_tables", "rk_slot_map",
+           "rk_plan_softmax", "rk_plan_draft_verify")
 
 
 class rk_plan_info(ctypes.Structure):
@@ -109,6 +114,24 @@ def load() -> ctypes.CDLL:
     lib.rk_debug_force_wait_timeout.restype = i32
     lib.rk_debug_fail_launches.argtypes = [i32]
     lib.rk_debug_fail_launches.restype = i32
+    lib.rk_softmax_workspace_size.argtypes = [i32, i32, i64, i64]
+    lib.rk_softmax_workspace_size.restype = sz
+    lib.rk_softmax.argtypes = [i32, i32, vp, i64, i64, i64, vp, vp, i64, vp, sz, vp]
+    lib.rk_softmax.restype = i32
+    lib.rk_draft_verify_workspace_size.argtypes = [i32, i64, i64]
+    lib.rk_draft_verify_workspace_size.restype = sz
+    lib.rk_draft_verify.argtypes = [i32, i32, vp, i64, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.rk_draft_verify.restype = i32
+    lib.rk_block_tables_workspace_size.argtypes = [i64]
+    lib.rk_block_tables_workspace_size.restype = sz
+    lib.rk_block_tables.argtypes = [vp, i64, i32, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp, sz, vp]
+    lib.rk_block_tables.restype = i32
+    lib.rk_slot_map.argtypes = [vp, vp, i64, i32, vp, i64, i32, vp, i64, i32, i64, vp, vp, vp, vp, vp]
+    lib.rk_slot_map.restype = i32
+    lib.rk_plan_softmax.argtypes = [i32, i32, i64, i64, i32, ctypes.POINTER(rk_plan_info)]
+    lib.rk_plan_softmax.restype = i32
+    lib.rk_plan_draft_verify.argtypes = [i32, i64, i64, i32, ctypes.POINTER(rk_plan_info)]
+    lib.rk_plan_draft_verify.restype = i32
     _lib = lib
     return lib
 
@@ -202,6 +225,59 @@ def rk_plan_scan(in_dtype, acc_dtype, out_dtype, ptr, out, ndim, shape, strides,
                              _i64_array(strides), dim, num_cus, ctypes.byref(info))
     if rc:
         raise RkError(rc, "rk_plan_scan")
+    return info
+
+
+def rk_softmax_workspace_size(in_dtype, out_dtype, n, lines) -> int:
+    return int(load().rk_softmax_workspace_size(in_dtype, out_dtype, n, lines))
+
+
+def rk_softmax(in_dtype, out_dtype, x, n, lines, x_stride, temperature, out, out_stride, workspace,
+               workspace_bytes, stream) -> int:
+    return load().rk_softmax(in_dtype, out_dtype, x, n, lines, x_stride, temperature, out, out_stride, workspace,
+                             workspace_bytes, stream)
+
+
+def rk_draft_verify_workspace_size(prob_dtype, vocab, n_req) -> int:
+    return int(load().rk_draft_verify_workspace_size(prob_dtype, vocab, n_req))
+
+
+def rk_draft_verify(prob_dtype, token_dtype, p, p_stride, q, q_stride, vocab, n_req, n_draft, max_draft, starts,
+                    drafted, u, r, tokens, accepted, workspace, workspace_bytes, stream) -> int:
+    return load().rk_draft_verify(prob_dtype, token_dtype, p, p_stride, q, q_stride, vocab, n_req, n_draft,
+                                  max_draft, starts, drafted, u, r, tokens, accepted, workspace, workspace_bytes,
+                                  stream)
+
+
+def rk_block_tables_workspace_size(n_req) -> int:
+    return int(load().rk_block_tables_workspace_size(n_req))
+
+
+def rk_block_tables(lens, n_req, block_size, held, held_out, table, table_stride, max_blocks, ring, ring_size,
+                    state, state_out, workspace, workspace_bytes, stream) -> int:
+    return load().rk_block_tables(lens, n_req, block_size, held, held_out, table, table_stride, max_blocks, ring,
+                                  ring_size, state, state_out, workspace, workspace_bytes, stream)
+
+
+def rk_slot_map(lens, fresh, n_req, block_size, table, table_stride, max_blocks, held, n_blocks, slot_dtype,
+                capacity, slots, positions, requests, starts, stream) -> int:
+    return load().rk_slot_map(lens, fresh, n_req, block_size, table, table_stride, max_blocks, held, n_blocks,
+                              slot_dtype, capacity, slots, positions, requests, starts, stream)
+
+
+def rk_plan_softmax(in_dtype, out_dtype, n, lines, num_cus=0) -> rk_plan_info:
+    info = rk_plan_info()
+    rc = load().rk_plan_softmax(in_dtype, out_dtype, n, lines, num_cus, ctypes.byref(info))
+    if rc:
+        raise RkError(rc, "rk_plan_softmax")
+    return info
+
+
+def rk_plan_draft_verify(prob_dtype, vocab, n_req, num_cus=0) -> rk_plan_info:
+    info = rk_plan_info()
+    rc = load().rk_plan_draft_verify(prob_dtype, vocab, n_req, num_cus, ctypes.byref(info))
+    if rc:
+        raise RkError(rc, "rk_plan_draft_verify")
     return info
 
 

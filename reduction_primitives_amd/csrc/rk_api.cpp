@@ -22,6 +22,7 @@
 #include <cstring>
 #include <limits>
 
+#include "rk_host.hpp"
 #include "rk_launch.hpp"
 #include "rk_plan.hpp"
 #include "rk_scan_plan.hpp"
@@ -1074,3 +1075,20 @@ int rk_scan(int op, int in_dtype, int acc_dtype, int out_dtype, const void *ptr,
 }
 
 }  // extern "C"
+
+namespace rk {
+namespace host {
+
+int device_cus() { return ::device_cus(); }
+int stream_slot(void *stream) { return arrive_slot(static_cast<hipStream_t>(stream)); }
+bool fused_finish() { return g_fused_finish.load(std::memory_order_relaxed); }
+bool injected_launch_failure() { return ::injected_launch_failure(); }
+bool debug_enabled() { return ::debug_enabled(); }
+void launch_events(void **begin, void **end)
+{
+    *begin = t_ev_begin;
+    *end = t_ev_end;
+}
+
+}  // namespace host
+}  // namespace rk

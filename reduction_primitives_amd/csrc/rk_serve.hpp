@@ -1,0 +1,164 @@
+// rk_serve.hpp -- plans and kernel arguments of the serving operators: softmax
+// of lines, verification of drafted tokens, block tables and slot maps.  Pure
+// C++ (no HIP), like rk_plan.hpp.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "rk_plan.hpp"
+
+namespace rk {
+namespace tune {
+// ---- softmax of lines
+constexpr int kSoftBlock = 256;           // threads of a split line's blocks
+constexpr int kSoftChunk = 8192;          // elements of one block of a split line
+// ---- draft verification
+constexpr int kVerifyBlock = 256;
+constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums
+// ---- block tables and slot maps
+constexpr int kScanBlock = 1024;          // threads of the one block that scans the requests
+constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
+constexpr int kSlotBlock = 256;
+constexpr int kSlotTokens = 4;            // consecutive tokens of one thread
+constexpr int kSlotLdsRequests = 8192;    // requests whose offsets a block keeps in LDS
+}  // namespace tune
+
+enum ServeKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2, VK_VERIFY = 3 };
+
+// ------------------------------------------------------------------ softmax
+
+struct SoftmaxPlan {
+    int kernel = VK_NONE;
+    int64_t grid = 0;         // blocks of the first launch
+    int block = 0;
+    int launches = 0;
+    int chunks = 1;           // blocks sharing a line
+    int64_t chunk = 0;        // elements of a chunk
+    int vec = 1;
+    size_t ws_bytes = 0;
+};
+
+struct SoftmaxArgs {
+    const void *x;
+    void *out;
+    const float *t;           // temperatures, or NULL (1)
+    float *stats;             // split: max, sum of every chunk of every line
+    int32_t *first;           // split: index of the first largest entry of every chunk
+    int64_t n, lines, xs, os;
+    int chunks;
+    int64_t chunk;
+};
+
+int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int cus, SoftmaxPlan *p);
+
+struct SoftmaxLaunch {
+    SoftmaxPlan plan;
+    SoftmaxArgs a;
+    int in, out;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_softmax(const SoftmaxLaunch &L);
+
+// ------------------------------------------------------- draft verification
+
+struct VerifyPlan {
+    int64_t tiles = 0;        // tiles of a line
+    int chunks = 0;           // blocks of a line
+    int64_t grid = 0;
+    int launches = 0;
+    bool fused_ok = false;    // the arrival counters of all requests fit a slot
+    size_t ws_bytes = 0;
+};
+
+struct VerifyArgs {
+    const void *p, *q;        // q NULL: drafts without probabilities
+    int64_t ps, qs;           // line strides
+    int64_t n;                // vocabulary
+    int64_t req, drafts;      // requests; drafted tokens of all requests
+    int max_draft;
+    const int32_t *starts;    // NULL: max_draft drafts for every request
+    const void *drafted;
+    const float *u, *r;
+    void *tokens;
+    int32_t *accepted;
+    double *sums;             // [req][tiles]
+    int64_t tiles;
+    int chunks;
+    int slot;                 // >= 0: the last block of a request finishes it
+};
+
+int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p);
+
+struct VerifyLaunch {
+    VerifyPlan plan;
+    VerifyArgs a;
+    int dtype, token_dtype;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_verify(const VerifyLaunch &L);
+
+// -------------------------------------------------- block tables, slot maps
+
+// Division of 0 <= x < 2^31 by d >= 1 as a multiplication: with l the bits
+// of d - 1 and m = floor(2^(31+l) / d) + 1, x / d = (x * m) >> (31 + l).
+// (m d exceeds 2^(31+l) by e with 1 <= e <= d <= 2^l, so x e < 2^(31+l), and
+// m < 2^32 since 2^(l-1) < d for d > 1, so the product fits 64 bits.)
+struct Divider {
+    uint32_t d;
+    uint32_t m;               // d = 1: unused, shift 0
+    int shift;
+};
+Divider make_divider(uint32_t d);
+
+struct TablesArgs {
+    const int32_t *lens, *held;
+    int32_t *held_out;
+    int64_t req;
+    Divider block;
+    int32_t *table;
+    int64_t ts;               // table stride
+    int max_blocks;
+    int32_t *ring;
+    int64_t ring_size;
+    const int64_t *state;
+    int64_t *state_out;
+    int64_t *offsets;         // the workspace, laid out as below
+};
+// Workspace of a block_tables call: four 64-bit words (blocks taken, blocks
+// given back, blocks that were free, ring place of the first free one), then
+// for every request and for the end a pair (blocks given back, blocks wanted
+// by the requests before it), then the blocks every request held.
+constexpr int64_t kTablesHeader = 4;
+constexpr int64_t tables_ws_bytes(int64_t req) { return (kTablesHeader + 2 * (req + 1)) * 8 + 4 * req; }
+
+struct TablesLaunch {
+    TablesArgs a;
+    int64_t grid;             // blocks of the second launch
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_tables(const TablesLaunch &L);
+
+struct SlotArgs {
+    const int32_t *lens, *fresh;
+    int64_t req;
+    Divider block;
+    const int32_t *table;
+    int64_t ts;
+    int max_blocks;
+    const int32_t *held;
+    int64_t n_blocks;
+    int64_t capacity;
+    void *slots;
+    int32_t *positions, *requests, *starts;
+    int64_t per_block;        // tokens of a block
+};
+struct SlotLaunch {
+    SlotArgs a;
+    int slot_dtype;
+    int64_t grid;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_slots(const SlotLaunch &L);
+
+}  // namespace rk

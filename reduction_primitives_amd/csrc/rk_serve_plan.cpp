@@ -1,0 +1,73 @@
+// rk_serve_plan.cpp -- launch plans of the serving operators (pure C++).
+#include "rk_serve.hpp"
+
+namespace rk {
+
+size_t round_up_256(size_t b);
+
+namespace {
+
+bool prob_dtype_ok(int d) { return d == F32 || d == BF16 || d == F16; }
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxLine = 0x7fffffff;
+
+}  // namespace
+
+int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int, SoftmaxPlan *p)
+{
+    *p = SoftmaxPlan();
+    if (!dtype_known(in_dtype) || !dtype_known(out_dtype) || n < 0 || lines < 0)
+        return ST_INVALID;
+    if (!prob_dtype_ok(in_dtype) || !prob_dtype_ok(out_dtype))
+        return ST_UNSUPPORTED;
+    if (n > kMaxLine || lines > kMaxGrid)
+        return ST_UNSUPPORTED;
+    p->vec = 16 / dtype_size(in_dtype);
+    if (n == 0 || lines == 0)
+        return ST_OK;
+    p->kernel = VK_SOFT_SPLIT;
+    p->block = tune::kSoftBlock;
+    p->chunk = tune::kSoftChunk;
+    p->chunks = int((n + p->chunk - 1) / p->chunk);
+    p->grid = lines * p->chunks;
+    p->launches = 2;
+    if (p->grid > kMaxGrid)
+        return ST_UNSUPPORTED;
+    p->ws_bytes = round_up_256(size_t(p->grid) * 12);
+    return ST_OK;
+}
+
+int plan_verify(int prob_dtype, int64_t n, int64_t req, int, VerifyPlan *p)
+{
+    *p = VerifyPlan();
+    if (!dtype_known(prob_dtype) || n < 1 || req < 0)
+        return ST_INVALID;
+    if (!prob_dtype_ok(prob_dtype) || n > kMaxLine || req > kMaxGrid)
+        return ST_UNSUPPORTED;
+    constexpr int waves = tune::kVerifyBlock / 64;
+    p->tiles = (n + tune::kVerifyTile - 1) / tune::kVerifyTile;
+    p->chunks = int((p->tiles + waves - 1) / waves);
+    p->grid = req * p->chunks;
+    if (p->grid > kMaxGrid)
+        return ST_UNSUPPORTED;
+    p->fused_ok = req * arrive_counters(p->chunks) <= kArriveCapacity;
+    p->launches = req == 0 ? 0 : p->chunks == 1 || p->fused_ok ? 1 : 2;
+    p->ws_bytes = round_up_256(size_t(req) * size_t(p->tiles) * 8);
+    return ST_OK;
+}
+
+Divider make_divider(uint32_t d)
+{
+    Divider r{d, 0, 0};
+    if (d > 1) {
+        int l = 0;
+        while ((uint64_t(1) << l) < d)
+            ++l;
+        r.shift = 31 + l;
+        r.m = uint32_t((uint64_t(1) << r.shift) / d + 1);
+    }
+    return r;
+}
+
+}  // namespace rk

@@ -1,0 +1,333 @@
+// serve_verify.hip -- verification of drafted tokens against the target's
+// probabilities, from given random numbers.
+//
+// Request b keeps its drafted tokens x_0, x_1, ... while
+//     u_i q_i(x_i) < p_i(x_i)
+// (the product of two float32 values is exact in float64, so the comparison
+// is).  At the first one turned down, i, the next token is drawn from
+//     w_j = max(p_i(j) - q_i(j), 0),
+// after the last one from w = p: the first j whose running sum passes
+// r sum(w).  Running sums are float64: a border between two tokens then moves
+// by 2^-52 of the whole sum with the order of the additions, not by the 2^-23
+// that would change drawn tokens.
+//
+// Only one target line per request, and one draft line where a token is
+// turned down, is read.  Every block of a request finds the kept tokens by
+// itself (a few dependent loads, all drafts at once), sums its tiles of the
+// line, a tile a wave, and the request's last block finds the tile in which
+// the running sum passes and goes through that tile alone.
+#define RK_UNIT unit_serve_verify
+#include "rk_serve_device.hpp"
+
+namespace rk {
+namespace {
+
+constexpr int kB = tune::kVerifyBlock;
+constexpr int kTile = tune::kVerifyTile;
+
+// Probabilities that are not positive finite numbers weigh nothing.
+__device__ __forceinline__ double weight(double w)
+{
+    return w > 0.0 && w < __builtin_inf() ? w : 0.0;
+}
+
+template <class Tok>
+__device__ __forceinline__ int64_t token_at(const void *p, int64_t i)
+{
+    return static_cast<const Tok *>(p)[i];
+}
+
+// What the whole block knows of its request.
+struct Drawn {
+    int64_t lo;               // its first draft
+    int count, kept;          // its drafts, and how many are kept
+    int64_t x;                // the token turned down (-1: none)
+};
+
+template <class In, class Tok>
+__device__ __forceinline__ Drawn accept(const VerifyArgs &a, int64_t b)
+{
+    using S = typename InTraits<In>::S;
+    Drawn d;
+    int64_t lo = b * a.max_draft, hi = lo + a.max_draft;
+    if (a.starts) {
+        lo = a.starts[b];
+        hi = a.starts[b + 1];
+        lo = lo < 0 ? 0 : lo > a.drafts ? a.drafts : lo;
+        hi = hi < lo ? lo : hi > a.drafts ? a.drafts : hi;
+        hi = hi - lo > a.max_draft ? lo + a.max_draft : hi;
+    }
+    d.lo = lo;
+    d.count = int(hi - lo);
+    d.kept = d.count;
+    d.x = -1;
+    for (int base = 0; base < d.count; base += 64) {
+        const int i = base + lane_id();
+        bool turned = false;
+        int64_t x = -1;
+        if (i < d.count) {
+            x = token_at<Tok>(a.drafted, lo + i);
+            turned = true;
+            if (x >= 0 && x < a.n) {
+                const double p = weight(InTraits<In>::template one<double>(
+                    static_cast<const S *>(a.p)[(lo + i + b) * a.ps + x]));
+                const double q = a.q ? InTraits<In>::template one<double>(static_cast<const S *>(a.q)[(lo + i) * a.qs + x])
+                                     : 1.0;
+                turned = !(double(a.u[lo + i]) * q < p);
+            }
+        }
+        const uint64_t m = __ballot(turned);
+        if (m) {
+            const int at = __builtin_ctzll(m);
+            d.kept = base + at;
+            d.x = read_lane(x, at);
+            break;
+        }
+    }
+    return d;
+}
+
+// The lines of the request's next token: target line p, draft line q (NULL:
+// nothing to subtract), and the one token whose weight loses 1 (-1: none).
+template <class S> struct Lines {
+    const S *p, *q;
+    int64_t x;
+};
+
+template <class S>
+__device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, const Drawn &d)
+{
+    Lines<S> l;
+    l.p = static_cast<const S *>(a.p) + (d.lo + d.kept + b) * a.ps;
+    const bool turned = d.kept < d.count;
+    l.q = turned && a.q ? static_cast<const S *>(a.q) + (d.lo + d.kept) * a.qs : nullptr;
+    l.x = turned && !a.q ? d.x : -1;
+    return l;
+}
+
+// Weight of entry i.
+template <class In, class S>
+__device__ __forceinline__ double weight_at(const Lines<S> &l, int64_t i)
+{
+    double w = InTraits<In>::template one<double>(l.p[i]);
+    if (l.q)
+        w -= InTraits<In>::template one<double>(l.q[i]);
+    else if (i == l.x)
+        w -= 1.0;
+    return weight(w);
+}
+
+// Sum of one tile's weights, in every lane of the wave.
+template <class In, class S>
+__device__ __forceinline__ double tile_sum(const Lines<S> &l, int64_t n, int64_t tile)
+{
+    constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
+    const int64_t base = tile * kTile;
+    double s = 0.0;
+    if (base + kTile <= n && !(l.x >= base && l.x < base + kTile)) {
+        u32x4 p[U], q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            p[u] = load16(l.p + base + (u * 64 + lane_id()) * V);
+        if (l.q) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                q[u] = load16(l.q + base + (u * 64 + lane_id()) * V);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                double e[V], f[V];
+                InTraits<In>::decode(p[u], e);
+                InTraits<In>::decode(q[u], f);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    s += weight(e[k] - f[k]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                double e[V];
+                InTraits<In>::decode(p[u], e);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    s += weight(e[k]);
+            }
+        }
+    } else {
+        const int64_t end = base + kTile < n ? base + kTile : n;
+        for (int64_t i = base + lane_id(); i < end; i += 64)
+            s += weight_at<In>(l, i);
+    }
+    return wave_reduce<OpSum>(s);
+}
+
+// The first index whose running sum passes r * (whole sum), -1 where nothing
+// weighs anything.  Called by the whole block, with the tiles' sums in `sums`.
+template <class In, class S>
+__device__ int64_t find(const Lines<S> &l, int64_t n, const double *sums, int64_t tiles, double r)
+{
+    constexpr int per = kTile / kB;
+    constexpr int none = 0x7fffffff;
+    __shared__ double part[2][kB / 64];
+    __shared__ double s_before;
+    __shared__ int s_tile, s_last, s_at, s_pos;
+    __syncthreads();                          // a second call's uses come after the first's
+    if (threadIdx.x == 0) {
+        s_tile = s_at = none;
+        s_last = s_pos = -1;
+    }
+    // the whole sum, in the order of the running one
+    double whole = 0.0, v = 0.0, before = 0.0, sum;
+    int turn = 0;
+    for (int64_t base = 0; base < tiles; base += kB, turn ^= 1) {
+        const int64_t i = base + threadIdx.x;
+        v = i < tiles ? load_partial(sums + i) : 0.0;
+        before = whole + block_prefix<kB>(v, part[turn], &sum);
+        whole += sum;
+    }
+    if (!(whole > 0.0))
+        return -1;
+    const double bar = r * whole;
+    // the tile in which it passes
+    double upto = 0.0;
+    int tile = none;
+    for (int64_t base = 0; base < tiles && tile == none; base += kB, turn ^= 1) {
+        const int i = int(base) + int(threadIdx.x);
+        if (tiles > kB) {                     // (otherwise the one round above has left v and before)
+            v = i < tiles ? load_partial(sums + i) : 0.0;
+            before = upto + block_prefix<kB>(v, part[turn], &sum);
+            upto += sum;
+        }
+        if (v > 0.0) {
+            atomicMax(&s_last, i);
+            if (before + v > bar)
+                atomicMin(&s_tile, i);
+        }
+        __syncthreads();
+        tile = s_tile;
+        if (tile == i)
+            s_before = before;
+    }
+    __syncthreads();
+    // none (r so near 1 that r * whole rounds to whole): the last entry that weighs something
+    const double start = tile == none ? -__builtin_inf() : s_before;
+    if (tile == none)
+        tile = s_last;
+    // the entry
+    const int64_t first = int64_t(tile) * kTile + int64_t(threadIdx.x) * per;
+    double w[per], mine = 0.0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        w[k] = first + k < n ? weight_at<In>(l, first + k) : 0.0;
+        mine += w[k];
+    }
+    double run = start + block_prefix<kB>(mine, part[turn], &sum);
+    int at = none, pos = -1;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        run += w[k];
+        if (w[k] > 0.0) {
+            pos = int(threadIdx.x) * per + k;
+            if (at == none && run > bar)
+                at = pos;
+        }
+    }
+    if (at != none)
+        atomicMin(&s_at, at);
+    if (pos >= 0)
+        atomicMax(&s_pos, pos);
+    __syncthreads();
+    return int64_t(tile) * kTile + (s_at != none ? s_at : s_pos);
+}
+
+template <class In, class S>
+__device__ __forceinline__ void sum_tiles(const VerifyArgs &a, int64_t b, const Lines<S> &l, int64_t from, int64_t step)
+{
+    for (int64_t tile = from + (threadIdx.x >> 6); tile < a.tiles; tile += step) {
+        const double s = tile_sum<In>(l, a.n, tile);
+        if (lane_id() == 0)
+            store_partial(a.sums + b * a.tiles + tile, s);
+    }
+    wait_stores();
+    __syncthreads();
+}
+
+// Draws the request's next token and writes its outputs.
+template <class In, class Tok>
+__device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Drawn &d)
+{
+    using S = typename InTraits<In>::S;
+    Lines<S> l = lines_of<S>(a, b, d);
+    double r = double(a.r[b]);
+    r = r > 0.0 ? (r < 1.0 ? r : 1.0) : 0.0;  // (NaN draws the first)
+    const double *sums = a.sums + b * a.tiles;
+    int64_t token = find<In>(l, a.n, sums, a.tiles, r);
+    if (token < 0 && (l.q || l.x >= 0)) {     // the draft leaves nothing of the target: draw from the target
+        l.q = nullptr;
+        l.x = -1;
+        sum_tiles<In>(a, b, l, 0, kB / 64);
+        token = find<In>(l, a.n, sums, a.tiles, r);
+    }
+    Tok *out = static_cast<Tok *>(a.tokens) + b * (int64_t(a.max_draft) + 1);
+    for (int i = int(threadIdx.x); i <= a.max_draft; i += kB)
+        out[i] = i < d.kept ? static_cast<const Tok *>(a.drafted)[d.lo + i] : i == d.kept ? Tok(token) : Tok(-1);
+    if (threadIdx.x == 0)
+        a.accepted[b] = d.kept;
+}
+
+template <class In, class Tok>
+__global__ __launch_bounds__(kB) void k_verify(VerifyArgs a)
+{
+    using S = typename InTraits<In>::S;
+    const int64_t b = blockIdx.x / uint32_t(a.chunks);
+    const int c = int(blockIdx.x % uint32_t(a.chunks));
+    const Drawn d = accept<In, Tok>(a, b);
+    const Lines<S> l = lines_of<S>(a, b, d);
+    sum_tiles<In>(a, b, l, int64_t(c) * (kB / 64), int64_t(a.chunks) * (kB / 64));
+    if (a.chunks > 1) {
+        if (a.slot < 0)
+            return;                           // the second launch finishes
+        __shared__ bool last;
+        if (threadIdx.x == 0)
+            last = arrive_last(a.slot, b, uint32_t(c), uint32_t(a.chunks));
+        __syncthreads();
+        if (!last)
+            return;
+    }
+    finish<In, Tok>(a, b, d);
+}
+
+template <class In, class Tok>
+__global__ __launch_bounds__(kB) void k_verify_finish(VerifyArgs a)
+{
+    const int64_t b = blockIdx.x;
+    finish<In, Tok>(a, b, accept<In, Tok>(a, b));
+}
+
+template <class In, class Tok>
+int run_verify(const VerifyLaunch &L)
+{
+    launch_timed(k_verify<In, Tok>, dim3(uint32_t(L.plan.grid)), dim3(kB), 0, L.stream, L.ev_begin, L.ev_end, L.a);
+    if (L.a.chunks > 1 && L.a.slot < 0)
+        launch_timed(k_verify_finish<In, Tok>, dim3(uint32_t(L.a.req)), dim3(kB), 0, L.stream, nullptr, nullptr, L.a);
+    return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
+}
+
+template <class In>
+int run_verify_in(const VerifyLaunch &L)
+{
+    return L.token_dtype == I64 ? run_verify<In, int64_t>(L) : run_verify<In, int32_t>(L);
+}
+
+}  // namespace
+
+int launch_verify(const VerifyLaunch &L)
+{
+    switch (L.dtype) {
+    case F32: return run_verify_in<float>(L);
+    case BF16: return run_verify_in<bf16_in>(L);
+    case F16: return run_verify_in<f16_in>(L);
+    }
+    return ST_UNSUPPORTED;
+}
+
+}  // namespace rk
