@@ -15,7 +15,8 @@ constexpr int kSoftBlock = 256;           // threads of a split line's blocks
 constexpr int kSoftChunk = 8192;          // elements of one block of a split line
 // ---- draft verification
 constexpr int kVerifyBlock = 256;
-constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums
+constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums at a time
+constexpr int kVerifyBlocksPerCu = 8;     // grid cap = CUs * this
 // ---- block tables and slot maps
 constexpr int kScanBlock = 1024;          // threads of the one block that scans the requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids

@@ -38,7 +38,7 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int, Sof
     return ST_OK;
 }
 
-int plan_verify(int prob_dtype, int64_t n, int64_t req, int, VerifyPlan *p)
+int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
 {
     *p = VerifyPlan();
     if (!dtype_known(prob_dtype) || n < 1 || req < 0)
@@ -47,7 +47,11 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int, VerifyPlan *p)
         return ST_UNSUPPORTED;
     constexpr int waves = tune::kVerifyBlock / 64;
     p->tiles = (n + tune::kVerifyTile - 1) / tune::kVerifyTile;
-    p->chunks = int((p->tiles + waves - 1) / waves);
+    // a wave a tile while the blocks fit the chip at once; beyond that, more tiles a wave
+    const int64_t most = int64_t(cus > 0 ? cus : tune::kDefaultCus) * tune::kVerifyBlocksPerCu;
+    int64_t chunks = (p->tiles + waves - 1) / waves, fit = req > 0 ? most / req : chunks;
+    fit = fit < 1 ? 1 : fit;
+    p->chunks = int(chunks < fit ? chunks : fit);
     p->grid = req * p->chunks;
     if (p->grid > kMaxGrid)
         return ST_UNSUPPORTED;

@@ -105,59 +105,91 @@ __device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, con
     return l;
 }
 
-// Weight of entry i.
+// Weights of V consecutive entries from i on, one vector load a line.  Entries
+// from n on weigh nothing: a vector that would pass the line's end is read
+// from n - V instead and its first entries, which belong to others, dropped.
+// EXACT: drop infinities too, and take 1 from entry l.x (the callers say when
+// neither can be there).  TAIL: the vectors may pass the line's end.
+template <class In, bool EXACT, bool TAIL, class S>
+struct Loaded {
+    static constexpr int V = InTraits<In>::vec;
+    u32x4 p, q;
+    int64_t at;               // index of the vector's first entry
+
+    __device__ __forceinline__ void load(const Lines<S> &l, int64_t i, int64_t n)
+    {
+        at = !TAIL || i + V <= n ? i : n - V;
+        p = load16(l.p + at);
+        if (l.q)
+            q = load16(l.q + at);
+    }
+
+    __device__ __forceinline__ void weights(const Lines<S> &l, int64_t i, double *w) const
+    {
+        InTraits<In>::decode(p, w);
+        if (l.q) {
+            double f[V];
+            InTraits<In>::decode(q, f);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                w[k] -= f[k];
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if constexpr (EXACT)
+                w[k] = weight(at + k == l.x ? w[k] - 1.0 : w[k]);
+            else
+                w[k] = __builtin_fmax(w[k], 0.0);          // (NaN: 0)
+            if constexpr (TAIL)
+                if (at + k < i)
+                    w[k] = 0.0;
+        }
+    }
+};
+
+// Lines shorter than a vector.
 template <class In, class S>
 __device__ __forceinline__ double weight_at(const Lines<S> &l, int64_t i)
 {
     double w = InTraits<In>::template one<double>(l.p[i]);
     if (l.q)
         w -= InTraits<In>::template one<double>(l.q[i]);
-    else if (i == l.x)
-        w -= 1.0;
-    return weight(w);
+    return weight(i == l.x ? w - 1.0 : w);
 }
 
 // Sum of one tile's weights, in every lane of the wave.
+template <class In, bool EXACT, bool TAIL, class S>
+__device__ __forceinline__ double sum_of(const Lines<S> &l, int64_t n, int64_t base)
+{
+    constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
+    Loaded<In, EXACT, TAIL, S> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        v[u].load(l, base + (u * 64 + lane_id()) * V, n);
+    double s = 0.0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        double w[V];
+        v[u].weights(l, base + (u * 64 + lane_id()) * V, w);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            s += w[k];
+    }
+    return wave_reduce<OpSum>(s);
+}
+
 template <class In, class S>
 __device__ __forceinline__ double tile_sum(const Lines<S> &l, int64_t n, int64_t tile)
 {
-    constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
     const int64_t base = tile * kTile;
-    double s = 0.0;
-    if (base + kTile <= n && !(l.x >= base && l.x < base + kTile)) {
-        u32x4 p[U], q[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            p[u] = load16(l.p + base + (u * 64 + lane_id()) * V);
-        if (l.q) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                q[u] = load16(l.q + base + (u * 64 + lane_id()) * V);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                double e[V], f[V];
-                InTraits<In>::decode(p[u], e);
-                InTraits<In>::decode(q[u], f);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    s += weight(e[k] - f[k]);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                double e[V];
-                InTraits<In>::decode(p[u], e);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    s += weight(e[k]);
-            }
-        }
-    } else {
-        const int64_t end = base + kTile < n ? base + kTile : n;
-        for (int64_t i = base + lane_id(); i < end; i += 64)
-            s += weight_at<In>(l, i);
+    if (n < InTraits<In>::vec)
+        return wave_reduce<OpSum>(lane_id() < n ? weight_at<In>(l, lane_id()) : 0.0);
+    if (!(l.x >= base && l.x < base + kTile)) {
+        const double s = base + kTile <= n ? sum_of<In, false, false>(l, n, base) : sum_of<In, false, true>(l, n, base);
+        if (s < __builtin_inf())
+            return s;
     }
-    return wave_reduce<OpSum>(s);
+    return sum_of<In, true, true>(l, n, base);
 }
 
 // The first index whose running sum passes r * (whole sum), -1 where nothing
@@ -214,19 +246,38 @@ __device__ int64_t find(const Lines<S> &l, int64_t n, const double *sums, int64_
         tile = s_last;
     // the entry
     const int64_t first = int64_t(tile) * kTile + int64_t(threadIdx.x) * per;
+    constexpr int V = InTraits<In>::vec;
+    static_assert(per % V == 0, "whole vectors a thread");
     double w[per], mine = 0.0;
+    int off[per / V];                         // place of each vector's first entry in the tile
+    if (n < V) {
 #pragma unroll
-    for (int k = 0; k < per; ++k) {
-        w[k] = first + k < n ? weight_at<In>(l, first + k) : 0.0;
-        mine += w[k];
+        for (int k = 0; k < per; ++k)
+            w[k] = first + k < n ? weight_at<In>(l, first + k) : 0.0;
+#pragma unroll
+        for (int u = 0; u < per / V; ++u)
+            off[u] = int(threadIdx.x) * per + u * V;
+    } else {
+        Loaded<In, true, true, S> v[per / V];
+#pragma unroll
+        for (int u = 0; u < per / V; ++u)
+            v[u].load(l, first + u * V, n);
+#pragma unroll
+        for (int u = 0; u < per / V; ++u) {
+            v[u].weights(l, first + u * V, w + u * V);
+            off[u] = int(v[u].at - int64_t(tile) * kTile);
+        }
     }
+#pragma unroll
+    for (int k = 0; k < per; ++k)
+        mine += w[k];
     double run = start + block_prefix<kB>(mine, part[turn], &sum);
     int at = none, pos = -1;
 #pragma unroll
     for (int k = 0; k < per; ++k) {
         run += w[k];
         if (w[k] > 0.0) {
-            pos = int(threadIdx.x) * per + k;
+            pos = off[k / V] + k % V;
             if (at == none && run > bar)
                 at = pos;
         }
