@@ -447,8 +447,9 @@ typedef enum {
                                    transposed or permuted view): tiles of lines x scan positions
                                    staged through LDS, look-back along the scan dim (+ a clearing
                                    launch) */
-    RK_KERNEL_SOFTMAX_SPLIT = 14, /* softmax: several blocks a line, statistics first, then the line */
-    RK_KERNEL_DRAFT_VERIFY = 15   /* draft verification: a wave per tile of a request's line */
+    RK_KERNEL_SOFTMAX_LINE = 14, /* softmax: a line in the registers of a wave or a block, one launch */
+    RK_KERNEL_SOFTMAX_SPLIT = 15, /* softmax: tiles of a line, statistics first, then the line (two launches) */
+    RK_KERNEL_DRAFT_VERIFY = 16   /* draft verification: a wave per tile of a request's line */
 } rk_kernel;
 
 typedef struct {
@@ -483,10 +484,10 @@ int rk_plan_scan(int in_dtype, int acc_dtype, int out_dtype, const void *ptr, co
                  const int64_t *shape, const int64_t *strides, int dim, int num_cus,
                  rk_plan_info *info);
 
-/* Plans of rk_softmax (split: blocks per line) and rk_draft_verify (split:
+/* Plans of rk_softmax (split: tiles per line) and rk_draft_verify (split:
  * blocks per request; tile_outputs: vocabulary entries a wave sums; launches as
  * outside a capture). */
-int rk_plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int num_cus, rk_plan_info *info);
+int rk_plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, rk_plan_info *info);
 int rk_plan_draft_verify(int prob_dtype, int64_t vocab, int64_t n_req, int num_cus, rk_plan_info *info);
 
 /* Whether a split reduction may finish inside its first launch (block 0

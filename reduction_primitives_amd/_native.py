@@ -22,11 +22,11 @@ RK_MODE_OVERWRITE, RK_MODE_FOLD, RK_MODE_HOST = 0, 1, 2
 (RK_KERNEL_NONE, RK_KERNEL_ALL, RK_KERNEL_ALL_STRIDED, RK_KERNEL_THREAD, RK_KERNEL_TILED,
  RK_KERNEL_COLUMNS, RK_KERNEL_ROW, RK_KERNEL_GENERIC, RK_KERNEL_ALL2, RK_KERNEL_SCAN_TILE,
  RK_KERNEL_SCAN_ROWWAVE, RK_KERNEL_SCAN_LINES, RK_KERNEL_SCAN_COLUMNS, RK_KERNEL_SCAN_TRANSPOSE,
- RK_KERNEL_SOFTMAX_SPLIT, RK_KERNEL_DRAFT_VERIFY) = range(16)
+ RK_KERNEL_SOFTMAX_LINE, RK_KERNEL_SOFTMAX_SPLIT, RK_KERNEL_DRAFT_VERIFY) = range(17)
 KERNEL_NAMES = {0: "none", 1: "all", 2: "all_strided", 3: "thread", 4: "tiled", 5: "columns",
                 6: "row", 7: "generic", 8: "all2", 9: "scan_tile", 10: "scan_rowwave",
                 11: "scan_lines", 12: "scan_columns", 13: "scan_transpose",
-                14: "softmax_split", 15: "draft_verify"}
+                14: "softmax_line", 15: "softmax_split", 16: "draft_verify"}
 
 # every function include/rk.h declares
 EXPORTS = ("rk_workspace_size", "rk_reduce_all", "rk_reduce_all2", "rk_reduce_dims", "rk_status_string",
@@ -128,7 +128,7 @@ def load() -> ctypes.CDLL:
     lib.rk_block_tables.restype = i32
     lib.rk_slot_map.argtypes = [vp, vp, i64, i32, vp, i64, i32, vp, i64, i32, i64, vp, vp, vp, vp, vp]
     lib.rk_slot_map.restype = i32
-    lib.rk_plan_softmax.argtypes = [i32, i32, i64, i64, i32, ctypes.POINTER(rk_plan_info)]
+    lib.rk_plan_softmax.argtypes = [i32, i32, i64, i64, ctypes.POINTER(rk_plan_info)]
     lib.rk_plan_softmax.restype = i32
     lib.rk_plan_draft_verify.argtypes = [i32, i64, i64, i32, ctypes.POINTER(rk_plan_info)]
     lib.rk_plan_draft_verify.restype = i32
@@ -265,9 +265,9 @@ def rk_slot_map(lens, fresh, n_req, block_size, table, table_stride, max_blocks,
                               slot_dtype, capacity, slots, positions, requests, starts, stream)
 
 
-def rk_plan_softmax(in_dtype, out_dtype, n, lines, num_cus=0) -> rk_plan_info:
+def rk_plan_softmax(in_dtype, out_dtype, n, lines) -> rk_plan_info:
     info = rk_plan_info()
-    rc = load().rk_plan_softmax(in_dtype, out_dtype, n, lines, num_cus, ctypes.byref(info))
+    rc = load().rk_plan_softmax(in_dtype, out_dtype, n, lines, ctypes.byref(info))
     if rc:
         raise RkError(rc, "rk_plan_softmax")
     return info

@@ -11,8 +11,15 @@
 namespace rk {
 namespace tune {
 // ---- softmax of lines
+constexpr int kSoftPer = 32;              // entries a thread holds of a line kept in registers
+constexpr int kSoftLanes = 512;           // most threads that share such a line
 constexpr int kSoftBlock = 256;           // threads of a split line's blocks
-constexpr int kSoftChunk = 8192;          // elements of one block of a split line
+constexpr int kSoftTile = 2048;           // entries of a wave's tile of a split line
+// Outputs beyond the eight L2s together (32 MB) are stored past the caches, so
+// the input stays there for its second reading: 320 x 131072 bf16 to f32 (168
+// MB out) 60.2 us with plain stores, 48.4 us with streaming ones.  Smaller
+// ones stay cached for whoever reads the probabilities next.
+constexpr int64_t kSoftStreamBytes = int64_t(32) << 20;
 // ---- draft verification
 constexpr int kVerifyBlock = 256;
 constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums at a time
@@ -27,6 +34,17 @@ constexpr int kSlotLdsRequests = 8192;    // requests whose offsets a block keep
 
 enum ServeKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2, VK_VERIFY = 3 };
 
+// Division of 0 <= x < 2^31 by d >= 1 as a multiplication: with l the bits
+// of d - 1 and m = floor(2^(31+l) / d) + 1, x / d = (x * m) >> (31 + l).
+// (m d exceeds 2^(31+l) by e with 1 <= e <= d <= 2^l, so x e < 2^(31+l), and
+// m < 2^32 since 2^(l-1) < d for d > 1, so the product fits 64 bits.)
+struct Divider {
+    uint32_t d;
+    uint32_t m;               // d = 1: unused, shift 0
+    int shift;
+};
+Divider make_divider(uint32_t d);
+
 // ------------------------------------------------------------------ softmax
 
 struct SoftmaxPlan {
@@ -34,9 +52,10 @@ struct SoftmaxPlan {
     int64_t grid = 0;         // blocks of the first launch
     int block = 0;
     int launches = 0;
-    int chunks = 1;           // blocks sharing a line
-    int64_t chunk = 0;        // elements of a chunk
+    int lanes = 0;            // threads sharing a line (VK_SOFT_LINE)
+    int chunks = 1;           // tiles of a line (VK_SOFT_SPLIT)
     int vec = 1;
+    bool stream_out = false;  // the writing launch stores past the caches (VK_SOFT_SPLIT)
     size_t ws_bytes = 0;
 };
 
@@ -44,14 +63,14 @@ struct SoftmaxArgs {
     const void *x;
     void *out;
     const float *t;           // temperatures, or NULL (1)
-    float *stats;             // split: max, sum of every chunk of every line
-    int32_t *first;           // split: index of the first largest entry of every chunk
+    float *stats;             // split: max, sum of every tile of every line
+    int32_t *first;           // split: place of the first largest entry in every tile
     int64_t n, lines, xs, os;
     int chunks;
-    int64_t chunk;
+    Divider per_line;         // split: blocks of a line
 };
 
-int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int cus, SoftmaxPlan *p);
+int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxPlan *p);
 
 struct SoftmaxLaunch {
     SoftmaxPlan plan;
@@ -100,17 +119,6 @@ struct VerifyLaunch {
 int launch_verify(const VerifyLaunch &L);
 
 // -------------------------------------------------- block tables, slot maps
-
-// Division of 0 <= x < 2^31 by d >= 1 as a multiplication: with l the bits
-// of d - 1 and m = floor(2^(31+l) / d) + 1, x / d = (x * m) >> (31 + l).
-// (m d exceeds 2^(31+l) by e with 1 <= e <= d <= 2^l, so x e < 2^(31+l), and
-// m < 2^32 since 2^(l-1) < d for d > 1, so the product fits 64 bits.)
-struct Divider {
-    uint32_t d;
-    uint32_t m;               // d = 1: unused, shift 0
-    int shift;
-};
-Divider make_divider(uint32_t d);
 
 struct TablesArgs {
     const int32_t *lens, *held;

@@ -53,25 +53,26 @@ extern "C" {
 size_t rk_softmax_workspace_size(int in_dtype, int out_dtype, int64_t n, int64_t lines)
 {
     SoftmaxPlan p;
-    return plan_softmax(in_dtype, out_dtype, n, lines, host::device_cus(), &p) == ST_OK ? p.ws_bytes : 0;
+    return plan_softmax(in_dtype, out_dtype, n, lines, &p) == ST_OK ? p.ws_bytes : 0;
 }
 
-int rk_plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int num_cus, rk_plan_info *info)
+int rk_plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, rk_plan_info *info)
 {
     if (!info)
         return RK_ERR_INVALID_ARGUMENT;
     SoftmaxPlan p;
-    const int rc = plan_softmax(in_dtype, out_dtype, n, lines, num_cus > 0 ? num_cus : host::device_cus(), &p);
+    const int rc = plan_softmax(in_dtype, out_dtype, n, lines, &p);
     if (rc)
         return rc;
     std::memset(info, 0, sizeof *info);
-    info->kernel = p.kernel == VK_SOFT_SPLIT ? RK_KERNEL_SOFTMAX_SPLIT : RK_KERNEL_NONE;
+    info->kernel = p.kernel == VK_SOFT_SPLIT ? RK_KERNEL_SOFTMAX_SPLIT
+                   : p.kernel == VK_SOFT_LINE ? RK_KERNEL_SOFTMAX_LINE : RK_KERNEL_NONE;
     info->launches = p.launches;
     info->grid = p.grid;
     info->block = p.block;
     info->split = p.chunks;
     info->vec = p.vec;
-    info->tile_outputs = int(p.chunk);
+    info->tile_outputs = p.kernel == VK_SOFT_SPLIT ? tune::kSoftTile : p.lanes * tune::kSoftPer;
     info->n_out = n * lines;
     info->reduce_len = n;
     info->workspace_bytes = p.ws_bytes;
@@ -83,7 +84,7 @@ int rk_softmax(int in_dtype, int out_dtype, const void *x, int64_t n, int64_t li
                void *stream)
 {
     SoftmaxPlan p;
-    int rc = plan_softmax(in_dtype, out_dtype, n, lines, host::device_cus(), &p);
+    int rc = plan_softmax(in_dtype, out_dtype, n, lines, &p);
     if (rc)
         return rc;
     if (!lines_fit(n, lines, x_stride) || !lines_fit(n, lines, out_stride) || (lines > 1 && out_stride < n))
@@ -121,13 +122,13 @@ int rk_softmax(int in_dtype, int out_dtype, const void *x, int64_t n, int64_t li
     L.a.out = out;
     L.a.t = temperature;
     L.a.stats = static_cast<float *>(workspace);
-    L.a.first = reinterpret_cast<int32_t *>(static_cast<float *>(workspace) + 2 * p.grid);
+    L.a.first = p.ws_bytes ? reinterpret_cast<int32_t *>(static_cast<float *>(workspace) + 2 * lines * p.chunks) : nullptr;
     L.a.n = n;
     L.a.lines = lines;
     L.a.xs = x_stride;
     L.a.os = out_stride;
     L.a.chunks = p.chunks;
-    L.a.chunk = p.chunk;
+    L.a.per_line = make_divider(uint32_t(p.kernel == VK_SOFT_SPLIT ? p.grid / lines : 1));
     L.in = in_dtype;
     L.out = out_dtype;
     L.stream = stream;

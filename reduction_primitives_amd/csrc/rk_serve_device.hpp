@@ -24,6 +24,11 @@ __device__ __forceinline__ void store16(void *p, u32x4 v)
     *static_cast<u32x4_any *>(p) = v;
 }
 
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
+{
+    return d.shift ? uint32_t((uint64_t(x) * d.m) >> d.shift) : x;
+}
+
 // Inclusive scan over the 64 lanes (all active).
 template <class T>
 __device__ __forceinline__ T wave_prefix(T v)

@@ -14,7 +14,7 @@ constexpr int64_t kMaxLine = 0x7fffffff;
 
 }  // namespace
 
-int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int, SoftmaxPlan *p)
+int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxPlan *p)
 {
     *p = SoftmaxPlan();
     if (!dtype_known(in_dtype) || !dtype_known(out_dtype) || n < 0 || lines < 0)
@@ -26,16 +26,26 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, int, Sof
     p->vec = 16 / dtype_size(in_dtype);
     if (n == 0 || lines == 0)
         return ST_OK;
-    p->kernel = VK_SOFT_SPLIT;
-    p->block = tune::kSoftBlock;
-    p->chunk = tune::kSoftChunk;
-    p->chunks = int((n + p->chunk - 1) / p->chunk);
-    p->grid = lines * p->chunks;
-    p->launches = 2;
-    if (p->grid > kMaxGrid)
-        return ST_UNSUPPORTED;
-    p->ws_bytes = round_up_256(size_t(p->grid) * 12);
-    return ST_OK;
+    p->launches = 1;
+    p->kernel = VK_SOFT_LINE;
+    if (n <= 64 * tune::kSoftPer) {
+        p->lanes = 64;
+        p->block = 256;
+        p->grid = (lines + 3) / 4;
+    } else if (n <= tune::kSoftLanes * tune::kSoftPer) {
+        p->lanes = p->block = n <= 256 * tune::kSoftPer ? 256 : tune::kSoftLanes;
+        p->grid = lines;
+    } else {
+        constexpr int waves = tune::kSoftBlock / 64;
+        p->kernel = VK_SOFT_SPLIT;
+        p->block = tune::kSoftBlock;
+        p->chunks = int((n + tune::kSoftTile - 1) / tune::kSoftTile);
+        p->grid = lines * ((p->chunks + waves - 1) / waves);
+        p->launches = 2;
+        p->stream_out = lines * n * dtype_size(out_dtype) > tune::kSoftStreamBytes;
+        p->ws_bytes = round_up_256(size_t(lines) * size_t(p->chunks) * 12);
+    }
+    return p->grid > kMaxGrid ? ST_UNSUPPORTED : ST_OK;
 }
 
 int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)

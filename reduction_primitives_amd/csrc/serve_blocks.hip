@@ -19,11 +19,6 @@
 namespace rk {
 namespace {
 
-__device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
-{
-    return d.shift ? uint32_t((uint64_t(x) * d.m) >> d.shift) : x;
-}
-
 __device__ __forceinline__ int blocks_of(int len, const Divider &d)
 {
     return len > 0 ? int(divide(uint32_t(len - 1), d)) + 1 : 0;

@@ -51,7 +51,7 @@ def check_softmax(got, x, t):
             assert np.array_equal(got64[i], want[i], equal_nan=True)
 
 
-SOFT_N = [1, 2, 7, 8, 63, 65, 257, 2047, 2048, 4099, 8191, 8192, 8193, 16384, 32768, 32769, 50001, 65537, 131072, 200003]
+SOFT_N = [1, 2, 7, 8, 63, 65, 257, 511, 2047, 2048, 2049, 4097, 8191, 8192, 8193, 16383, 16384, 16385, 32769, 50001, 65536, 65537, 131072, 200003]
 
 
 @pytest.mark.parametrize("n", SOFT_N)
@@ -104,7 +104,7 @@ def test_softmax_masks_and_odd_values(n, dt):
     assert got[9, 0] == 1
 
 
-@pytest.mark.parametrize("n", [77, 8200, 33333])
+@pytest.mark.parametrize("n", [77, 8200, 33333, 70003])
 @pytest.mark.parametrize("din,dout", [(F32, F32), (F16, F32), (BF16, BF16), (F32, F16)])
 @pytest.mark.parametrize("offset,pad", [(1, 0), (3, 5), (0, 24)])
 def test_softmax_strides_and_offsets(n, din, dout, offset, pad):

@@ -135,16 +135,19 @@ def test_tensor_refusals():
 
 def test_plans():
     rk = _rk()
-    assert rk.rk_plan_softmax(0, 0, 0, 5, 256).kernel == rk.RK_KERNEL_NONE
-    for n in (1, 8192, 8193, 131072, 200001):
-        p = rk.rk_plan_softmax(1, 0, n, 7, 256)
+    assert rk.rk_plan_softmax(0, 0, 0, 5).kernel == rk.RK_KERNEL_NONE
+    for n in (1, 2048, 2049, 8192, 8193, 16384, 16385, 65537, 131072, 200001):
+        p = rk.rk_plan_softmax(1, 0, n, 7)
         assert p.split * p.tile_outputs >= n > (p.split - 1) * p.tile_outputs
         assert p.workspace_bytes % 256 == 0
+        line = n <= 16384
+        assert p.kernel == (rk.RK_KERNEL_SOFTMAX_LINE if line else rk.RK_KERNEL_SOFTMAX_SPLIT)
+        assert p.launches == (1 if line else 2) and (p.workspace_bytes == 0) == line
     p = rk.rk_plan_draft_verify(0, 131072, 64, 256)
     assert p.kernel == rk.RK_KERNEL_DRAFT_VERIFY and p.launches == 1
     assert p.workspace_bytes >= 64 * -(-131072 // p.tile_outputs) * 8
-    assert rk.rk_plan_draft_verify(0, 131072, 5000, 256).launches == 2      # more counters than a slot holds
-    assert rk.rk_plan_draft_verify(0, 100, 5000, 256).split == 1
+    assert rk.rk_plan_draft_verify(0, 131072, 5000, 256).split == 1         # a block a request fills the chip
+    assert rk.rk_plan_draft_verify(0, 100, 1, 256).split == 1
     prev = rk.rk_debug_set_fused_finish(0)
     try:
         assert rk.rk_plan_draft_verify(0, 131072, 64, 256).launches == 2
