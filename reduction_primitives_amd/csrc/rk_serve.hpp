@@ -11,10 +11,17 @@
 namespace rk {
 namespace tune {
 // ---- softmax of lines
+// A line of up to kSoftLanes * kSoftPer entries is one block's (a wave's up to
+// 64 * kSoftPer), in one launch; longer ones are split over two.  Measured,
+// one block against split: 5 x 8192 f32 3.4 / 4.9 us, 512 x 8192 8.3 / 10.9,
+// 128 x 20000 6.6 / 9.3, 512 x 32768 bf16 19.5 / 20.8, 5 x 32768 5.5 / 5.2;
+// with 64 entries a thread 5 x 65536 took 10.9 us against 5.4.
 constexpr int kSoftPer = 32;              // entries a thread holds of a line kept in registers
-constexpr int kSoftLanes = 512;           // most threads that share such a line
+constexpr int kSoftLanes = 1024;          // most threads that share such a line
 constexpr int kSoftBlock = 256;           // threads of a split line's blocks
-constexpr int kSoftTile = 2048;           // entries of a wave's tile of a split line
+// Entries of a wave's tile of a split line.  4096: 5 x 131072 f32 6.7 us,
+// 320 x 131072 bf16 to f32 49.2; 2048: 5.6, 49.1; 1024: 5.6, 49.8.
+constexpr int kSoftTile = 2048;
 // Outputs beyond the eight L2s together (32 MB) are stored past the caches, so
 // the input stays there for its second reading: 320 x 131072 bf16 to f32 (168
 // MB out) 60.2 us with plain stores, 48.4 us with streaming ones.  Smaller

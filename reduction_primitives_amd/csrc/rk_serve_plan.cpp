@@ -33,7 +33,10 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
         p->block = 256;
         p->grid = (lines + 3) / 4;
     } else if (n <= tune::kSoftLanes * tune::kSoftPer) {
-        p->lanes = p->block = n <= 256 * tune::kSoftPer ? 256 : tune::kSoftLanes;
+        p->lanes = 256;
+        while (p->lanes * tune::kSoftPer < n)
+            p->lanes *= 2;
+        p->block = p->lanes;
         p->grid = lines;
     } else {
         constexpr int waves = tune::kSoftBlock / 64;

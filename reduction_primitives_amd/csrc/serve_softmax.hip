@@ -3,7 +3,7 @@
 //   p_i = exp((x_i - m) / t) / s,   m = max_j x_j,   s = sum_j exp((x_j - m) / t)
 //
 // Two forms.  A line of up to 32 entries a thread of one block (a wave for the
-// shortest, 512 threads for the longest) is read once, kept in registers, and
+// shortest, 1024 threads for the longest) is read once, kept in registers, and
 // written: one launch, each byte moved once.  Of a longer one the first launch
 // leaves every tile's largest entry m_c and s_c = sum exp((x_j - m_c) / t), a
 // tile a wave, with no barrier between the waves; the second folds them,
@@ -481,6 +481,7 @@ int run_softmax(const SoftmaxLaunch &L)
         case 64: launch_line<In, Out, 64, 256>(L); break;
         case 256: launch_line<In, Out, 256, 256>(L); break;
         case 512: launch_line<In, Out, 512, 512>(L); break;
+        case 1024: launch_line<In, Out, 1024, 1024>(L); break;
         default: return ST_UNSUPPORTED;
         }
     } else {

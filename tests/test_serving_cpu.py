@@ -136,11 +136,11 @@ def test_tensor_refusals():
 def test_plans():
     rk = _rk()
     assert rk.rk_plan_softmax(0, 0, 0, 5).kernel == rk.RK_KERNEL_NONE
-    for n in (1, 2048, 2049, 8192, 8193, 16384, 16385, 65537, 131072, 200001):
+    for n in (1, 2048, 2049, 8192, 8193, 16384, 16385, 32768, 32769, 131072, 200001):
         p = rk.rk_plan_softmax(1, 0, n, 7)
         assert p.split * p.tile_outputs >= n > (p.split - 1) * p.tile_outputs
         assert p.workspace_bytes % 256 == 0
-        line = n <= 16384
+        line = n <= 32768
         assert p.kernel == (rk.RK_KERNEL_SOFTMAX_LINE if line else rk.RK_KERNEL_SOFTMAX_SPLIT)
         assert p.launches == (1 if line else 2) and (p.workspace_bytes == 0) == line
     p = rk.rk_plan_draft_verify(0, 131072, 64, 256)
