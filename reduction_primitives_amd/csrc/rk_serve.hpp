@@ -35,8 +35,8 @@ constexpr int kVerifyBlocksPerCu = 8;     // grid cap = CUs * this
 constexpr int kScanBlock = 1024;          // threads of the one block that scans the requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
 constexpr int kSlotBlock = 256;
-constexpr int kSlotTokens = 4;            // consecutive tokens of one thread
-constexpr int kSlotLdsRequests = 8192;    // requests whose offsets a block keeps in LDS
+constexpr int kSlotLdsRequests = 4096;    // requests a block keeps in LDS (12 bytes each)
+constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this
 }  // namespace tune
 
 enum ServeKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2, VK_VERIFY = 3 };

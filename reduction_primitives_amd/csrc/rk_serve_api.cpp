@@ -345,8 +345,8 @@ int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int bl
                 return RK_ERR_INVALID_ARGUMENT;
     }
     const int cus = host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus;
-    const int64_t step = int64_t(tune::kSlotBlock) * tune::kSlotTokens;
-    int64_t per = (capacity + int64_t(cus) * 4 - 1) / (int64_t(cus) * 4);
+    const int64_t step = int64_t(tune::kSlotBlock) * (16 / ssz), most = int64_t(cus) * tune::kSlotBlocksPerCu;
+    int64_t per = (capacity + most - 1) / most;
     per = (per + step - 1) / step * step;
     per = per < step ? step : per;
     const int64_t grid = capacity > 0 ? (capacity + per - 1) / per : 1;

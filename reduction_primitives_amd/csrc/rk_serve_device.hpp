@@ -9,20 +9,34 @@
 
 namespace rk {
 
-// 16 bytes at any element's address: gfx950 loads and stores them in one
-// instruction whatever the alignment.  Lines of an odd length start anywhere,
-// so no alignment beyond the element's own is asked of them.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+// WORDS 32-bit words at any element's address, in one load or store: gfx950
+// takes global accesses of any alignment.  Lines of an odd length start
+// anywhere, so no alignment beyond the element's own is asked of them.
+template <int WORDS> struct Words {
+    typedef uint32_t T __attribute__((ext_vector_type(WORDS)));
+    typedef uint32_t Any __attribute__((ext_vector_type(WORDS), aligned(2)));
+    __device__ __forceinline__ static T load(const void *p) { return *static_cast<const Any *>(p); }
+    template <bool STREAM>
+    __device__ __forceinline__ static void store(void *p, T v)
+    {
+        if constexpr (STREAM)                              // past the caches
+            __builtin_nontemporal_store(v, static_cast<Any *>(p));
+        else
+            *static_cast<Any *>(p) = v;
+    }
+};
 
-__device__ __forceinline__ u32x4 load16(const void *p)
+// A small array's bits as N words.
+template <int N, class T, size_t M>
+__device__ __forceinline__ typename Words<N>::T words_of(const T (&v)[M])
 {
-    return *static_cast<const u32x4_any *>(p);
+    static_assert(sizeof v == 4 * N, "size mismatch");
+    typename Words<N>::T w;
+    __builtin_memcpy(&w, v, sizeof v);
+    return w;
 }
 
-__device__ __forceinline__ void store16(void *p, u32x4 v)
-{
-    *static_cast<u32x4_any *>(p) = v;
-}
+__device__ __forceinline__ u32x4 load16(const void *p) { return Words<4>::load(p); }
 
 __device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
 {

@@ -225,81 +225,168 @@ __global__ __launch_bounds__(tune::kScanBlock) void k_slot_starts(SlotArgs a)
         a.starts[a.req] = int32_t(sum);
 }
 
-// LDS: the block scans the counts itself; otherwise a.starts holds the sums.
+// What a block keeps in LDS of every request, req + 1 words each.
+struct Kept {
+    uint32_t *start;          // tokens before it
+    int32_t *first;           // position of its first new token
+    int32_t *blocks;          // blocks of its table line that count
+};
+
+__device__ __forceinline__ int counted(int held, int max_blocks) { return held < max_blocks ? held : max_blocks; }
+
+// The block's own scan of all requests, four a thread at a time.  `lo` and
+// `hi`: the requests of the block's tokens `from` and `to` - 1.
+template <int B>
+__device__ __forceinline__ void scan_requests(const SlotArgs &a, const Kept &k, int64_t from, int64_t to, int *lo, int *hi)
+{
+    __shared__ uint32_t part[2][B / 64];
+    const int req = int(a.req);
+    uint32_t sum = 0;
+    int turn = 0;
+    for (int base = 0; base < req; base += 4 * B, turn ^= 1) {
+        const int b = base + 4 * int(threadIdx.x);
+        int len[4], fresh[4], held[4];
+        if (b + 4 <= req) {
+            const u32x4 l = load16(a.lens + b), f = load16(a.fresh + b), h = load16(a.held + b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                len[i] = int(l[i]);
+                fresh[i] = int(f[i]);
+                held[i] = int(h[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = b + i < req ? b + i : req - 1;
+                len[i] = a.lens[c];
+                fresh[i] = a.fresh[c];
+                held[i] = a.held[c];
+            }
+        }
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fresh[i] = b + i < req ? fresh_of(fresh[i], len[i]) : 0;
+            mine = sat_add(mine, uint32_t(fresh[i]));
+        }
+        uint32_t all;
+        uint32_t at = sat_add(sum, block_prefix_sat<B>(mine, part[turn], &all));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t end = sat_add(at, uint32_t(fresh[i]));
+            if (b + i < req) {
+                k.start[b + i] = at;
+                k.first[b + i] = len[i] - fresh[i];
+                k.blocks[b + i] = counted(held[i], a.max_blocks);
+                if (blockIdx.x == 0)
+                    a.starts[b + i] = int32_t(at);
+                if (from >= at && from < end)
+                    *lo = b + i;
+                if (to - 1 >= at && to - 1 < end)
+                    *hi = b + i;
+            }
+            at = end;
+        }
+        sum = sat_add(sum, all);
+    }
+    if (threadIdx.x == 0) {
+        k.start[req] = sum;
+        if (blockIdx.x == 0)
+            a.starts[req] = int32_t(sum);
+    }
+}
+
+// T tokens a thread, 16 bytes of slots, at a time: every store of a wave covers
+// one run of whole lines.  LDS: the block scans the requests itself and looks
+// them up there; otherwise a.starts holds the sums.
 template <class Slot, bool LDS>
 __global__ __launch_bounds__(tune::kSlotBlock) void k_slots(SlotArgs a)
 {
-    constexpr int B = tune::kSlotBlock, T = tune::kSlotTokens;
-    extern __shared__ uint32_t s_starts[];
+    constexpr int B = tune::kSlotBlock, T = 16 / int(sizeof(Slot));
+    extern __shared__ uint32_t lds[];
+    __shared__ int s_lo, s_hi;
     const int req = int(a.req);
-    const int32_t *starts = a.starts;
-    if constexpr (LDS) {
-        __shared__ uint32_t part[2][B / 64];
-        uint32_t sum = 0;
-        int turn = 0;
-        for (int base = 0; base < req; base += B, turn ^= 1) {
-            const int b = base + int(threadIdx.x);
-            uint32_t t;
-            const uint32_t v = b < req ? uint32_t(fresh_of(a.fresh[b], a.lens[b])) : 0u;
-            const uint32_t s = sat_add(sum, block_prefix_sat<B>(v, part[turn], &t));
-            if (b < req) {
-                s_starts[b] = s;
-                if (blockIdx.x == 0)
-                    a.starts[b] = int32_t(s);
-            }
-            sum = sat_add(sum, t);
-        }
-        if (threadIdx.x == 0) {
-            s_starts[req] = sum;
-            if (blockIdx.x == 0)
-                a.starts[req] = int32_t(sum);
-        }
-        __syncthreads();
-        starts = reinterpret_cast<const int32_t *>(s_starts);
-    }
-    const int64_t total = starts[req];
     const int64_t from = int64_t(blockIdx.x) * a.per_block;
     const int64_t to = from + a.per_block < a.capacity ? from + a.per_block : a.capacity;
+    const Kept kept{lds, reinterpret_cast<int32_t *>(lds + req + 1), reinterpret_cast<int32_t *>(lds + 2 * (req + 1))};
+    if (threadIdx.x == 0) {
+        s_lo = 0;
+        s_hi = req - 1;
+    }
+    if constexpr (LDS) {
+        __syncthreads();
+        scan_requests<B>(a, kept, from, to, &s_lo, &s_hi);
+    }
+    __syncthreads();
+    const auto start = [&](int b) { return int64_t(LDS ? kept.start[b] : uint32_t(a.starts[b])); };
+    const int64_t total = start(req);
+    const int s0 = s_lo, s1 = s_hi + 1;
     Slot *slots = static_cast<Slot *>(a.slots);
     for (int64_t t = from + int64_t(threadIdx.x) * T; t < to; t += int64_t(B) * T) {
-        int b = -1;
-        if (t < total) {                      // starts[lo] <= t < starts[hi]
-            int lo = 0, hi = req;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (starts[mid] <= t)
-                    lo = mid;
+        Slot slot[T];
+        int pos[T], who[T], off[T];
+        int32_t id[T];
+        int b = s0;
+        if (t < total) {                      // start(lo) <= t < start(hi)
+            int hi = s1;
+            while (hi - b > 1) {
+                const int mid = (b + hi) >> 1;
+                if (start(mid) <= t)
+                    b = mid;
                 else
                     hi = mid;
             }
-            b = lo;
         }
+        int64_t begin = start(b), end = t < total ? start(b + 1) : begin;
 #pragma unroll
         for (int k = 0; k < T; ++k) {
             const int64_t i = t + k;
-            if (i >= to)
-                break;
-            Slot slot = Slot(-1);
-            int pos = 0, r = -1;
-            if (i < total) {
-                while (i >= starts[b + 1])
+            id[k] = -1;
+            pos[k] = 0;
+            off[k] = 0;
+            who[k] = -1;
+            if (i < total && i < to) {
+                while (i >= end) {
                     ++b;
-                r = b;
-                const int len = a.lens[b];
-                pos = len - fresh_of(a.fresh[b], len) + int(i - starts[b]);
-                const int blk = int(divide(uint32_t(pos), a.block));
-                const int held = a.held[b];
-                if (blk < held && blk < a.max_blocks) {
-                    const int32_t id = a.table[int64_t(b) * a.ts + blk];
-                    if (id >= 0 && id < a.n_blocks)
-                        slot = Slot(int64_t(id) * a.block.d + (pos - blk * int(a.block.d)));
+                    begin = end;
+                    end = start(b + 1);
                 }
+                int first, blocks;
+                if constexpr (LDS) {
+                    first = kept.first[b];
+                    blocks = kept.blocks[b];
+                } else {
+                    const int len = a.lens[b];
+                    first = len - fresh_of(a.fresh[b], len);
+                    blocks = counted(a.held[b], a.max_blocks);
+                }
+                who[k] = b;
+                pos[k] = first + int(i - begin);
+                const int blk = int(divide(uint32_t(pos[k]), a.block));
+                off[k] = pos[k] - blk * int(a.block.d);
+                if (blk < blocks)
+                    id[k] = a.table[int64_t(b) * a.ts + blk];
             }
-            slots[i] = slot;
+        }
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+            slot[k] = id[k] >= 0 && id[k] < a.n_blocks ? Slot(int64_t(id[k]) * a.block.d + off[k]) : Slot(-1);
+        if (t + T <= to) {
+            Words<4>::template store<false>(slots + t, words_of<4>(slot));
             if (a.positions)
-                a.positions[i] = pos;
+                Words<T>::template store<false>(a.positions + t, words_of<T>(pos));
             if (a.requests)
-                a.requests[i] = r;
+                Words<T>::template store<false>(a.requests + t, words_of<T>(who));
+        } else {
+#pragma unroll
+            for (int k = 0; k < T; ++k)
+                if (t + k < to) {
+                    slots[t + k] = slot[k];
+                    if (a.positions)
+                        a.positions[t + k] = pos[k];
+                    if (a.requests)
+                        a.requests[t + k] = who[k];
+                }
         }
     }
 }
@@ -309,7 +396,7 @@ int run_slots(const SlotLaunch &L)
 {
     const dim3 grid(uint32_t(L.grid)), block(tune::kSlotBlock);
     if (L.a.req <= tune::kSlotLdsRequests) {
-        launch_timed(k_slots<Slot, true>, grid, block, (size_t(L.a.req) + 1) * 4, L.stream, L.ev_begin, L.ev_end, L.a);
+        launch_timed(k_slots<Slot, true>, grid, block, (size_t(L.a.req) + 1) * 12, L.stream, L.ev_begin, L.ev_end, L.a);
     } else {
         launch_timed(k_slot_starts, dim3(1), dim3(tune::kScanBlock), 0, L.stream, L.ev_begin, L.ev_end, L.a);
         launch_timed(k_slots<Slot, false>, grid, block, 0, L.stream, nullptr, nullptr, L.a);

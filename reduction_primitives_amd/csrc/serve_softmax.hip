@@ -68,21 +68,6 @@ template <class In> constexpr uint32_t kMaskedWord = 0xff800000u;
 template <> constexpr uint32_t kMaskedWord<bf16_in> = 0xff80ff80u;
 template <> constexpr uint32_t kMaskedWord<f16_in> = 0xfc00fc00u;
 
-// WORDS 32-bit words at any element's address, in one load or store.
-template <int WORDS> struct Words {
-    typedef uint32_t T __attribute__((ext_vector_type(WORDS)));
-    typedef uint32_t Any __attribute__((ext_vector_type(WORDS), aligned(2)));
-    __device__ __forceinline__ static T load(const void *p) { return *static_cast<const Any *>(p); }
-    template <bool STREAM>
-    __device__ __forceinline__ static void store(void *p, T v)
-    {
-        if constexpr (STREAM)                              // past the caches
-            __builtin_nontemporal_store(v, static_cast<Any *>(p));
-        else
-            *static_cast<Any *>(p) = v;
-    }
-};
-
 // Entries of a vector: 16 bytes of the wider of input and output.  Loads then
 // take 8 bytes a lane where the output is twice as wide, and every store of a
 // wave covers one run of whole lines; with 16-byte loads there, a lane's two

@@ -429,7 +429,7 @@ def batch(seed, req, longest, block, new):
 
 
 @pytest.mark.parametrize("req,longest,block,new", [(1, 1, 1, 1), (1, 5000, 16, 5000), (3, 70, 7, 70), (255, 40, 16, 1), (256, 99, 24, 5),
-                                                   (257, 300, 128, 300), (1025, 64, 8, 8), (8192, 12, 4, 3), (8193, 12, 4, 3),
+                                                   (257, 300, 128, 300), (1025, 64, 8, 8), (4096, 12, 4, 3), (4097, 12, 4, 3), (1023, 700, 3, 700),
                                                    (20000, 9, 16, 2)])
 @pytest.mark.parametrize("spare,dtype", [(0, torch.int64), (37, torch.int32)])
 def test_slots_sizes(req, longest, block, new, spare, dtype):
