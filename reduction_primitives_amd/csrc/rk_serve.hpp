@@ -34,9 +34,15 @@ constexpr int kVerifyBlocksPerCu = 8;     // grid cap = CUs * this
 // ---- block tables and slot maps
 constexpr int kScanBlock = 1024;          // threads of the one block that scans the requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
+constexpr int kMoveEach = 4;              // ids a lane moves at a time
+constexpr int kMoveBlocksPerCu = 8;       // grid cap = CUs * this, past a wave a request
 constexpr int kSlotBlock = 256;
 constexpr int kSlotLdsRequests = 4096;    // requests a block keeps in LDS (12 bytes each)
 constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this
+// Outputs beyond the eight L2s together are stored past the caches (3.1M tokens,
+// 50 MB: 13.7 us with plain stores, 12.1 us without); smaller ones stay there
+// for the kernels that write the cache.
+constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
 }  // namespace tune
 
 enum ServeKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2, VK_VERIFY = 3 };
@@ -127,6 +133,16 @@ int launch_verify(const VerifyLaunch &L);
 
 // -------------------------------------------------- block tables, slot maps
 
+// What the first launch of a block_tables call leaves for the second.
+struct TablesPlan {
+    int64_t give0, take0;     // blocks given back, blocks wanted by the requests before this one
+    int32_t held, need;
+};
+struct TablesTotals {
+    int64_t taken, given;     // blocks that move out of and into the ring
+    int64_t there, head;      // blocks that were free, and the ring place of the first
+};
+
 struct TablesArgs {
     const int32_t *lens, *held;
     int32_t *held_out;
@@ -139,14 +155,11 @@ struct TablesArgs {
     int64_t ring_size;
     const int64_t *state;
     int64_t *state_out;
-    int64_t *offsets;         // the workspace, laid out as below
+    TablesTotals *totals;     // the workspace: the totals, then a plan for every request and the end
+    TablesPlan *plan;
+    Divider waves;            // waves that move one request's blocks
 };
-// Workspace of a block_tables call: four 64-bit words (blocks taken, blocks
-// given back, blocks that were free, ring place of the first free one), then
-// for every request and for the end a pair (blocks given back, blocks wanted
-// by the requests before it), then the blocks every request held.
-constexpr int64_t kTablesHeader = 4;
-constexpr int64_t tables_ws_bytes(int64_t req) { return (kTablesHeader + 2 * (req + 1)) * 8 + 4 * req; }
+constexpr int64_t tables_ws_bytes(int64_t req) { return int64_t(sizeof(TablesTotals)) + (req + 1) * int64_t(sizeof(TablesPlan)); }
 
 struct TablesLaunch {
     TablesArgs a;
@@ -172,6 +185,7 @@ struct SlotArgs {
 struct SlotLaunch {
     SlotArgs a;
     int slot_dtype;
+    bool stream_out;          // store past the caches
     int64_t grid;
     void *stream, *ev_begin, *ev_end;
 };

@@ -282,11 +282,13 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
                 return RK_ERR_INVALID_ARGUMENT;
     }
     const int cus = host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus;
-    // at most every entry of the table moves, and at most the ring's blocks go each way
-    int64_t moves = n_req * int64_t(max_blocks);
-    moves = moves < 2 * ring_size ? moves : 2 * ring_size;
-    int64_t grid = (moves + tune::kMoveBlock - 1) / tune::kMoveBlock;
-    grid = grid < 1 ? 1 : grid < int64_t(cus) * 8 ? grid : int64_t(cus) * 8;
+    // a wave a request, more where requests are few and their lines long
+    constexpr int block_waves = tune::kMoveBlock / 64, ids = 64 * tune::kMoveEach;
+    int64_t waves = n_req > 0 ? int64_t(cus) * tune::kMoveBlocksPerCu * block_waves / n_req : 1;
+    const int64_t useful = (int64_t(max_blocks) + ids - 1) / ids;
+    waves = waves < useful ? waves : useful;
+    waves = waves < 1 ? 1 : waves;
+    const int64_t grid = n_req > 0 ? (n_req * waves + block_waves - 1) / block_waves : 0;
     if (host::debug_enabled())
         std::fprintf(stderr, "rk_block_tables: requests=%lld block=%d max_blocks=%d ring=%lld grid=%lld\n",
                      (long long)n_req, block_size, max_blocks, (long long)ring_size, (long long)grid);
@@ -304,7 +306,9 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
     L.a.ring_size = ring_size;
     L.a.state = state;
     L.a.state_out = state_out;
-    L.a.offsets = static_cast<int64_t *>(workspace);
+    L.a.totals = static_cast<TablesTotals *>(workspace);
+    L.a.plan = reinterpret_cast<TablesPlan *>(L.a.totals + 1);
+    L.a.waves = make_divider(uint32_t(waves));
     L.grid = grid;
     L.stream = stream;
     host::launch_events(&L.ev_begin, &L.ev_end);
@@ -371,6 +375,7 @@ int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int bl
     L.a.starts = starts;
     L.a.per_block = per;
     L.slot_dtype = slot_dtype;
+    L.stream_out = capacity * (ssz + (positions ? 4 : 0) + (requests ? 4 : 0)) > tune::kSlotStreamBytes;
     L.grid = grid;
     L.stream = stream;
     host::launch_events(&L.ev_begin, &L.ev_end);

@@ -43,41 +43,55 @@ __device__ __forceinline__ uint32_t divide(uint32_t x, const Divider &d)
     return d.shift ? uint32_t((uint64_t(x) * d.m) >> d.shift) : x;
 }
 
-// Inclusive scan over the 64 lanes (all active).
-template <class T>
+struct Plus {
+    template <class T> __device__ __forceinline__ static T apply(T a, T b) { return a + b; }
+};
+
+// Inclusive scan over the 64 lanes (all active) by DPP moves: shifts within
+// rows of 16, then the last lane of a row to the next row, of the lower half
+// to the upper.  Lanes without a source get 0, which Op must take as neutral.
+template <int CTRL, int ROWS, class T>
+__device__ __forceinline__ T dpp_or_0(T v)
+{
+    return move_words(v, [](uint32_t w) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, CTRL, ROWS, 0xf, false);
+    });
+}
+
+template <class Op = Plus, class T>
 __device__ __forceinline__ T wave_prefix(T v)
 {
-    const int lane = lane_id();
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const T o = __shfl_up(v, d);
-        if (lane >= d)
-            v += o;
-    }
+    v = Op::apply(v, dpp_or_0<0x111, 0xf>(v));    // row_shr:1
+    v = Op::apply(v, dpp_or_0<0x112, 0xf>(v));
+    v = Op::apply(v, dpp_or_0<0x114, 0xf>(v));
+    v = Op::apply(v, dpp_or_0<0x118, 0xf>(v));
+    v = Op::apply(v, dpp_or_0<0x142, 0xa>(v));    // row_bcast:15 into rows 1 and 3
+    v = Op::apply(v, dpp_or_0<0x143, 0xc>(v));    // row_bcast:31 into rows 2 and 3
     return v;
 }
 
 // Exclusive scan over a block of whole waves; `total` is the block's sum.
 // `part` is LDS of BLOCK / 64 values; callers separate two uses by a barrier.
-template <int BLOCK, class T>
+template <int BLOCK, class Op = Plus, class T>
 __device__ __forceinline__ T block_prefix(T v, T *part, T *total)
 {
     constexpr int NW = BLOCK / 64;
-    const T incl = wave_prefix(v);
+    const T incl = wave_prefix<Op>(v);
     const int w = int(threadIdx.x >> 6);
     if (lane_id() == 63)
         part[w] = incl;
+    const T excl = dpp_or_0<0x138, 0xf>(incl);    // wave_shr:1
     __syncthreads();
     T before = T(0), sum = T(0);
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
         const T s = part[i];
         if (i < w)
-            before += s;
-        sum += s;
+            before = Op::apply(before, s);
+        sum = Op::apply(sum, s);
     }
     *total = sum;
-    return before + (incl - v);
+    return Op::apply(before, excl);
 }
 
 template <class... KArgs, class... Args>

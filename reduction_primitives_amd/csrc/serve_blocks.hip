@@ -25,133 +25,180 @@ __device__ __forceinline__ int blocks_of(int len, const Divider &d)
 }
 
 
-// Workspace (see kTablesHeader): pairs (given back before, taken before) of
-// every request and of the end, then the blocks each request held.
-__device__ __forceinline__ int64_t *offsets_of(const TablesArgs &a) { return a.offsets + kTablesHeader; }
-__device__ __forceinline__ int32_t *held_of(const TablesArgs &a)
-{
-    return reinterpret_cast<int32_t *>(offsets_of(a) + 2 * (a.req + 1));
-}
-
 __device__ __forceinline__ int64_t ring_place(int64_t v, int64_t size)
 {
     const int64_t m = v % size;
     return m < 0 ? m + size : m;
 }
 
+// A place of the ring, 0 <= at < 2 * size.
+__device__ __forceinline__ int64_t wrap(int64_t at, int64_t size) { return at >= size ? at - size : at; }
+
+// What one request asks for.
+struct Ask {
+    int held, need, over;     // blocks it holds and gets to hold; blocks beyond the table's width
+    __device__ __forceinline__ int give() const { return held > need ? held - need : 0; }
+    __device__ __forceinline__ int take() const { return need > held ? need - held : 0; }
+};
+
+__device__ __forceinline__ Ask ask(int len, int held, const TablesArgs &a)
+{
+    Ask q;
+    const int want = blocks_of(len, a.block);
+    q.need = want < a.max_blocks ? want : a.max_blocks;
+    q.over = want - q.need;
+    q.held = held < 0 ? 0 : held > a.max_blocks ? a.max_blocks : held;
+    return q;
+}
+
+// First launch, one block: four requests a thread at a time.
 __global__ __launch_bounds__(tune::kScanBlock) void k_tables_scan(TablesArgs a)
 {
     constexpr int B = tune::kScanBlock;
     __shared__ int64_t part[2][2][B / 64];
-    __shared__ unsigned long long s_over;
-    int64_t *off = offsets_of(a);
-    int32_t *before = held_of(a);
-    if (threadIdx.x == 0)
-        s_over = 0;
+    __shared__ int64_t part_over[B / 64];
+    const int64_t head = a.state[0], tail = a.state[1];
     int64_t gives = 0, takes = 0, over = 0;
+    Ask q[4];
+    int64_t g0[4], t0[4];
     int turn = 0;
-    for (int64_t base = 0; base < a.req; base += B, turn ^= 1) {
-        const int64_t b = base + threadIdx.x;
+    for (int64_t base = 0; base < a.req; base += 4 * B, turn ^= 1) {
+        const int64_t b = base + 4 * int64_t(threadIdx.x);
+        int len[4] = {0, 0, 0, 0}, held[4] = {0, 0, 0, 0};
+        if (b + 4 <= a.req) {
+            const u32x4 l = load16(a.lens + b), h = load16(a.held + b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                len[i] = int(l[i]);
+                held[i] = int(h[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (b + i < a.req) {
+                    len[i] = a.lens[b + i];
+                    held[i] = a.held[b + i];
+                }
+        }
         int64_t give = 0, take = 0;
-        int held = 0;
-        if (b < a.req) {
-            const int want = blocks_of(a.lens[b], a.block);
-            const int need = want < a.max_blocks ? want : a.max_blocks;
-            held = a.held[b];
-            held = held < 0 ? 0 : held > a.max_blocks ? a.max_blocks : held;
-            give = held > need ? held - need : 0;
-            take = need > held ? need - held : 0;
-            over += want - need;
-            before[b] = held;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = ask(len[i], held[i], a);
+            g0[i] = give;
+            t0[i] = take;
+            give += q[i].give();
+            take += q[i].take();
+            over += q[i].over;
         }
         int64_t g, t;
-        const int64_t g0 = gives + block_prefix<B>(give, part[turn][0], &g);
-        const int64_t t0 = takes + block_prefix<B>(take, part[turn][1], &t);
+        const int64_t gb = gives + block_prefix<B>(give, part[turn][0], &g);
+        const int64_t tb = takes + block_prefix<B>(take, part[turn][1], &t);
         gives += g;
         takes += t;
-        if (b < a.req) {
-            off[2 * b] = g0;
-            off[2 * b + 1] = t0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            g0[i] += gb;
+            t0[i] += tb;
+            if (b + i < a.req)
+                a.plan[b + i] = TablesPlan{g0[i], t0[i], q[i].held, q[i].need};
         }
     }
-    if (over)
-        atomicAdd(&s_over, (unsigned long long)over);
-    const int64_t head = a.state[0], tail = a.state[1];
-    __syncthreads();                          // state and held are read before they may be written
+    int64_t missing;
+    block_prefix<B>(over, part_over, &missing);   // (state and held have been read before they may be written)
     const int64_t size = a.ring_size;
     int64_t there = tail - head;
     there = there < 0 ? 0 : there > size ? size : there;
     const int64_t given = gives < size - there ? gives : size - there;
     const int64_t taken = takes < there + given ? takes : there + given;
-    for (int64_t b = threadIdx.x; b < a.req; b += B) {
-        const int want = blocks_of(a.lens[b], a.block);
-        const int need = want < a.max_blocks ? want : a.max_blocks;
-        const int held = before[b];
-        const int64_t left = taken - off[2 * b + 1];
-        const int64_t take = need > held ? need - held : 0;
-        const int64_t got = left < 0 ? 0 : left < take ? left : take;
-        a.held_out[b] = (need < held ? need : held) + int(got);
+    for (int64_t base = 0; base < a.req; base += 4 * B) {
+        const int64_t b = base + 4 * int64_t(threadIdx.x);
+        int out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (a.req > 4 * B && b + i < a.req) {   // (otherwise the one round above has left q and t0)
+                const TablesPlan p = a.plan[b + i];
+                q[i] = Ask{p.held, p.need, 0};
+                t0[i] = p.take0;
+            }
+            const int64_t left = taken - t0[i];
+            const int take = q[i].take();
+            out[i] = (q[i].need < q[i].held ? q[i].need : q[i].held) + (left < 0 ? 0 : left < take ? int(left) : take);
+        }
+        if (b + 4 <= a.req) {
+            Words<4>::template store<false>(a.held_out + b, words_of<4>(out));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (b + i < a.req)
+                    a.held_out[b + i] = out[i];
+        }
     }
     if (threadIdx.x == 0) {
-        off[2 * a.req] = gives;
-        off[2 * a.req + 1] = takes;
-        a.offsets[0] = taken;
-        a.offsets[1] = given;
-        a.offsets[2] = there;
-        a.offsets[3] = ring_place(head, size);
+        a.plan[a.req] = TablesPlan{gives, takes, 0, 0};
+        *a.totals = TablesTotals{taken, given, there, ring_place(head, size)};
         a.state_out[0] = head + taken;
         a.state_out[1] = tail + given;
-        a.state_out[2] = takes - taken + int64_t(s_over);
+        a.state_out[2] = takes - taken + missing;
         a.state_out[3] = gives - given;
     }
 }
 
-// The last request whose offset (0: given back, 1: taken) is <= i; off holds
-// an end entry, and i < the end.
-__device__ __forceinline__ int64_t owner(const int64_t *off, int64_t req, int64_t i, int which)
+// The block id of give number g: of the last request whose gives begin at or
+// before it.
+__device__ __forceinline__ int32_t given_id(const TablesArgs &a, int64_t g)
 {
-    int64_t lo = 0, hi = req;                 // off[lo] <= i < off[hi]
+    int64_t lo = 0, hi = a.req;               // give0 of lo <= g < give0 of hi
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) / 2;
-        if (off[2 * mid + which] <= i)
+        if (a.plan[mid].give0 <= g)
             lo = mid;
         else
             hi = mid;
     }
-    return lo;
+    return a.table[lo * a.ts + a.plan[lo].need + (g - a.plan[lo].give0)];
 }
 
-// The block id of give number g.
-__device__ __forceinline__ int32_t given_id(const TablesArgs &a, const int64_t *off, int64_t g)
-{
-    const int64_t b = owner(off, a.req, g, 0);
-    const int64_t need = blocks_of(a.lens[b], a.block);      // b gives back: need < held <= max_blocks
-    return a.table[b * a.ts + need + (g - off[2 * b])];
-}
-
+// Second launch: a.waves waves move a request's blocks, kMoveEach entries a lane
+// at a time.
 __global__ __launch_bounds__(tune::kMoveBlock) void k_tables_move(TablesArgs a)
 {
-    const int64_t *off = offsets_of(a);
-    const int32_t *held = held_of(a);
-    const int64_t taken = a.offsets[0], given = a.offsets[1], there = a.offsets[2], head = a.offsets[3];
-    const int64_t stride = int64_t(gridDim.x) * tune::kMoveBlock;
-    for (int64_t i = int64_t(blockIdx.x) * tune::kMoveBlock + threadIdx.x; i < taken + given; i += stride) {
-        if (i < taken) {
-            int32_t id;
-            if (i < there) {
-                int64_t at = head + i;
-                at = at >= a.ring_size ? at - a.ring_size : at;
-                id = a.ring[at];
-            } else {
-                id = given_id(a, off, i - there);
+    constexpr int E = tune::kMoveEach;
+    const uint32_t w = blockIdx.x * (tune::kMoveBlock / 64) + uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
+    const uint32_t b = divide(w, a.waves);
+    if (b >= uint32_t(a.req))
+        return;
+    const TablesPlan p = a.plan[b];
+    const TablesTotals all = *a.totals;
+    int32_t *line = a.table + int64_t(b) * a.ts;
+    const bool gives = p.held > p.need;
+    const int64_t from = gives ? p.give0 : p.take0;
+    const int64_t limit = (gives ? all.given : all.taken) - from;
+    int64_t count = gives ? p.held - p.need : p.need - p.held;
+    count = count < limit ? count : limit;
+    const int first = gives ? p.need : p.held;
+    for (int64_t k = int64_t(w - b * a.waves.d) * (64 * E) + lane_id(); k < count; k += int64_t(a.waves.d) * (64 * E)) {
+        int32_t id[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int64_t i = k + 64 * e;
+            if (i < count) {
+                if (gives)
+                    id[e] = line[first + i];
+                else if (from + i < all.there)
+                    id[e] = a.ring[wrap(all.head + from + i, a.ring_size)];
+                else
+                    id[e] = given_id(a, from + i - all.there);
             }
-            const int64_t b = owner(off, a.req, i, 1);
-            a.table[b * a.ts + held[b] + (i - off[2 * b + 1])] = id;
-        } else {
-            const int64_t g = i - taken;
-            int64_t at = head + there + g;    // < 2 * ring_size
-            at = at >= a.ring_size ? at - a.ring_size : at;
-            a.ring[at] = given_id(a, off, g);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int64_t i = k + 64 * e;
+            if (i < count) {
+                if (gives)                    // (head + there + given <= head + size < 2 * size)
+                    a.ring[wrap(all.head + all.there + from + i, a.ring_size)] = id[e];
+                else
+                    line[first + i] = id[e];
+            }
         }
     }
 }
@@ -172,38 +219,9 @@ __device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y)
     return s < 0x7fffffffu ? s : 0x7fffffffu;
 }
 
-
-// Exclusive saturating scan over a block; total: the block's sum.
-template <int BLOCK>
-__device__ __forceinline__ uint32_t block_prefix_sat(uint32_t v, uint32_t *part, uint32_t *total)
-{
-    constexpr int NW = BLOCK / 64;
-    const int lane = lane_id();
-    uint32_t incl = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(incl, d);
-        if (lane >= d)
-            incl = sat_add(incl, o);
-    }
-    uint32_t excl = __shfl_up(incl, 1);
-    if (lane == 0)
-        excl = 0;
-    const int w = int(threadIdx.x >> 6);
-    if (lane == 63)
-        part[w] = incl;
-    __syncthreads();
-    uint32_t before = 0, sum = 0;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        const uint32_t s = part[i];
-        if (i < w)
-            before = sat_add(before, s);
-        sum = sat_add(sum, s);
-    }
-    *total = sum;
-    return sat_add(before, excl);
-}
+struct SatPlus {
+    __device__ __forceinline__ static uint32_t apply(uint32_t a, uint32_t b) { return sat_add(a, b); }
+};
 
 // More requests than a block keeps in LDS: their offsets, by one block.
 __global__ __launch_bounds__(tune::kScanBlock) void k_slot_starts(SlotArgs a)
@@ -216,7 +234,7 @@ __global__ __launch_bounds__(tune::kScanBlock) void k_slot_starts(SlotArgs a)
         const int64_t b = base + threadIdx.x;
         uint32_t t;
         const uint32_t v = b < a.req ? uint32_t(fresh_of(a.fresh[b], a.lens[b])) : 0u;
-        const uint32_t s = sat_add(sum, block_prefix_sat<B>(v, part[turn], &t));
+        const uint32_t s = sat_add(sum, block_prefix<B, SatPlus>(v, part[turn], &t));
         if (b < a.req)
             a.starts[b] = int32_t(s);
         sum = sat_add(sum, t);
@@ -270,7 +288,7 @@ __device__ __forceinline__ void scan_requests(const SlotArgs &a, const Kept &k, 
             mine = sat_add(mine, uint32_t(fresh[i]));
         }
         uint32_t all;
-        uint32_t at = sat_add(sum, block_prefix_sat<B>(mine, part[turn], &all));
+        uint32_t at = sat_add(sum, block_prefix<B, SatPlus>(mine, part[turn], &all));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t end = sat_add(at, uint32_t(fresh[i]));
@@ -299,7 +317,7 @@ __device__ __forceinline__ void scan_requests(const SlotArgs &a, const Kept &k, 
 // T tokens a thread, 16 bytes of slots, at a time: every store of a wave covers
 // one run of whole lines.  LDS: the block scans the requests itself and looks
 // them up there; otherwise a.starts holds the sums.
-template <class Slot, bool LDS>
+template <class Slot, bool LDS, bool STREAM>
 __global__ __launch_bounds__(tune::kSlotBlock) void k_slots(SlotArgs a)
 {
     constexpr int B = tune::kSlotBlock, T = 16 / int(sizeof(Slot));
@@ -372,11 +390,11 @@ __global__ __launch_bounds__(tune::kSlotBlock) void k_slots(SlotArgs a)
         for (int k = 0; k < T; ++k)
             slot[k] = id[k] >= 0 && id[k] < a.n_blocks ? Slot(int64_t(id[k]) * a.block.d + off[k]) : Slot(-1);
         if (t + T <= to) {
-            Words<4>::template store<false>(slots + t, words_of<4>(slot));
+            Words<4>::template store<STREAM>(slots + t, words_of<4>(slot));
             if (a.positions)
-                Words<T>::template store<false>(a.positions + t, words_of<T>(pos));
+                Words<T>::template store<STREAM>(a.positions + t, words_of<T>(pos));
             if (a.requests)
-                Words<T>::template store<false>(a.requests + t, words_of<T>(who));
+                Words<T>::template store<STREAM>(a.requests + t, words_of<T>(who));
         } else {
 #pragma unroll
             for (int k = 0; k < T; ++k)
@@ -396,10 +414,14 @@ int run_slots(const SlotLaunch &L)
 {
     const dim3 grid(uint32_t(L.grid)), block(tune::kSlotBlock);
     if (L.a.req <= tune::kSlotLdsRequests) {
-        launch_timed(k_slots<Slot, true>, grid, block, (size_t(L.a.req) + 1) * 12, L.stream, L.ev_begin, L.ev_end, L.a);
+        const size_t lds = (size_t(L.a.req) + 1) * 12;
+        if (L.stream_out)
+            launch_timed(k_slots<Slot, true, true>, grid, block, lds, L.stream, L.ev_begin, L.ev_end, L.a);
+        else
+            launch_timed(k_slots<Slot, true, false>, grid, block, lds, L.stream, L.ev_begin, L.ev_end, L.a);
     } else {
         launch_timed(k_slot_starts, dim3(1), dim3(tune::kScanBlock), 0, L.stream, L.ev_begin, L.ev_end, L.a);
-        launch_timed(k_slots<Slot, false>, grid, block, 0, L.stream, nullptr, nullptr, L.a);
+        launch_timed(k_slots<Slot, false, false>, grid, block, 0, L.stream, nullptr, nullptr, L.a);
     }
     return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
@@ -409,7 +431,8 @@ int run_slots(const SlotLaunch &L)
 int launch_tables(const TablesLaunch &L)
 {
     launch_timed(k_tables_scan, dim3(1), dim3(tune::kScanBlock), 0, L.stream, L.ev_begin, L.ev_end, L.a);
-    launch_timed(k_tables_move, dim3(uint32_t(L.grid)), dim3(tune::kMoveBlock), 0, L.stream, nullptr, nullptr, L.a);
+    if (L.grid > 0)
+        launch_timed(k_tables_move, dim3(uint32_t(L.grid)), dim3(tune::kMoveBlock), 0, L.stream, nullptr, nullptr, L.a);
     return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
