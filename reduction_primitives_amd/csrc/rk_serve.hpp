@@ -32,10 +32,11 @@ constexpr int kVerifyBlock = 256;
 constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums at a time
 constexpr int kVerifyBlocksPerCu = 8;     // grid cap = CUs * this
 // ---- block tables and slot maps
-constexpr int kScanBlock = 1024;          // threads of the one block that scans the requests
+constexpr int kScanBlock = 1024;          // threads of the one block that scans a slot map's many requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
 constexpr int kMoveEach = 4;              // ids a lane moves at a time
-constexpr int kMoveBlocksPerCu = 8;       // grid cap = CUs * this, past a wave a request
+constexpr int kMoveBlocksPerCu = 4;       // grid cap = CUs * this, past a wave a request
+constexpr int kMoveLdsRequests = 4096;    // requests a one-launch call takes
 constexpr int kSlotBlock = 256;
 constexpr int kSlotLdsRequests = 4096;    // requests a block keeps in LDS (12 bytes each)
 constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this
@@ -139,8 +140,8 @@ struct TablesPlan {
     int32_t held, need;
 };
 struct TablesTotals {
-    int64_t taken, given;     // blocks that move out of and into the ring
-    int64_t there, head;      // blocks that were free, and the ring place of the first
+    int64_t gives, takes;     // blocks given back and wanted in all
+    int64_t head, tail;       // of the ring, before the call
 };
 
 struct TablesArgs {
@@ -163,7 +164,8 @@ constexpr int64_t tables_ws_bytes(int64_t req) { return int64_t(sizeof(TablesTot
 
 struct TablesLaunch {
     TablesArgs a;
-    int64_t grid;             // blocks of the second launch
+    bool one_launch;
+    int64_t grid;             // blocks that move ids
     void *stream, *ev_begin, *ev_end;
 };
 int launch_tables(const TablesLaunch &L);

@@ -309,6 +309,8 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
     L.a.totals = static_cast<TablesTotals *>(workspace);
     L.a.plan = reinterpret_cast<TablesPlan *>(L.a.totals + 1);
     L.a.waves = make_divider(uint32_t(waves));
+    L.one_launch = n_req > 0 && n_req <= tune::kMoveLdsRequests && n_req * int64_t(max_blocks) < (int64_t(1) << 31) &&
+                   held_out != held && state_out != state;
     L.grid = grid;
     L.stream = stream;
     host::launch_events(&L.ev_begin, &L.ev_end);

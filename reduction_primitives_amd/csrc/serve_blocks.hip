@@ -7,8 +7,8 @@
 // block number i of those it takes comes from place head + T_b + i.  A place
 // at or behind the old tail holds a block given back in this very call: it
 // is read from the giver's table row, never from the ring, so no block waits
-// for another's store.  The first launch, one block, scans the requests; the
-// second moves the ids, any number of blocks on any request's.
+// for another's store.  A wave (or several) moves a request's ids, which lie
+// next to each other in the ring and in the table.
 //
 // slot_map.  starts_b, the exclusive sum of the new tokens, is scanned by
 // every block for itself (a few thousand counts cost less than a launch);
@@ -25,8 +25,12 @@ __device__ __forceinline__ int blocks_of(int len, const Divider &d)
 }
 
 
+// v modulo size (1 <= size < 2^31), not negative.  A 64-bit remainder takes
+// over a hundred instructions, so counters that fit 32 bits do without.
 __device__ __forceinline__ int64_t ring_place(int64_t v, int64_t size)
 {
+    if (v >= 0 && v < (int64_t(1) << 32))
+        return uint32_t(v) % uint32_t(size);
     const int64_t m = v % size;
     return m < 0 ? m + size : m;
 }
@@ -39,31 +43,18 @@ struct Ask {
     int held, need, over;     // blocks it holds and gets to hold; blocks beyond the table's width
     __device__ __forceinline__ int give() const { return held > need ? held - need : 0; }
     __device__ __forceinline__ int take() const { return need > held ? need - held : 0; }
+    __device__ __forceinline__ int after(int64_t left) const   // blocks held when `left` blocks are left for it
+    {
+        const int kept = need < held ? need : held;
+        return kept + (left < 0 ? 0 : left < take() ? int(left) : take());
+    }
 };
 
-__device__ __forceinline__ Ask ask(int len, int held, const TablesArgs &a)
-{
-    Ask q;
-    const int want = blocks_of(len, a.block);
-    q.need = want < a.max_blocks ? want : a.max_blocks;
-    q.over = want - q.need;
-    q.held = held < 0 ? 0 : held > a.max_blocks ? a.max_blocks : held;
-    return q;
-}
-
-// First launch, one block: four requests a thread at a time.
-__global__ __launch_bounds__(tune::kScanBlock) void k_tables_scan(TablesArgs a)
-{
-    constexpr int B = tune::kScanBlock;
-    __shared__ int64_t part[2][2][B / 64];
-    __shared__ int64_t part_over[B / 64];
-    const int64_t head = a.state[0], tail = a.state[1];
-    int64_t gives = 0, takes = 0, over = 0;
+// Four requests from b on (those from req on ask for nothing).
+struct Asks {
     Ask q[4];
-    int64_t g0[4], t0[4];
-    int turn = 0;
-    for (int64_t base = 0; base < a.req; base += 4 * B, turn ^= 1) {
-        const int64_t b = base + 4 * int64_t(threadIdx.x);
+    __device__ __forceinline__ void load(const TablesArgs &a, int64_t b)
+    {
         int len[4] = {0, 0, 0, 0}, held[4] = {0, 0, 0, 0};
         if (b + 4 <= a.req) {
             const u32x4 l = load16(a.lens + b), h = load16(a.held + b);
@@ -80,103 +71,55 @@ __global__ __launch_bounds__(tune::kScanBlock) void k_tables_scan(TablesArgs a)
                     held[i] = a.held[b + i];
                 }
         }
-        int64_t give = 0, take = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            q[i] = ask(len[i], held[i], a);
-            g0[i] = give;
-            t0[i] = take;
-            give += q[i].give();
-            take += q[i].take();
-            over += q[i].over;
-        }
-        int64_t g, t;
-        const int64_t gb = gives + block_prefix<B>(give, part[turn][0], &g);
-        const int64_t tb = takes + block_prefix<B>(take, part[turn][1], &t);
-        gives += g;
-        takes += t;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            g0[i] += gb;
-            t0[i] += tb;
-            if (b + i < a.req)
-                a.plan[b + i] = TablesPlan{g0[i], t0[i], q[i].held, q[i].need};
+            const int want = blocks_of(len[i], a.block);
+            q[i].need = want < a.max_blocks ? want : a.max_blocks;
+            q[i].over = want - q[i].need;
+            q[i].held = held[i] < 0 ? 0 : held[i] > a.max_blocks ? a.max_blocks : held[i];
         }
     }
-    int64_t missing;
-    block_prefix<B>(over, part_over, &missing);   // (state and held have been read before they may be written)
-    const int64_t size = a.ring_size;
-    int64_t there = tail - head;
-    there = there < 0 ? 0 : there > size ? size : there;
-    const int64_t given = gives < size - there ? gives : size - there;
-    const int64_t taken = takes < there + given ? takes : there + given;
-    for (int64_t base = 0; base < a.req; base += 4 * B) {
-        const int64_t b = base + 4 * int64_t(threadIdx.x);
-        int out[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (a.req > 4 * B && b + i < a.req) {   // (otherwise the one round above has left q and t0)
-                const TablesPlan p = a.plan[b + i];
-                q[i] = Ask{p.held, p.need, 0};
-                t0[i] = p.take0;
-            }
-            const int64_t left = taken - t0[i];
-            const int take = q[i].take();
-            out[i] = (q[i].need < q[i].held ? q[i].need : q[i].held) + (left < 0 ? 0 : left < take ? int(left) : take);
-        }
-        if (b + 4 <= a.req) {
-            Words<4>::template store<false>(a.held_out + b, words_of<4>(out));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (b + i < a.req)
-                    a.held_out[b + i] = out[i];
-        }
-    }
-    if (threadIdx.x == 0) {
-        a.plan[a.req] = TablesPlan{gives, takes, 0, 0};
-        *a.totals = TablesTotals{taken, given, there, ring_place(head, size)};
-        a.state_out[0] = head + taken;
-        a.state_out[1] = tail + given;
-        a.state_out[2] = takes - taken + missing;
-        a.state_out[3] = gives - given;
-    }
-}
+};
 
-// The block id of give number g: of the last request whose gives begin at or
-// before it.
-__device__ __forceinline__ int32_t given_id(const TablesArgs &a, int64_t g)
+// The ring before and after the call.
+struct Ring {
+    int64_t there, head;      // blocks that were free, and the place of the first
+    int64_t given, taken;     // blocks that come and go
+
+    __device__ __forceinline__ Ring(int64_t head_, int64_t tail, int64_t size, int64_t gives, int64_t takes)
+    {
+        head = ring_place(head_, size);
+        there = tail - head_;
+        there = there < 0 ? 0 : there > size ? size : there;
+        given = gives < size - there ? gives : size - there;
+        taken = takes < there + given ? takes : there + given;
+    }
+};
+
+__device__ __forceinline__ void write_state(const TablesArgs &a, const Ring &r, int64_t head, int64_t tail, int64_t gives,
+                                            int64_t takes, int64_t over)
 {
-    int64_t lo = 0, hi = a.req;               // give0 of lo <= g < give0 of hi
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.plan[mid].give0 <= g)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return a.table[lo * a.ts + a.plan[lo].need + (g - a.plan[lo].give0)];
+    a.state_out[0] = head + r.taken;
+    a.state_out[1] = tail + r.given;
+    a.state_out[2] = takes - r.taken + over;
+    a.state_out[3] = gives - r.given;
 }
 
-// Second launch: a.waves waves move a request's blocks, kMoveEach entries a lane
-// at a time.
-__global__ __launch_bounds__(tune::kMoveBlock) void k_tables_move(TablesArgs a)
+// A wave's share `part` of `parts` of one request's moves, kMoveEach ids a
+// lane at a time.  p: the request's plan; given_id(g): the id of give number g.
+template <class GivenId>
+__device__ __forceinline__ void move(const TablesArgs &a, int64_t b, const TablesPlan &p, const Ring &r, uint32_t part,
+                                     uint32_t parts, GivenId &&given_id)
 {
     constexpr int E = tune::kMoveEach;
-    const uint32_t w = blockIdx.x * (tune::kMoveBlock / 64) + uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
-    const uint32_t b = divide(w, a.waves);
-    if (b >= uint32_t(a.req))
-        return;
-    const TablesPlan p = a.plan[b];
-    const TablesTotals all = *a.totals;
-    int32_t *line = a.table + int64_t(b) * a.ts;
+    int32_t *line = a.table + b * a.ts;
     const bool gives = p.held > p.need;
     const int64_t from = gives ? p.give0 : p.take0;
-    const int64_t limit = (gives ? all.given : all.taken) - from;
+    const int64_t limit = (gives ? r.given : r.taken) - from;
     int64_t count = gives ? p.held - p.need : p.need - p.held;
     count = count < limit ? count : limit;
     const int first = gives ? p.need : p.held;
-    for (int64_t k = int64_t(w - b * a.waves.d) * (64 * E) + lane_id(); k < count; k += int64_t(a.waves.d) * (64 * E)) {
+    for (int64_t k = int64_t(part) * (64 * E) + lane_id(); k < count; k += int64_t(parts) * (64 * E)) {
         int32_t id[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -184,10 +127,10 @@ __global__ __launch_bounds__(tune::kMoveBlock) void k_tables_move(TablesArgs a)
             if (i < count) {
                 if (gives)
                     id[e] = line[first + i];
-                else if (from + i < all.there)
-                    id[e] = a.ring[wrap(all.head + from + i, a.ring_size)];
+                else if (from + i < r.there)
+                    id[e] = a.ring[wrap(r.head + from + i, a.ring_size)];
                 else
-                    id[e] = given_id(a, from + i - all.there);
+                    id[e] = given_id(from + i - r.there);
             }
         }
 #pragma unroll
@@ -195,12 +138,164 @@ __global__ __launch_bounds__(tune::kMoveBlock) void k_tables_move(TablesArgs a)
             const int64_t i = k + 64 * e;
             if (i < count) {
                 if (gives)                    // (head + there + given <= head + size < 2 * size)
-                    a.ring[wrap(all.head + all.there + from + i, a.ring_size)] = id[e];
+                    a.ring[wrap(r.head + r.there + from + i, a.ring_size)] = id[e];
                 else
                     line[first + i] = id[e];
             }
         }
     }
+}
+
+// One launch: every block scans the requests for itself (more work in all, but
+// one launch and no round trip through memory between scan and moves), keeps
+// the plans of its own waves' requests and, for blocks given back and taken
+// again in this call, where every request's gives begin.  Only for outputs
+// apart from the inputs: other blocks may still read these.
+__global__ __launch_bounds__(tune::kMoveBlock) void k_tables(TablesArgs a)
+{
+    constexpr int B = tune::kMoveBlock, W = B / 64;
+    __shared__ int64_t part[2][B / 64], part_over[B / 64];
+    __shared__ TablesPlan plans[W];
+    extern __shared__ uint32_t give0[];
+    const int64_t head = a.state[0], tail = a.state[1];
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const uint32_t w0 = blockIdx.x * W, w = w0 + uint32_t(wave);
+    const int b0 = int(divide(w0, a.waves)), b1 = int(divide(w0 + W - 1, a.waves));
+    uint64_t sum = 0;                         // gives, takes in its halves
+    int64_t over = 0;
+    int turn = 0;
+    for (int base = 0; base < int(a.req); base += 4 * B, turn ^= 1) {
+        const int b = base + 4 * int(threadIdx.x);
+        Asks asks;
+        asks.load(a, b);
+        uint64_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine += uint64_t(asks.q[i].give()) << 32 | uint32_t(asks.q[i].take());
+        int64_t all;
+        uint64_t at = sum + uint64_t(block_prefix<B>(int64_t(mine), part[turn], &all));
+        sum += uint64_t(all);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Ask &q = asks.q[i];
+            over += q.over;
+            if (b + i < int(a.req)) {
+                give0[b + i] = uint32_t(at >> 32);
+                if (b + i >= b0 && b + i <= b1)
+                    plans[b + i - b0] = TablesPlan{int64_t(at >> 32), int64_t(uint32_t(at)), q.held, q.need};
+            }
+            at += uint64_t(q.give()) << 32 | uint32_t(q.take());
+        }
+    }
+    __syncthreads();
+    const int64_t gives = int64_t(sum >> 32), takes = int64_t(uint32_t(sum));
+    const Ring r(head, tail, a.ring_size, gives, takes);
+    if (blockIdx.x == 0) {
+        int64_t beyond;
+        block_prefix<B>(over, part_over, &beyond);
+        if (threadIdx.x == 0)
+            write_state(a, r, head, tail, gives, takes, beyond);
+    }
+    const uint32_t b = divide(w, a.waves), share = w - b * a.waves.d;
+    if (b >= uint32_t(a.req))
+        return;
+    const TablesPlan p = plans[b - uint32_t(b0)];
+    if (share == 0 && lane_id() == 0)
+        a.held_out[b] = Ask{p.held, p.need, 0}.after(r.taken - p.take0);
+    move(a, b, p, r, share, a.waves.d, [&](int64_t g) {
+        int lo = 0, hi = int(a.req);          // the last request whose gives begin at or before g
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (int64_t(give0[mid]) <= g)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int64_t need = blocks_of(a.lens[lo], a.block);      // (it gives back: need < held <= max_blocks)
+        return a.table[lo * a.ts + need + (g - int64_t(give0[lo]))];
+    });
+}
+
+// Two launches, for outputs that are the inputs and for more requests: one
+// block scans them, leaves the plans, and writes held_out and state_out.
+template <int B>
+__global__ __launch_bounds__(B) void k_tables_scan(TablesArgs a)
+{
+    __shared__ int64_t part[2][2][B / 64], part_over[B / 64];
+    const int64_t head = a.state[0], tail = a.state[1];
+    int64_t gives = 0, takes = 0, over = 0, take0 = 0;
+    Asks asks;
+    int turn = 0;
+    for (int64_t base = 0; base < a.req; base += 4 * B, turn ^= 1) {
+        const int64_t b = base + 4 * int64_t(threadIdx.x);
+        asks.load(a, b);
+        int64_t give = 0, take = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            give += asks.q[i].give();
+            take += asks.q[i].take();
+            over += asks.q[i].over;
+        }
+        int64_t g, t;
+        int64_t give0 = gives + block_prefix<B>(give, part[turn][0], &g);
+        take0 = takes + block_prefix<B>(take, part[turn][1], &t);
+        gives += g;
+        takes += t;
+        int64_t at = take0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Ask &q = asks.q[i];
+            if (b + i < a.req)
+                a.plan[b + i] = TablesPlan{give0, at, q.held, q.need};
+            give0 += q.give();
+            at += q.take();
+        }
+    }
+    int64_t beyond;
+    block_prefix<B>(over, part_over, &beyond);    // (state and held have been read before they may be written)
+    const Ring r(head, tail, a.ring_size, gives, takes);
+    for (int64_t base = 0; base < a.req; base += 4 * B) {
+        const int64_t b = base + 4 * int64_t(threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (b + i >= a.req)
+                continue;
+            if (a.req > 4 * B) {              // (otherwise the one round above has left asks and take0)
+                const TablesPlan p = a.plan[b + i];
+                asks.q[i] = Ask{p.held, p.need, 0};
+                take0 = p.take0;
+            }
+            a.held_out[b + i] = asks.q[i].after(r.taken - take0);
+            take0 += asks.q[i].take();
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.plan[a.req] = TablesPlan{gives, takes, 0, 0};
+        *a.totals = TablesTotals{gives, takes, head, tail};
+        write_state(a, r, head, tail, gives, takes, beyond);
+    }
+}
+
+__global__ __launch_bounds__(tune::kMoveBlock) void k_tables_move(TablesArgs a)
+{
+    const uint32_t w = blockIdx.x * (tune::kMoveBlock / 64) + uint32_t(__builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)));
+    const uint32_t b = divide(w, a.waves);
+    if (b >= uint32_t(a.req))
+        return;
+    const TablesPlan p = a.plan[b];
+    const TablesTotals t = *a.totals;
+    const Ring r(t.head, t.tail, a.ring_size, t.gives, t.takes);
+    move(a, b, p, r, w - b * a.waves.d, a.waves.d, [&](int64_t g) {
+        int64_t lo = 0, hi = a.req;           // the last request whose gives begin at or before g
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            if (a.plan[mid].give0 <= g)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return a.table[lo * a.ts + a.plan[lo].need + (g - a.plan[lo].give0)];
+    });
 }
 
 // ------------------------------------------------------------------ slots
@@ -430,9 +525,17 @@ int run_slots(const SlotLaunch &L)
 
 int launch_tables(const TablesLaunch &L)
 {
-    launch_timed(k_tables_scan, dim3(1), dim3(tune::kScanBlock), 0, L.stream, L.ev_begin, L.ev_end, L.a);
-    if (L.grid > 0)
-        launch_timed(k_tables_move, dim3(uint32_t(L.grid)), dim3(tune::kMoveBlock), 0, L.stream, nullptr, nullptr, L.a);
+    const dim3 grid(uint32_t(L.grid)), block(tune::kMoveBlock);
+    if (L.one_launch) {
+        launch_timed(k_tables, grid, block, size_t(L.a.req) * 4, L.stream, L.ev_begin, L.ev_end, L.a);
+    } else {
+        if (L.a.req <= 1024)
+            launch_timed(k_tables_scan<256>, dim3(1), dim3(256), 0, L.stream, L.ev_begin, L.ev_end, L.a);
+        else
+            launch_timed(k_tables_scan<1024>, dim3(1), dim3(1024), 0, L.stream, L.ev_begin, L.ev_end, L.a);
+        if (L.grid > 0)
+            launch_timed(k_tables_move, grid, block, 0, L.stream, nullptr, nullptr, L.a);
+    }
     return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
