@@ -35,7 +35,7 @@ constexpr int kVerifyBlocksPerCu = 8;     // grid cap = CUs * this
 constexpr int kScanBlock = 1024;          // threads of the one block that scans a slot map's many requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
 constexpr int kMoveEach = 4;              // ids a lane moves at a time
-constexpr int kMoveBlocksPerCu = 4;       // grid cap = CUs * this, past a wave a request
+constexpr int kMoveBlocksPerCu = 4;       // grid cap = CUs * this (two launches: past a wave a request)
 constexpr int kMoveLdsRequests = 4096;    // requests a one-launch call takes
 constexpr int kSlotBlock = 256;
 constexpr int kSlotLdsRequests = 4096;    // requests a block keeps in LDS (12 bytes each)

@@ -282,13 +282,22 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
                 return RK_ERR_INVALID_ARGUMENT;
     }
     const int cus = host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus;
-    // a wave a request, more where requests are few and their lines long
+    const bool one_launch = n_req > 0 && n_req <= tune::kMoveLdsRequests &&
+                            n_req * int64_t(max_blocks) < (int64_t(1) << 31) && held_out != held && state_out != state;
     constexpr int block_waves = tune::kMoveBlock / 64, ids = 64 * tune::kMoveEach;
-    int64_t waves = n_req > 0 ? int64_t(cus) * tune::kMoveBlocksPerCu * block_waves / n_req : 1;
-    const int64_t useful = (int64_t(max_blocks) + ids - 1) / ids;
-    waves = waves < useful ? waves : useful;
-    waves = waves < 1 ? 1 : waves;
-    const int64_t grid = n_req > 0 ? (n_req * waves + block_waves - 1) / block_waves : 0;
+    const int64_t cap = int64_t(cus) * tune::kMoveBlocksPerCu;
+    int64_t grid, waves = 1;
+    if (one_launch) {                         // what can move, dealt to all waves
+        const int64_t most = n_req * int64_t(max_blocks);
+        grid = (most + ids * block_waves - 1) / (ids * block_waves);
+        grid = grid < 1 ? 1 : grid < cap ? grid : cap;
+    } else {                                  // a wave a request, more where requests are few and their lines long
+        const int64_t useful = (int64_t(max_blocks) + ids - 1) / ids;
+        waves = n_req > 0 ? cap * block_waves / n_req : 1;
+        waves = waves < useful ? waves : useful;
+        waves = waves < 1 ? 1 : waves;
+        grid = (n_req * waves + block_waves - 1) / block_waves;
+    }
     if (host::debug_enabled())
         std::fprintf(stderr, "rk_block_tables: requests=%lld block=%d max_blocks=%d ring=%lld grid=%lld\n",
                      (long long)n_req, block_size, max_blocks, (long long)ring_size, (long long)grid);
@@ -309,8 +318,7 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
     L.a.totals = static_cast<TablesTotals *>(workspace);
     L.a.plan = reinterpret_cast<TablesPlan *>(L.a.totals + 1);
     L.a.waves = make_divider(uint32_t(waves));
-    L.one_launch = n_req > 0 && n_req <= tune::kMoveLdsRequests && n_req * int64_t(max_blocks) < (int64_t(1) << 31) &&
-                   held_out != held && state_out != state;
+    L.one_launch = one_launch;
     L.grid = grid;
     L.stream = stream;
     host::launch_events(&L.ev_begin, &L.ev_end);

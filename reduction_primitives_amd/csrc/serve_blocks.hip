@@ -146,74 +146,130 @@ __device__ __forceinline__ void move(const TablesArgs &a, int64_t b, const Table
     }
 }
 
+// The last request of [lo, hi) whose offset is <= i: off[lo] <= i.
+__device__ __forceinline__ int owner(const uint32_t *off, int lo, int hi, uint32_t i)
+{
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// The same for one i of the whole wave among up to 4096 requests: 64 probes at
+// a time, two rounds.
+__device__ __forceinline__ int wave_owner(const uint32_t *off, int req, uint32_t i)
+{
+    static_assert(tune::kMoveLdsRequests <= 64 * 64, "two rounds");
+    const int step = (req + 63) / 64;
+    int at = lane_id() * step;
+    const int lo = (__popcll(__ballot(at < req && off[at < req ? at : 0] <= i)) - 1) * step;
+    at = lo + lane_id();
+    const bool in = lane_id() < step && at < req;
+    return lo + __popcll(__ballot(in && off[in ? at : 0] <= i)) - 1;
+}
+
 // One launch: every block scans the requests for itself (more work in all, but
-// one launch and no round trip through memory between scan and moves), keeps
-// the plans of its own waves' requests and, for blocks given back and taken
-// again in this call, where every request's gives begin.  Only for outputs
-// apart from the inputs: other blocks may still read these.
+// one launch and no round trip through memory between scan and moves) and keeps
+// their offsets in LDS; the ids that move are then dealt to the waves in equal
+// shares, whatever requests they belong to.  A wave finds the requests at its
+// ends together, its lanes theirs by bisection between these (bisection among
+// all 2048 took 4 us more).  Only for outputs apart from the inputs: other blocks may still
+// read these.
 __global__ __launch_bounds__(tune::kMoveBlock) void k_tables(TablesArgs a)
 {
-    constexpr int B = tune::kMoveBlock, W = B / 64;
-    __shared__ int64_t part[2][B / 64], part_over[B / 64];
-    __shared__ TablesPlan plans[W];
+    constexpr int B = tune::kMoveBlock, E = tune::kMoveEach;
+    __shared__ uint64_t part[2][B / 64], part_over[B / 64];
     extern __shared__ uint32_t give0[];
+    const int req = int(a.req);
+    uint32_t *take0 = give0 + req + 1;
+    int *first = reinterpret_cast<int *>(take0 + req + 1);     // the first of its table line's entries that move
     const int64_t head = a.state[0], tail = a.state[1];
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const uint32_t w0 = blockIdx.x * W, w = w0 + uint32_t(wave);
-    const int b0 = int(divide(w0, a.waves)), b1 = int(divide(w0 + W - 1, a.waves));
     uint64_t sum = 0;                         // gives, takes in its halves
-    int64_t over = 0;
+    uint64_t over = 0;
     int turn = 0;
-    for (int base = 0; base < int(a.req); base += 4 * B, turn ^= 1) {
+    for (int base = 0; base < req; base += 4 * B, turn ^= 1) {
         const int b = base + 4 * int(threadIdx.x);
         Asks asks;
         asks.load(a, b);
-        uint64_t mine = 0;
+        uint64_t mine = 0, all;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             mine += uint64_t(asks.q[i].give()) << 32 | uint32_t(asks.q[i].take());
-        int64_t all;
-        uint64_t at = sum + uint64_t(block_prefix<B>(int64_t(mine), part[turn], &all));
-        sum += uint64_t(all);
+        uint64_t at = sum + block_prefix<B>(mine, part[turn], &all);
+        sum += all;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const Ask &q = asks.q[i];
             over += q.over;
-            if (b + i < int(a.req)) {
+            if (b + i < req) {
                 give0[b + i] = uint32_t(at >> 32);
-                if (b + i >= b0 && b + i <= b1)
-                    plans[b + i - b0] = TablesPlan{int64_t(at >> 32), int64_t(uint32_t(at)), q.held, q.need};
+                take0[b + i] = uint32_t(at);
+                first[b + i] = q.need < q.held ? q.need : q.held;
             }
             at += uint64_t(q.give()) << 32 | uint32_t(q.take());
         }
     }
-    __syncthreads();
     const int64_t gives = int64_t(sum >> 32), takes = int64_t(uint32_t(sum));
+    if (threadIdx.x == 0) {
+        give0[req] = uint32_t(gives);
+        take0[req] = uint32_t(takes);
+    }
+    __syncthreads();
     const Ring r(head, tail, a.ring_size, gives, takes);
     if (blockIdx.x == 0) {
-        int64_t beyond;
+        uint64_t beyond;
         block_prefix<B>(over, part_over, &beyond);
         if (threadIdx.x == 0)
-            write_state(a, r, head, tail, gives, takes, beyond);
+            write_state(a, r, head, tail, gives, takes, int64_t(beyond));
     }
-    const uint32_t b = divide(w, a.waves), share = w - b * a.waves.d;
-    if (b >= uint32_t(a.req))
-        return;
-    const TablesPlan p = plans[b - uint32_t(b0)];
-    if (share == 0 && lane_id() == 0)
-        a.held_out[b] = Ask{p.held, p.need, 0}.after(r.taken - p.take0);
-    move(a, b, p, r, share, a.waves.d, [&](int64_t g) {
-        int lo = 0, hi = int(a.req);          // the last request whose gives begin at or before g
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (int64_t(give0[mid]) <= g)
-                lo = mid;
-            else
-                hi = mid;
+    const uint32_t threads = gridDim.x * B, id0 = blockIdx.x * B + threadIdx.x;
+    for (int b = int(id0); b < req; b += int(threads)) {
+        const int64_t left = r.taken - take0[b], take = take0[b + 1] - take0[b];
+        a.held_out[b] = first[b] + int(left < 0 ? 0 : left < take ? left : take);
+    }
+    const auto given_id = [&](uint32_t g, int lo, int hi) {
+        const int b = owner(give0, lo, hi, g);
+        return a.table[b * a.ts + first[b] + (g - give0[b])];
+    };
+    const int64_t moves = r.taken + r.given;
+    const int64_t wave = blockIdx.x * (B / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    for (int64_t base = wave * (64 * E); base < moves; base += int64_t(threads) * E) {
+        // the requests that the wave's ids can belong to: takes first, then gives
+        const int64_t end = base + 64 * E < moves ? base + 64 * E : moves;
+        int t_lo = 0, t_hi = 0, g_lo = 0, g_hi = 0;
+        if (base < r.taken) {
+            t_lo = wave_owner(take0, req, uint32_t(base));
+            t_hi = wave_owner(take0, req, uint32_t((end < r.taken ? end : r.taken) - 1)) + 1;
         }
-        const int64_t need = blocks_of(a.lens[lo], a.block);      // (it gives back: need < held <= max_blocks)
-        return a.table[lo * a.ts + need + (g - int64_t(give0[lo]))];
-    });
+        if (end > r.taken) {
+            g_lo = wave_owner(give0, req, uint32_t((base > r.taken ? base : r.taken) - r.taken));
+            g_hi = wave_owner(give0, req, uint32_t(end - 1 - r.taken)) + 1;
+        }
+        int32_t id[E];
+        int32_t *to[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int64_t i = base + 64 * e + lane_id();
+            to[e] = nullptr;
+            if (i < r.taken) {
+                const int b = owner(take0, t_lo, t_hi, uint32_t(i));
+                to[e] = a.table + (b * a.ts + first[b] + (i - take0[b]));
+                id[e] = i < r.there ? a.ring[wrap(r.head + i, a.ring_size)] : given_id(uint32_t(i - r.there), 0, req);
+            } else if (i < end) {
+                const uint32_t g = uint32_t(i - r.taken);
+                to[e] = a.ring + wrap(r.head + r.there + g, a.ring_size);   // (head + there + given <= head + size)
+                id[e] = given_id(g, g_lo, g_hi);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (to[e])
+                *to[e] = id[e];
+    }
 }
 
 // Two launches, for outputs that are the inputs and for more requests: one
@@ -527,7 +583,7 @@ int launch_tables(const TablesLaunch &L)
 {
     const dim3 grid(uint32_t(L.grid)), block(tune::kMoveBlock);
     if (L.one_launch) {
-        launch_timed(k_tables, grid, block, size_t(L.a.req) * 4, L.stream, L.ev_begin, L.ev_end, L.a);
+        launch_timed(k_tables, grid, block, (size_t(L.a.req) * 3 + 2) * 4, L.stream, L.ev_begin, L.ev_end, L.a);
     } else {
         if (L.a.req <= 1024)
             launch_timed(k_tables_scan<256>, dim3(1), dim3(256), 0, L.stream, L.ev_begin, L.ev_end, L.a);
