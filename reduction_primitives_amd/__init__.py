@@ -304,8 +304,8 @@ _SERVING = ("softmax", "draft_verify", "block_tables", "slot_map")
 
 
 def __getattr__(name):
-    # the serving operators' module needs torch when it loads; this package
-    # does not (the C ABI's bindings and plans work without a device)
+    # the serving operators' module loads torch and librk.so; this package
+    # does not, so that it can be imported to build the library
     if name in _SERVING:
         from . import serving
         globals().update({n: getattr(serving, n) for n in _SERVING})

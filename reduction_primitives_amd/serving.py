@@ -11,87 +11,102 @@ Buffers that are not given are allocated with torch on the call's stream.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _native as N
+
+_lib = N.load()
 
 _CODES = {torch.float32: N.RK_F32, torch.bfloat16: N.RK_BF16, torch.float16: N.RK_F16, torch.float64: N.RK_F64,
           torch.int32: N.RK_I32, torch.int64: N.RK_I64}
 
 
-class _Call:
-    """The device and stream of one call: the operands' device is made the
-    current one, and what the call allocates belongs to its stream."""
-
-    __slots__ = ("device", "stream", "handle", "_guards")
-
-    def __init__(self, name, stream, **operands):
-        first = None
-        for what, t in operands.items():
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{name}: {what} is not on a GPU")
-            if first is None:
-                first = t.get_device()
-            elif t.get_device() != first:
-                raise ValueError(f"{name}: {what} is on another device")
-        if stream is not None and stream.device_index != first:
-            raise ValueError(f"{name}: the stream belongs to another device")
-        self.device = first
-        self.stream = stream
-        self.handle = torch._C._cuda_getCurrentRawStream(first) if stream is None else stream.cuda_stream
-        self._guards = ()
-
-    def __enter__(self):
-        guards = []
-        if self.device != torch.cuda.current_device():
-            guards.append(torch.cuda.device(self.device))
-        if self.stream is not None:
-            guards.append(torch.cuda.stream(self.stream))
-        for g in guards:
-            g.__enter__()
-        self._guards = guards
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
-
-    def workspace(self, given, size):
-        """The caller's workspace, or one of size() bytes."""
-        return self.empty(max(int(size()), 256), torch.uint8) if given is None else given
+_PROBS = (N.RK_F32, N.RK_BF16, N.RK_F16)
+_IDS = (N.RK_I32, N.RK_I64)
+_f32, _i32, _i64 = torch.float32, torch.int32, torch.int64
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _code(name, what, t, allowed):
-    c = _CODES.get(t if isinstance(t, torch.dtype) else t.dtype)
+# The checks below run on every call of a decode step, where the kernels take
+# a few microseconds: each looks at a tensor once, in one expression, and says
+# what is wrong only when something is.
+
+def _flat(name, what, t, n, dtype, dev):
+    """t's address, for a contiguous tensor of n elements of dtype on dev."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _wrong(name, what, t, dev)
+        raise ValueError(f"{name}: {what} takes {n} contiguous {dtype}")
+    return t.data_ptr()
+
+
+def _lines(name, what, t, dev):
+    """Stride of a 2-d tensor on dev whose lines are contiguous."""
+    if t.dim() != 2 or t.get_device() != dev:
+        _wrong(name, what, t, dev)
+        raise ValueError(f"{name}: {what} takes two dims, the second contiguous")
+    stride, one = t.stride()
+    if one != 1 and t.size(1) > 1:
+        raise ValueError(f"{name}: {what} takes two dims, the second contiguous")
+    return stride
+
+
+def _wrong(name, what, t, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: {what} is not on a GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: {what} is on another device")
+
+
+def _device(name, what, t):
+    dev = t.get_device()
+    if dev < 0:
+        _wrong(name, what, t, dev)
+    return dev
+
+
+def _code(name, what, dtype, allowed):
+    c = _CODES.get(dtype)
     if c not in allowed:
-        raise ValueError(f"{name}: {what} cannot be {t if isinstance(t, torch.dtype) else t.dtype}")
+        raise ValueError(f"{name}: {what} cannot be {dtype}")
     return c
 
 
-def _lines(name, what, t):
-    """(lines, entries, stride) of a 2-d tensor whose lines are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: {what} takes two dims, the second contiguous")
-    return t.shape[0], t.shape[1], t.stride(0)
-
-
-def _flat(name, what, t, n, dtype):
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: {what} takes {n} contiguous {dtype}")
-
-
-def _check(rc, what):
+def _launch(name, dev, stream, call, *args):
+    """call(*args, stream handle) with dev the current device."""
+    if stream is None:
+        stream = _current_stream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"{name}: the stream belongs to another device")
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        rc = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, stream)
     if rc:
-        raise N.RkError(rc, what)
+        raise N.RkError(rc, "rk_" + name)
 
 
-_PROBS = (N.RK_F32, N.RK_BF16, N.RK_F16)
-_IDS = (N.RK_I32, N.RK_I64)
+def _empty(shape, dtype, dev, stream):
+    """A tensor that belongs to the call's stream, so that the caching allocator
+    hands its bytes to no other stream's work too early."""
+    with torch.cuda.device(dev), (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _workspace(name, given, size, dev, stream):
+    """The caller's workspace, or one of size() bytes."""
+    if given is None:
+        with torch.cuda.device(dev):
+            n = size()
+        return _empty(max(n, 256), torch.uint8, dev, stream)
+    if given.get_device() != dev or not given.is_contiguous():
+        _wrong(name, "workspace", given, dev)
+        raise ValueError(f"{name}: workspace takes a contiguous tensor")
+    return given
 
 
 def softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, stream=None):
@@ -99,21 +114,19 @@ def softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, strea
     (rk_softmax).  temperature: float32, one per line; a value <= 0 picks the
     first largest entry.  `out` defaults to a new tensor of out_dtype (x's
     dtype); it may be x itself.  Returns out."""
-    name = "softmax"
-    in_code = _code(name, "x", x, _PROBS)
-    lines, n, xs = _lines(name, "x", x)
-    with _Call(name, stream, x=x, temperature=temperature, out=out, workspace=workspace) as call:
-        if temperature is not None:
-            _flat(name, "temperature", temperature, lines, torch.float32)
-        if out is None:
-            out = call.empty((lines, n), out_dtype or x.dtype)
-        elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("softmax: out takes x's shape and out_dtype")
-        out_code = _code(name, "out", out, _PROBS)
-        ws = call.workspace(workspace, lambda: N.rk_softmax_workspace_size(in_code, out_code, n, lines))
-        _check(N.rk_softmax(in_code, out_code, x.data_ptr(), n, lines, xs,
-                            None if temperature is None else temperature.data_ptr(), out.data_ptr(),
-                            _lines(name, "out", out)[2], ws.data_ptr(), ws.nbytes, call.handle), "rk_softmax")
+    dev = _device("softmax", "x", x)
+    in_code = _code("softmax", "x", x.dtype, _PROBS)
+    xs = _lines("softmax", "x", x, dev)
+    lines, n = x.shape
+    t = None if temperature is None else _flat("softmax", "temperature", temperature, lines, _f32, dev)
+    if out is None:
+        out = _empty((lines, n), out_dtype or x.dtype, dev, stream)
+    elif out.shape != x.shape or (out_dtype is not None and out.dtype is not out_dtype):
+        raise ValueError("softmax: out takes x's shape and out_dtype")
+    out_code = _code("softmax", "out", out.dtype, _PROBS)
+    ws = _workspace("softmax", workspace, lambda: N.rk_softmax_workspace_size(in_code, out_code, n, lines), dev, stream)
+    _launch("softmax", dev, stream, _lib.rk_softmax, in_code, out_code, x.data_ptr(), n, lines, xs, t, out.data_ptr(),
+            _lines("softmax", "out", out, dev), ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -127,9 +140,11 @@ def draft_verify(p, q, drafted, u, r, starts=None, max_draft=None, tokens=None, 
     accepted): per request the kept tokens, the drawn one and -1 behind it,
     and how many drafts were kept."""
     name = "draft_verify"
-    code = _code(name, "p", p, _PROBS)
-    tok = _code(name, "drafted", drafted, _IDS)
-    rows, vocab, ps = _lines(name, "p", p)
+    dev = _device(name, "p", p)
+    code = _code(name, "p", p.dtype, _PROBS)
+    tok = _code(name, "drafted", drafted.dtype, _IDS)
+    ps = _lines(name, "p", p, dev)
+    rows, vocab = p.shape
     req, drafts = r.numel(), drafted.numel()
     if max_draft is None:
         if starts is not None:
@@ -137,31 +152,25 @@ def draft_verify(p, q, drafted, u, r, starts=None, max_draft=None, tokens=None, 
         max_draft = drafts // max(req, 1)
     if rows != drafts + req:
         raise ValueError("draft_verify: p takes a line for every draft and one for every request")
-    qs = 0
+    q_ptr, qs = None, 0
     if q is not None:
-        if q.dtype != p.dtype or q.shape[0] != drafts or q.shape[1] != vocab:
+        qs = _lines(name, "q", q, dev)
+        if q.dtype is not p.dtype or q.shape != (drafts, vocab):
             raise ValueError("draft_verify: q takes p's dtype and vocabulary, a line for every draft")
-        qs = _lines(name, "q", q)[2]
-    _flat(name, "drafted", drafted, drafts, drafted.dtype)
-    _flat(name, "u", u, drafts, torch.float32)
-    _flat(name, "r", r, req, torch.float32)
-    if starts is not None:
-        _flat(name, "starts", starts, req + 1, torch.int32)
-    with _Call(name, stream, p=p, q=q, drafted=drafted, u=u, r=r, starts=starts, tokens=tokens, accepted=accepted,
-               workspace=workspace) as call:
-        if tokens is None:
-            tokens = call.empty((req, max_draft + 1), drafted.dtype)
-        else:
-            _flat(name, "tokens", tokens, req * (max_draft + 1), drafted.dtype)
-        if accepted is None:
-            accepted = call.empty(req, torch.int32)
-        else:
-            _flat(name, "accepted", accepted, req, torch.int32)
-        ws = call.workspace(workspace, lambda: N.rk_draft_verify_workspace_size(code, vocab, req))
-        _check(N.rk_draft_verify(code, tok, p.data_ptr(), ps, None if q is None else q.data_ptr(), qs, vocab, req,
-                                 drafts, max_draft, None if starts is None else starts.data_ptr(),
-                                 drafted.data_ptr(), u.data_ptr(), r.data_ptr(), tokens.data_ptr(),
-                                 accepted.data_ptr(), ws.data_ptr(), ws.nbytes, call.handle), "rk_draft_verify")
+        q_ptr = q.data_ptr()
+    x_ptr = _flat(name, "drafted", drafted, drafts, drafted.dtype, dev)
+    u_ptr = _flat(name, "u", u, drafts, _f32, dev)
+    r_ptr = _flat(name, "r", r, req, _f32, dev)
+    s_ptr = None if starts is None else _flat(name, "starts", starts, req + 1, _i32, dev)
+    if tokens is None:
+        tokens = _empty((req, max_draft + 1), drafted.dtype, dev, stream)
+    if accepted is None:
+        accepted = _empty((req,), _i32, dev, stream)
+    t_ptr = _flat(name, "tokens", tokens, req * (max_draft + 1), drafted.dtype, dev)
+    a_ptr = _flat(name, "accepted", accepted, req, _i32, dev)
+    ws = _workspace(name, workspace, lambda: N.rk_draft_verify_workspace_size(code, vocab, req), dev, stream)
+    _launch(name, dev, stream, _lib.rk_draft_verify, code, tok, p.data_ptr(), ps, q_ptr, qs, vocab, req, drafts, max_draft,
+            s_ptr, x_ptr, u_ptr, r_ptr, t_ptr, a_ptr, ws.data_ptr(), ws.nbytes)
     return tokens, accepted
 
 
@@ -172,26 +181,32 @@ def block_tables(lens, block_size, held, table, ring, state, held_out=None, stat
     (4 in all) where it is updated in place; held and state are, unless held_out and state_out
     (4 int64) are given.  Returns (held_out, state_out)."""
     name = "block_tables"
-    req = lens.numel()
-    _, width, ts = _lines(name, "table", table)
-    if table.shape[0] != req or table.dtype != torch.int32:
-        raise ValueError("block_tables: table takes an int32 line for every request")
+    dev = _device(name, "lens", lens)
+    req, blocks = lens.numel(), ring.numel()
+    ts = _table(name, table, req, dev)
     held_out = held if held_out is None else held_out
     state_out = state if state_out is None else state_out
-    _flat(name, "lens", lens, req, torch.int32)
-    _flat(name, "held", held, req, torch.int32)
-    _flat(name, "held_out", held_out, req, torch.int32)
-    _flat(name, "ring", ring, ring.numel(), torch.int32)
-    _flat(name, "state_out", state_out, 4, torch.int64)
-    if state.dtype != torch.int64 or not state.is_contiguous() or state.numel() < 2:
-        raise ValueError("block_tables: state takes int64 head and tail")
-    with _Call(name, stream, lens=lens, held=held, table=table, ring=ring, state=state, held_out=held_out,
-               state_out=state_out, workspace=workspace) as call:
-        ws = call.workspace(workspace, lambda: N.rk_block_tables_workspace_size(req))
-        _check(N.rk_block_tables(lens.data_ptr(), req, block_size, held.data_ptr(), held_out.data_ptr(),
-                                 table.data_ptr(), ts, width, ring.data_ptr(), ring.numel(), state.data_ptr(),
-                                 state_out.data_ptr(), ws.data_ptr(), ws.nbytes, call.handle), "rk_block_tables")
+    l_ptr = _flat(name, "lens", lens, req, _i32, dev)
+    h_ptr = _flat(name, "held", held, req, _i32, dev)
+    o_ptr = h_ptr if held_out is held else _flat(name, "held_out", held_out, req, _i32, dev)
+    r_ptr = _flat(name, "ring", ring, blocks, _i32, dev)
+    so_ptr = _flat(name, "state_out", state_out, 4, _i64, dev)
+    if state is state_out:
+        s_ptr = so_ptr
+    else:
+        s_ptr = _flat(name, "state", state, max(state.numel(), 2), _i64, dev)
+    ws = _workspace(name, workspace, lambda: N.rk_block_tables_workspace_size(req), dev, stream)
+    _launch(name, dev, stream, _lib.rk_block_tables, l_ptr, req, block_size, h_ptr, o_ptr, table.data_ptr(), ts,
+            table.size(1), r_ptr, blocks, s_ptr, so_ptr, ws.data_ptr(), ws.nbytes)
     return held_out, state_out
+
+
+def _table(name, table, req, dev):
+    """Line stride of a block table."""
+    ts = _lines(name, "table", table, dev)
+    if table.size(0) != req or table.dtype is not _i32:
+        raise ValueError(f"{name}: table takes an int32 line for every request")
+    return ts
 
 
 def slot_map(lens, fresh, block_size, table, held, n_blocks, capacity=None, slot_dtype=None, slots=None,
@@ -201,36 +216,27 @@ def slot_map(lens, fresh, block_size, table, held, n_blocks, capacity=None, slot
     the blocks of the pool; capacity: entries of the outputs (slots' own
     when slots is given).  Returns (slots, positions, requests, starts)."""
     name = "slot_map"
+    dev = _device(name, "lens", lens)
     req = lens.numel()
-    _, width, ts = _lines(name, "table", table)
-    if table.shape[0] != req or table.dtype != torch.int32:
-        raise ValueError("slot_map: table takes an int32 line for every request")
-    _flat(name, "lens", lens, req, torch.int32)
-    _flat(name, "fresh", fresh, req, torch.int32)
-    _flat(name, "held", held, req, torch.int32)
-    if slots is not None:
-        capacity = slots.numel() if capacity is None else capacity
-        _flat(name, "slots", slots, capacity, slot_dtype or slots.dtype)
-    elif capacity is None:
-        raise ValueError("slot_map: needs capacity or slots")
-    with _Call(name, stream, lens=lens, fresh=fresh, table=table, held=held, slots=slots, positions=positions,
-               requests=requests, starts=starts) as call:
+    ts = _table(name, table, req, dev)
+    l_ptr = _flat(name, "lens", lens, req, _i32, dev)
+    f_ptr = _flat(name, "fresh", fresh, req, _i32, dev)
+    h_ptr = _flat(name, "held", held, req, _i32, dev)
+    if capacity is None:
         if slots is None:
-            slots = call.empty(capacity, slot_dtype or torch.int64)
-        code = _code(name, "slots", slots, _IDS)
-        if positions is None:
-            positions = call.empty(capacity, torch.int32)
-        else:
-            _flat(name, "positions", positions, capacity, torch.int32)
-        if requests is None:
-            requests = call.empty(capacity, torch.int32)
-        else:
-            _flat(name, "requests", requests, capacity, torch.int32)
-        if starts is None:
-            starts = call.empty(req + 1, torch.int32)
-        else:
-            _flat(name, "starts", starts, req + 1, torch.int32)
-        _check(N.rk_slot_map(lens.data_ptr(), fresh.data_ptr(), req, block_size, table.data_ptr(), ts, width,
-                             held.data_ptr(), n_blocks, code, capacity, slots.data_ptr(), positions.data_ptr(),
-                             requests.data_ptr(), starts.data_ptr(), call.handle), "rk_slot_map")
+            raise ValueError("slot_map: needs capacity or slots")
+        capacity = slots.numel()
+    if slots is None:
+        slots = _empty((capacity,), slot_dtype or _i64, dev, stream)
+    code = _code(name, "slots", slots.dtype, _IDS)
+    if positions is None:
+        positions = _empty((capacity,), _i32, dev, stream)
+    if requests is None:
+        requests = _empty((capacity,), _i32, dev, stream)
+    if starts is None:
+        starts = _empty((req + 1,), _i32, dev, stream)
+    _launch(name, dev, stream, _lib.rk_slot_map, l_ptr, f_ptr, req, block_size, table.data_ptr(), ts, table.size(1), h_ptr,
+            n_blocks, code, capacity, _flat(name, "slots", slots, capacity, slot_dtype or slots.dtype, dev),
+            _flat(name, "positions", positions, capacity, _i32, dev), _flat(name, "requests", requests, capacity, _i32, dev),
+            _flat(name, "starts", starts, req + 1, _i32, dev))
     return slots, positions, requests, starts

@@ -531,6 +531,57 @@ def test_other_stream_and_injected_failure():
         rk.softmax(torch.zeros(2, 200000, device=DEV), workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
 
 
+def test_tensor_refusals():
+    """What the Python calls refuse before the library sees it."""
+    rk = _rk()
+    x = torch.zeros(2, 8, device=DEV)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    i64 = lambda *s: torch.zeros(*s, dtype=torch.int64, device=DEV)  # noqa: E731
+    f = lambda *s: torch.zeros(*s, device=DEV)  # noqa: E731
+
+    def refused(match, call, *args, **kw):
+        with pytest.raises(ValueError, match=match):
+            call(*args, **kw)
+    refused("two dims", rk.softmax, x.t())
+    refused("two dims", rk.softmax, x[0])
+    refused("cannot be", rk.softmax, x.double())
+    refused("cannot be", rk.softmax, x, out=torch.zeros_like(x).double())
+    refused("shape", rk.softmax, x, out=f(2, 9))
+    refused("shape", rk.softmax, x, out=f(2, 8), out_dtype=BF16)
+    refused("two dims", rk.softmax, x, out=f(8, 2).t())
+    refused("temperature", rk.softmax, x, temperature=f(3))
+    refused("temperature is not on a GPU", rk.softmax, x, temperature=torch.zeros(2))
+    refused("workspace is not on a GPU", rk.softmax, x, workspace=torch.zeros(9))
+    v = rk.draft_verify
+    refused("every draft", v, f(5, 8), None, i32(4), f(4), f(2), max_draft=2)
+    refused("max_draft", v, f(6, 8), None, i32(4), f(4), f(2), starts=i32(3))
+    refused("takes p's dtype", v, f(6, 8), f(4, 7), i32(4), f(4), f(2))
+    refused("takes p's dtype", v, f(6, 8), f(4, 8).half(), i32(4), f(4), f(2))
+    refused("drafted cannot be", v, f(6, 8), None, f(4), f(4), f(2))
+    refused("u takes", v, f(6, 8), None, i32(4), f(3), f(2))
+    refused("r takes", v, f(6, 8), None, i32(4), f(4), f(4)[::2])
+    refused("starts takes", v, f(6, 8), None, i32(4), f(4), f(2), starts=i64(3), max_draft=2)
+    refused("tokens takes", v, f(6, 8), None, i32(4), f(4), f(2), tokens=i64(2, 3))
+    refused("accepted takes", v, f(6, 8), None, i32(4), f(4), f(2), accepted=i32(3))
+    t = rk.block_tables
+    refused("table", t, i32(3), 16, i32(3), i32(2, 4), i32(9), i64(4))
+    refused("table", t, i32(3), 16, i32(3), i64(3, 4), i32(9), i64(4))
+    refused("state_out", t, i32(3), 16, i32(3), i32(3, 4), i32(9), i64(2))
+    refused("state takes", t, i32(3), 16, i32(3), i32(3, 4), i32(9), i64(1), state_out=i64(4))
+    refused("held takes", t, i32(3), 16, i32(4), i32(3, 4), i32(9), i64(4))
+    refused("ring takes", t, i32(3), 16, i32(3), i32(3, 4), i64(9), i64(4))
+    m = rk.slot_map
+    refused("capacity", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10)
+    refused("slots takes", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10, capacity=5, slots=i64(4))
+    refused("slots takes", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10, slots=i64(5), slot_dtype=torch.int32)
+    refused("slots cannot be", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10, slots=f(5))
+    refused("positions takes", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10, capacity=5, positions=i32(4))
+    refused("starts takes", m, i32(3), i32(3), 16, i32(3, 4), i32(3), 10, capacity=5, starts=i32(3))
+    refused("fresh takes", m, i32(3), i32(6)[::2], 16, i32(3, 4), i32(3), 10, capacity=5)
+    with pytest.raises(rk.RkError, match="rk_slot_map"):
+        m(i32(3), i32(3), 0, i32(3, 4), i32(3), 10, capacity=5)
+
+
 class Step:
     """A serving step with drafts: room for the drafts, their slots, the
     target's probabilities, the verification, and the tables cut back to what
