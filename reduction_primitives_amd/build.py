@@ -1,4 +1,5 @@
-"""Build librk.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Build librk.so (the HIP kernels and the C ABI) in-tree for gfx950, and
+_serving.so, the serving operators' calls from Python.
 
     python -m reduction_primitives_amd.build [--force]
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librk.so")
+BINDING = os.path.join(HERE, "_serving.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 
@@ -104,17 +106,40 @@ def _compile(src_name: str, force: bool):
     return obj, "\n".join(noise) or None
 
 
+def _build_binding(force: bool) -> None:
+    """Compile serve_bind.cpp, a host-only Python module over torch's headers."""
+    src = os.path.join(CSRC, "serve_bind.cpp")
+    if not force and not _stale(BINDING, src):
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = ["g++"] + HOST_FLAGS + ["-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                                  "-isystem", os.path.join(root, "include"),
+                                  "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+                                  "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile every unit (only stale ones unless force) and link librk.so."""
+    """Compile every unit (only stale ones unless force), link librk.so and
+    build the Python module."""
     os.makedirs(OUT_DIR, exist_ok=True)
     units = KERNEL_UNITS + HIP_HOST_UNITS + PURE_UNITS
     jobs = jobs or min(len(units), max(1, min(os.cpu_count() or 1, 16)))
     objs = []
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_build_binding, force)
         for obj, msg in ex.map(lambda s: _compile(s, force), units):
             objs.append(obj)
             if msg and verbose:
                 print(msg, file=sys.stderr)
+        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         tmp = LIB + ".tmp"

@@ -568,6 +568,8 @@ def test_tensor_refusals():
     refused("table", t, i32(3), 16, i32(3), i64(3, 4), i32(9), i64(4))
     refused("state_out", t, i32(3), 16, i32(3), i32(3, 4), i32(9), i64(2))
     refused("state takes", t, i32(3), 16, i32(3), i32(3, 4), i32(9), i64(1), state_out=i64(4))
+    with pytest.raises(TypeError, match="held takes a tensor"):
+        t(i32(3), 16, [1, 2, 3], i32(3, 4), i32(9), i64(4))
     refused("held takes", t, i32(3), 16, i32(4), i32(3, 4), i32(9), i64(4))
     refused("ring takes", t, i32(3), 16, i32(3), i32(3, 4), i64(9), i64(4))
     m = rk.slot_map
