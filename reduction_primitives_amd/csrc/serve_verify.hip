@@ -37,6 +37,12 @@ __device__ __forceinline__ int64_t token_at(const void *p, int64_t i)
     return static_cast<const Tok *>(p)[i];
 }
 
+template <class T>
+__device__ __forceinline__ T wave_uniform(T v)
+{
+    return move_words(v, [](uint32_t w) { return uint32_t(__builtin_amdgcn_readfirstlane(int(w))); });
+}
+
 // What the whole block knows of its request.
 struct Drawn {
     int64_t lo;               // its first draft
@@ -57,8 +63,10 @@ __device__ __forceinline__ Drawn accept(const VerifyArgs &a, int64_t b)
         hi = hi < lo ? lo : hi > a.drafts ? a.drafts : hi;
         hi = hi - lo > a.max_draft ? lo + a.max_draft : hi;
     }
+    // uniform, and kept in scalar registers: addresses that follow from it take none of the vector ones
+    lo = wave_uniform(lo);
     d.lo = lo;
-    d.count = int(hi - lo);
+    d.count = wave_uniform(int(hi - lo));
     d.kept = d.count;
     d.x = -1;
     for (int base = 0; base < d.count; base += 64) {
@@ -80,10 +88,11 @@ __device__ __forceinline__ Drawn accept(const VerifyArgs &a, int64_t b)
         if (m) {
             const int at = __builtin_ctzll(m);
             d.kept = base + at;
-            d.x = read_lane(x, at);
+            d.x = wave_uniform(read_lane(x, at));
             break;
         }
     }
+    d.kept = wave_uniform(d.kept);
     return d;
 }
 
@@ -105,29 +114,33 @@ __device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, con
     return l;
 }
 
-// Weights of V consecutive entries from i on, one vector load a line.  Entries
-// from n on weigh nothing: a vector that would pass the line's end is read
-// from n - V instead and its first entries, which belong to others, dropped.
-// EXACT: drop infinities too, and take 1 from entry l.x (the callers say when
-// neither can be there).  TAIL: the vectors may pass the line's end.
-template <class In, bool EXACT, bool TAIL, class S>
+// Weights of V consecutive entries, one vector load a line: entries i .. i +
+// V - 1 after entry `base` of the line (base uniform, i a lane's).  Entries from n
+// on weigh nothing: a vector that would pass the line's end is read from n - V
+// instead and its first entries, which belong to others, dropped.
+// FAST: the vectors do not pass the line's end, l.x is not among them, and
+// infinities (which weigh nothing) come out as infinities.
+template <class In, bool FAST, class S>
 struct Loaded {
     static constexpr int V = InTraits<In>::vec;
     u32x4 p, q;
-    int64_t at;               // index of the vector's first entry
 
-    __device__ __forceinline__ void load(const Lines<S> &l, int64_t i, int64_t n)
+    // the vector's first entry, after base
+    __device__ __forceinline__ static int at(int i, int64_t left) { return FAST || i + V <= left ? i : int(left) - V; }
+
+    // left: entries of the line after base
+    __device__ __forceinline__ void load(const S *lp, const S *lq, int i, int64_t left)
     {
-        at = !TAIL || i + V <= n ? i : n - V;
-        p = load16(l.p + at);
-        if (l.q)
-            q = load16(l.q + at);
+        p = load16(lp + at(i, left));
+        if (lq)
+            q = load16(lq + at(i, left));
     }
 
-    __device__ __forceinline__ void weights(const Lines<S> &l, int64_t i, double *w) const
+    // x: l.x after base
+    __device__ __forceinline__ void weights(const S *lq, int i, int64_t left, int64_t x, double *w) const
     {
         InTraits<In>::decode(p, w);
-        if (l.q) {
+        if (lq) {
             double f[V];
             InTraits<In>::decode(q, f);
 #pragma unroll
@@ -136,13 +149,12 @@ struct Loaded {
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            if constexpr (EXACT)
-                w[k] = weight(at + k == l.x ? w[k] - 1.0 : w[k]);
-            else
+            if constexpr (FAST) {
                 w[k] = __builtin_fmax(w[k], 0.0);          // (NaN: 0)
-            if constexpr (TAIL)
-                if (at + k < i)
-                    w[k] = 0.0;
+            } else {
+                w[k] = weight(at(i, left) + k == x ? w[k] - 1.0 : w[k]);
+                w[k] = at(i, left) + k < i ? 0.0 : w[k];
+            }
         }
     }
 };
@@ -157,39 +169,48 @@ __device__ __forceinline__ double weight_at(const Lines<S> &l, int64_t i)
     return weight(i == l.x ? w - 1.0 : w);
 }
 
-// Sum of one tile's weights, in every lane of the wave.
-template <class In, bool EXACT, bool TAIL, class S>
+// A lane's part of the sum of the tile at `base`, G vectors of a line in flight.
+template <class In, bool FAST, int G, class S>
 __device__ __forceinline__ double sum_of(const Lines<S> &l, int64_t n, int64_t base)
 {
     constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
-    Loaded<In, EXACT, TAIL, S> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        v[u].load(l, base + (u * 64 + lane_id()) * V, n);
+    static_assert(U % G == 0, "whole rounds");
+    const S *lp = l.p + base, *lq = l.q ? l.q + base : nullptr;
+    const int64_t left = n - base, x = l.x - base;
     double s = 0.0;
+#pragma unroll 1
+    for (int g = 0; g < U; g += G) {
+        Loaded<In, FAST, S> v[G];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        double w[V];
-        v[u].weights(l, base + (u * 64 + lane_id()) * V, w);
+        for (int u = 0; u < G; ++u)
+            v[u].load(lp, lq, ((g + u) * 64 + lane_id()) * V, left);
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            s += w[k];
+        for (int u = 0; u < G; ++u) {
+            double w[V];
+            v[u].weights(lq, ((g + u) * 64 + lane_id()) * V, left, x, w);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                s += w[k];
+            issue_barrier();                  // one vector's float64 weights at a time: registers bound the waves
+        }
     }
-    return wave_reduce<OpSum>(s);
+    return s;
 }
 
+// Sum of one tile's weights, in every lane of the wave.
 template <class In, class S>
-__device__ __forceinline__ double tile_sum(const Lines<S> &l, int64_t n, int64_t tile)
+__device__ __forceinline__ double tile_sum(const Lines<S> &l, int64_t n, int64_t tile, bool fast)
 {
+    constexpr int U = kTile / (64 * InTraits<In>::vec);
     const int64_t base = tile * kTile;
     if (n < InTraits<In>::vec)
         return wave_reduce<OpSum>(lane_id() < n ? weight_at<In>(l, lane_id()) : 0.0);
-    if (!(l.x >= base && l.x < base + kTile)) {
-        const double s = base + kTile <= n ? sum_of<In, false, false>(l, n, base) : sum_of<In, false, true>(l, n, base);
+    if (fast && base + kTile <= n && !(l.x >= base && l.x < base + kTile)) {
+        const double s = wave_reduce<OpSum>(sum_of<In, true, U>(l, n, base));
         if (s < __builtin_inf())
             return s;
     }
-    return sum_of<In, true, true>(l, n, base);
+    return wave_reduce<OpSum>(sum_of<In, false, U / 2>(l, n, base));
 }
 
 // What a block's threads, in order, have to say: the place of the first one
@@ -271,7 +292,8 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
     const int t = tile.at != kNowhere ? tile.at : last;
     const double start = tile.at != kNowhere ? tile.before : -__builtin_inf();
     // the entry
-    const int64_t first = int64_t(t) * kTile + int64_t(threadIdx.x) * per;
+    const int64_t base = int64_t(wave_uniform(t)) * kTile, left = n - base;
+    const int first = int(threadIdx.x) * per;
     double w[per], mine = 0.0;
     int off[per / V];                         // place of each vector's first entry in the tile
     if (n < V) {
@@ -280,16 +302,18 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
             w[k] = first + k < n ? weight_at<In>(l, first + k) : 0.0;
 #pragma unroll
         for (int u = 0; u < per / V; ++u)
-            off[u] = int(threadIdx.x) * per + u * V;
+            off[u] = first + u * V;
     } else {
-        Loaded<In, true, true, S> x[per / V];
+        using L = Loaded<In, false, S>;
+        const S *lp = l.p + base, *lq = l.q ? l.q + base : nullptr;
+        L x[per / V];
 #pragma unroll
         for (int u = 0; u < per / V; ++u)
-            x[u].load(l, first + u * V, n);
+            x[u].load(lp, lq, first + u * V, left);
 #pragma unroll
         for (int u = 0; u < per / V; ++u) {
-            x[u].weights(l, first + u * V, w + u * V);
-            off[u] = int(x[u].at - int64_t(t) * kTile);
+            x[u].weights(lq, first + u * V, left, l.x - base, w + u * V);
+            off[u] = L::at(first + u * V, left);
         }
     }
 #pragma unroll
@@ -308,11 +332,11 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
     return int64_t(t) * kTile + (entry.at != kNowhere ? entry.at : entry.last);
 }
 
-template <class In, class S>
+template <class In, bool FAST, class S>
 __device__ __forceinline__ void sum_tiles(const VerifyArgs &a, int64_t b, const Lines<S> &l, int64_t from, int64_t step)
 {
-    for (int64_t tile = from + (threadIdx.x >> 6); tile < a.tiles; tile += step) {
-        const double s = tile_sum<In>(l, a.n, tile);
+    for (int64_t tile = from + wave_uniform(int(threadIdx.x >> 6)); tile < a.tiles; tile += step) {
+        const double s = tile_sum<In>(l, a.n, tile, FAST);
         if (lane_id() == 0)
             store_partial(a.sums + b * a.tiles + tile, s);
     }
@@ -320,7 +344,7 @@ __device__ __forceinline__ void sum_tiles(const VerifyArgs &a, int64_t b, const 
     __syncthreads();
 }
 
-// Draws the request's next token and writes its outputs.
+// Draws the request's next token.
 template <class In, class Tok>
 __device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Drawn &d)
 {
@@ -333,12 +357,22 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Dra
     if (token < 0 && (l.q || l.x >= 0)) {     // the draft leaves nothing of the target: draw from the target
         l.q = nullptr;
         l.x = -1;
-        sum_tiles<In>(a, b, l, 0, kB / 64);
+        sum_tiles<In, false>(a, b, l, 0, kB / 64);
         token = find<In>(l, a.n, sums, a.tiles, r);
     }
+    if (threadIdx.x == 0)
+        static_cast<Tok *>(a.tokens)[b * (int64_t(a.max_draft) + 1) + d.kept] = Tok(token);
+}
+
+// What is known before the next token is: the kept tokens, how many they are,
+// and -1 behind the next one.
+template <class Tok>
+__device__ __forceinline__ void write_kept(const VerifyArgs &a, int64_t b, const Drawn &d)
+{
     Tok *out = static_cast<Tok *>(a.tokens) + b * (int64_t(a.max_draft) + 1);
     for (int i = int(threadIdx.x); i <= a.max_draft; i += kB)
-        out[i] = i < d.kept ? static_cast<const Tok *>(a.drafted)[d.lo + i] : i == d.kept ? Tok(token) : Tok(-1);
+        if (i != d.kept)
+            out[i] = i < d.kept ? static_cast<const Tok *>(a.drafted)[d.lo + i] : Tok(-1);
     if (threadIdx.x == 0)
         a.accepted[b] = d.kept;
 }
@@ -351,7 +385,9 @@ __global__ __launch_bounds__(kB) void k_verify(VerifyArgs a)
     const int c = int(blockIdx.x % uint32_t(a.chunks));
     const Drawn d = accept<In, Tok>(a, b);
     const Lines<S> l = lines_of<S>(a, b, d);
-    sum_tiles<In>(a, b, l, int64_t(c) * (kB / 64), int64_t(a.chunks) * (kB / 64));
+    if (c == 0)
+        write_kept<Tok>(a, b, d);
+    sum_tiles<In, true>(a, b, l, int64_t(c) * (kB / 64), int64_t(a.chunks) * (kB / 64));
     if (a.chunks > 1) {
         if (a.slot < 0)
             return;                           // the second launch finishes
