@@ -213,41 +213,32 @@ __device__ __forceinline__ double tile_sum(const Lines<S> &l, int64_t n, int64_t
     return wave_reduce<OpSum>(sum_of<In, false, U / 2>(l, n, base));
 }
 
-// What a block's threads, in order, have to say: the place of the first one
-// that passes, with the running sum before it, and of the last one that weighs
-// something.  A lane is picked by ballot and the waves meet in LDS (LDS
-// atomics of 64 lanes on one word took 4.7 of this kernel's 11 us).
+// The place that the first of a block's threads to have one names in `at`, and
+// the last in `last` (kNowhere: none has).  A lane is picked by ballot and the
+// waves meet in LDS (LDS atomics of 64 lanes on one word took 4.7 of this
+// kernel's 11 us).
 struct Found {
-    int at, last;             // kNowhere: none
-    double before;
+    int at, last;
 };
 constexpr int kNowhere = -1;
 
 struct FoundLds {
     int at[kB / 64], last[kB / 64];
-    double before[kB / 64];
 };
 
-__device__ __forceinline__ Found first_of(FoundLds &lds, bool passes, int at, double before, bool some, int last)
+__device__ __forceinline__ Found first_of(FoundLds &lds, int at, int last)
 {
-    const uint64_t mp = __ballot(passes), ms = __ballot(some);
-    const int w = int(threadIdx.x >> 6), lane = lane_id();
-    if (mp ? lane == __builtin_ctzll(mp) : lane == 0) {
-        lds.at[w] = mp ? at : kNowhere;
-        lds.before[w] = before;
+    const uint64_t ma = __ballot(at != kNowhere), ml = __ballot(last != kNowhere);
+    if (lane_id() == 0) {
+        lds.at[threadIdx.x >> 6] = ma ? read_lane(at, __builtin_ctzll(ma)) : kNowhere;
+        lds.last[threadIdx.x >> 6] = ml ? read_lane(last, 63 - __builtin_clzll(ml)) : kNowhere;
     }
-    if (ms ? lane == 63 - __builtin_clzll(ms) : lane == 0)
-        lds.last[w] = ms ? last : kNowhere;
     __syncthreads();
-    Found f{kNowhere, kNowhere, 0.0};
+    Found f{kNowhere, kNowhere};
 #pragma unroll
     for (int i = 0; i < kB / 64; ++i) {
-        if (f.at == kNowhere && lds.at[i] != kNowhere) {
-            f.at = lds.at[i];
-            f.before = lds.before[i];
-        }
-        if (lds.last[i] != kNowhere)
-            f.last = lds.last[i];
+        f.at = f.at == kNowhere ? lds.at[i] : f.at;
+        f.last = lds.last[i] != kNowhere ? lds.last[i] : f.last;
     }
     return f;
 }
@@ -259,38 +250,61 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
 {
     constexpr int V = InTraits<In>::vec, per = kTile / kB;
     static_assert(per % V == 0, "whole vectors a thread");
-    __shared__ double part[2][kB / 64];
-    __shared__ FoundLds lds[2];
-    __syncthreads();                          // a second call's uses come after the first's
-    // the whole sum, in the order of the running one
-    double whole = 0.0, v = 0.0, before = 0.0, sum;
-    int turn = 0;
-    for (int64_t base = 0; base < tiles; base += kB, turn ^= 1) {
-        const int64_t i = base + threadIdx.x;
-        v = i < tiles ? load_partial(sums + i) : 0.0;
-        before = whole + block_prefix<kB>(v, part[turn], &sum);
-        whole += sum;
-    }
+    __shared__ double part[kB / 64];
+    __shared__ FoundLds lds;
+    // The whole sum, in the order of the running one, and the tile in which the
+    // running sum passes: every wave for itself, four sums a lane, no barrier.
+    constexpr int K = 4;
+    double v[K], before = 0.0, whole = 0.0;
+    const auto round = [&](int64_t base, double upto) {        // returns the running sum after it
+        double mine = 0.0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t i = base + lane_id() * K + k;
+            v[k] = i < tiles ? load_partial(sums + i) : 0.0;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            mine += v[k];
+        const double incl = wave_prefix(mine);
+        before = upto + dpp_or_0<0x138, 0xf>(incl);            // wave_shr:1
+        return upto + read_lane(incl, 63);
+    };
+    for (int64_t base = 0; base < tiles; base += 64 * K)
+        whole = round(base, whole);
     if (!(whole > 0.0))
         return -1;
     const double bar = r * whole;
-    // the tile in which it passes
-    Found tile{kNowhere, kNowhere, 0.0};
-    double upto = 0.0;
-    int last = kNowhere, turn2 = 0;
-    for (int64_t base = 0; base < tiles && tile.at == kNowhere; base += kB, turn ^= 1, turn2 ^= 1) {
-        const int i = int(base) + int(threadIdx.x);
-        if (tiles > kB) {                     // (otherwise the one round above has left v and before)
-            v = i < tiles ? load_partial(sums + i) : 0.0;
-            before = upto + block_prefix<kB>(v, part[turn], &sum);
-            upto += sum;
+    int t = kNowhere, last = kNowhere;
+    double start = -__builtin_inf(), upto = 0.0;
+    for (int64_t base = 0; base < tiles && t == kNowhere; base += 64 * K) {
+        if (tiles > 64 * K)                   // (otherwise the one round above has left v and before)
+            upto = round(base, upto);
+        int at = kNowhere, pos = kNowhere;
+        double run = before, begin = 0.0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int i = int(base) + lane_id() * K + k;
+            const double next = run + v[k];
+            pos = v[k] > 0.0 ? i : pos;
+            if (at == kNowhere && v[k] > 0.0 && next > bar) {
+                at = i;
+                begin = run;
+            }
+            run = next;
         }
-        tile = first_of(lds[turn2], v > 0.0 && before + v > bar, i, before, v > 0.0, i);
-        last = tile.last != kNowhere ? tile.last : last;
+        const uint64_t passes = __ballot(at != kNowhere), some = __ballot(pos != kNowhere);
+        if (passes) {
+            t = read_lane(at, __builtin_ctzll(passes));
+            start = read_lane(begin, __builtin_ctzll(passes));
+        }
+        if (some)
+            last = read_lane(pos, 63 - __builtin_clzll(some));
     }
     // none (r so near 1 that r * whole rounds to whole): the last entry that weighs something
-    const int t = tile.at != kNowhere ? tile.at : last;
-    const double start = tile.at != kNowhere ? tile.before : -__builtin_inf();
+    if (t == kNowhere)
+        t = last;
+    __syncthreads();                          // a second call's uses of LDS come after the first's
     // the entry
     const int64_t base = int64_t(wave_uniform(t)) * kTile, left = n - base;
     const int first = int(threadIdx.x) * per;
@@ -319,7 +333,7 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
 #pragma unroll
     for (int k = 0; k < per; ++k)
         mine += w[k];
-    double run = start + block_prefix<kB>(mine, part[turn], &sum);
+    double sum, run = start + block_prefix<kB>(mine, part, &sum);
     int at = kNowhere, pos = kNowhere;
 #pragma unroll
     for (int k = 0; k < per; ++k) {
@@ -328,7 +342,7 @@ __device__ __forceinline__ int64_t find(const Lines<S> &l, int64_t n, const doub
         pos = w[k] > 0.0 ? place : pos;
         at = at == kNowhere && w[k] > 0.0 && run > bar ? place : at;
     }
-    const Found entry = first_of(lds[turn2], at != kNowhere, at, 0.0, pos != kNowhere, pos);
+    const Found entry = first_of(lds, at, pos);
     return int64_t(t) * kTile + (entry.at != kNowhere ? entry.at : entry.last);
 }
 
