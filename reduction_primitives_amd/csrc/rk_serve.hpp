@@ -22,6 +22,10 @@ constexpr int kSoftBlock = 256;           // threads of a split line's blocks
 // Entries of a wave's tile of a split line.  4096: 5 x 131072 f32 6.7 us,
 // 320 x 131072 bf16 to f32 49.2; 2048: 5.6, 49.1; 1024: 5.6, 49.8.
 constexpr int kSoftTile = 2048;
+// Every wave of the writing launch folds its line's statistics, 64 tiles at a
+// time, for itself; past this many tiles (a million entries) a launch between
+// folds them once a line.
+constexpr int kSoftFoldTiles = 512;
 // Outputs beyond the eight L2s together (32 MB) are stored past the caches, so
 // the input stays there for its second reading: 320 x 131072 bf16 to f32 (168
 // MB out) 60.2 us with plain stores, 48.4 us with streaming ones.  Smaller
@@ -69,6 +73,7 @@ struct SoftmaxPlan {
     int lanes = 0;            // threads sharing a line (VK_SOFT_LINE)
     int chunks = 1;           // tiles of a line (VK_SOFT_SPLIT)
     int vec = 1;
+    bool fold = false;        // a launch of its own folds the lines' statistics (VK_SOFT_SPLIT)
     bool stream_out = false;  // the writing launch stores past the caches (VK_SOFT_SPLIT)
     size_t ws_bytes = 0;
 };
@@ -77,8 +82,9 @@ struct SoftmaxArgs {
     const void *x;
     void *out;
     const float *t;           // temperatures, or NULL (1)
-    float *stats;             // split: max, sum of every tile of every line
-    int32_t *first;           // split: place of the first largest entry in every tile
+    float *stats;             // split: max, sum of every tile of every line, then (fold) of every line
+    int32_t *first;           // split: place of the first largest entry in every tile, then (fold) its tile
+    bool fold;
     int64_t n, lines, xs, os;
     int chunks;
     Divider per_line;         // split: blocks of a line

@@ -122,7 +122,9 @@ int rk_softmax(int in_dtype, int out_dtype, const void *x, int64_t n, int64_t li
     L.a.out = out;
     L.a.t = temperature;
     L.a.stats = static_cast<float *>(workspace);
-    L.a.first = p.ws_bytes ? reinterpret_cast<int32_t *>(static_cast<float *>(workspace) + 2 * lines * p.chunks) : nullptr;
+    L.a.first = p.ws_bytes ? reinterpret_cast<int32_t *>(static_cast<float *>(workspace) + 2 * lines * (p.chunks + p.fold))
+                           : nullptr;
+    L.a.fold = p.fold;
     L.a.n = n;
     L.a.lines = lines;
     L.a.xs = x_stride;
@@ -297,6 +299,8 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
         waves = waves < useful ? waves : useful;
         waves = waves < 1 ? 1 : waves;
         grid = (n_req * waves + block_waves - 1) / block_waves;
+        if (grid > int64_t(0xffffffff) / tune::kMoveBlock)
+            return RK_ERR_UNSUPPORTED;
     }
     if (host::debug_enabled())
         std::fprintf(stderr, "rk_block_tables: requests=%lld block=%d max_blocks=%d ring=%lld grid=%lld\n",

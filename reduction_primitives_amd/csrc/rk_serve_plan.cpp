@@ -9,7 +9,8 @@ namespace {
 
 bool prob_dtype_ok(int d) { return d == F32 || d == BF16 || d == F16; }
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxLines = 0x7fffffff;
+constexpr int64_t kMaxThreads = 0xffffffff;   // of one launch
 constexpr int64_t kMaxLine = 0x7fffffff;
 
 }  // namespace
@@ -21,7 +22,7 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
         return ST_INVALID;
     if (!prob_dtype_ok(in_dtype) || !prob_dtype_ok(out_dtype))
         return ST_UNSUPPORTED;
-    if (n > kMaxLine || lines > kMaxGrid)
+    if (n > kMaxLine || lines > kMaxLines)
         return ST_UNSUPPORTED;
     p->vec = 16 / dtype_size(in_dtype);
     if (n == 0 || lines == 0)
@@ -44,11 +45,12 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
         p->block = tune::kSoftBlock;
         p->chunks = int((n + tune::kSoftTile - 1) / tune::kSoftTile);
         p->grid = lines * ((p->chunks + waves - 1) / waves);
-        p->launches = 2;
+        p->fold = p->chunks > tune::kSoftFoldTiles;
+        p->launches = p->fold ? 3 : 2;
         p->stream_out = lines * n * dtype_size(out_dtype) > tune::kSoftStreamBytes;
-        p->ws_bytes = round_up_256(size_t(lines) * size_t(p->chunks) * 12);
+        p->ws_bytes = round_up_256(size_t(lines) * size_t(p->chunks + (p->fold ? 1 : 0)) * 12);
     }
-    return p->grid > kMaxGrid ? ST_UNSUPPORTED : ST_OK;
+    return p->grid > kMaxThreads / p->block ? ST_UNSUPPORTED : ST_OK;
 }
 
 int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
@@ -56,7 +58,7 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
     *p = VerifyPlan();
     if (!dtype_known(prob_dtype) || n < 1 || req < 0)
         return ST_INVALID;
-    if (!prob_dtype_ok(prob_dtype) || n > kMaxLine || req > kMaxGrid)
+    if (!prob_dtype_ok(prob_dtype) || n > kMaxLine || req > kMaxLines)
         return ST_UNSUPPORTED;
     constexpr int waves = tune::kVerifyBlock / 64;
     p->tiles = (n + tune::kVerifyTile - 1) / tune::kVerifyTile;
@@ -66,7 +68,7 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
     fit = fit < 1 ? 1 : fit;
     p->chunks = int(chunks < fit ? chunks : fit);
     p->grid = req * p->chunks;
-    if (p->grid > kMaxGrid)
+    if (p->grid > kMaxThreads / tune::kVerifyBlock)
         return ST_UNSUPPORTED;
     p->fused_ok = req * arrive_counters(p->chunks) <= kArriveCapacity;
     p->launches = req == 0 ? 0 : p->chunks == 1 || p->fused_ok ? 1 : 2;

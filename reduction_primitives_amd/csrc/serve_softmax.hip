@@ -7,7 +7,8 @@
 // written: one launch, each byte moved once.  Of a longer one the first launch
 // leaves every tile's largest entry m_c and s_c = sum exp((x_j - m_c) / t), a
 // tile a wave, with no barrier between the waves; the second folds them,
-// s = sum_c s_c exp((m_c - m) / t), reads the line again and writes it.
+// s = sum_c s_c exp((m_c - m) / t), reads the line again and writes it (lines
+// of over a million entries are folded by a launch between).
 //
 // Sums and statistics are float32; the one rounding to the output's type is
 // the store's.  An entry of -inf counts as masked (0 whatever the temperature
@@ -403,7 +404,65 @@ __global__ __launch_bounds__(tune::kSoftBlock) void k_soft_stats(SoftmaxArgs a)
         tile_stats<In, false>(a, tile);
 }
 
-// Fold the line's statistics and write a tile of it.
+// A line's statistics.
+struct Folded {
+    float m, s;               // largest entry, sum (t > 0)
+    int tile;                 // the first tile that holds the largest entry (t <= 0)
+};
+
+// Folded by `threads` threads, `reduce` giving all of them the reduction of
+// their values.
+template <class Reduce>
+__device__ __forceinline__ Folded fold_line(const SoftmaxArgs &a, int64_t line, int thread, int threads, float t, float c,
+                                            Reduce &&reduce)
+{
+    const float *st = a.stats + 2 * line * a.chunks;
+    Folded l{OpMax::identity<float>(), 0.0f, kNone};
+    for (int i = thread; i < a.chunks; i += threads)
+        l.m = OpMax::apply(l.m, st[2 * i]);
+    l.m = reduce(OpMax(), l.m);
+    if (t <= 0.0f) {
+        for (int i = thread; i < a.chunks; i += threads)
+            if (st[2 * i] == l.m && i < l.tile)
+                l.tile = i;
+        l.tile = reduce(OpMin(), l.tile);
+    } else {
+        for (int i = thread; i < a.chunks; i += threads)
+            l.s += st[2 * i + 1] * soft_term<true>(st[2 * i], l.m, c);
+        l.s = reduce(OpSum(), l.s);
+    }
+    return l;
+}
+
+// The launch between, for lines of many tiles: one block a line.
+__global__ __launch_bounds__(tune::kSoftBlock) void k_soft_fold(SoftmaxArgs a)
+{
+    constexpr int B = tune::kSoftBlock;
+    __shared__ float part[2][B / 64];
+    __shared__ int parti[B / 64];
+    const int64_t line = blockIdx.x;
+    const float t = a.t ? a.t[line] : 1.0f;
+    int use = 0;
+    const Folded l = fold_line(a, line, int(threadIdx.x), B, t, scale_of(t), [&](auto op, auto v) {
+        if constexpr (std::is_same_v<decltype(v), int>)
+            return line_all<decltype(op), B>(v, parti);
+        else
+            return line_all<decltype(op), B>(v, part[use++]);
+    });
+    if (threadIdx.x == 0) {
+        a.stats[2 * (a.lines * a.chunks + line)] = l.m;
+        a.stats[2 * (a.lines * a.chunks + line) + 1] = l.s;
+        a.first[a.lines * a.chunks + line] = l.tile;
+    }
+}
+
+__device__ __forceinline__ Folded folded(const SoftmaxArgs &a, int64_t line)
+{
+    const int64_t at = a.lines * a.chunks + line;
+    return Folded{a.stats[2 * at], a.stats[2 * at + 1], a.first[at]};
+}
+
+// Write a tile of the line.
 template <class In, class Out, bool STREAM, bool FULL>
 __device__ __forceinline__ void tile_write(const SoftmaxArgs &a, const Tile &tile)
 {
@@ -412,32 +471,22 @@ __device__ __forceinline__ void tile_write(const SoftmaxArgs &a, const Tile &til
     p.load(static_cast<const typename P::S *>(a.x) + tile.line * a.xs + tile.base, tile.n, lane_id());
     const float t = a.t ? a.t[tile.line] : 1.0f;
     const float c = scale_of(t);
-    const float *st = a.stats + 2 * tile.line * a.chunks;
-    float m = OpMax::identity<float>();
-    for (int i = lane_id(); i < a.chunks; i += 64)
-        m = OpMax::apply(m, st[2 * i]);
-    m = wave_reduce<OpMax>(m);
+    const Folded l = a.fold ? folded(a, tile.line) : fold_line(a, tile.line, lane_id(), 64, t, c, [](auto op, auto v) {
+        return wave_reduce<decltype(op)>(v);
+    });
     auto *out = static_cast<typename OutTraits<Out>::S *>(a.out) + tile.line * a.os + tile.base;
     if (t <= 0.0f) {
-        int first = kNone;                    // the first tile that holds the largest entry
-        for (int i = lane_id(); i < a.chunks; i += 64)
-            if (st[2 * i] == m && i < first)
-                first = i;
-        first = wave_reduce<OpMin>(first);
         int64_t at = -1;
-        if (first != kNone && some(m))
-            at = int64_t(first) * tune::kSoftTile + a.first[tile.line * a.chunks + first] - tile.base;
-        p.template write_one<Out, STREAM>(out, at, others_of(m));
+        if (l.tile != kNone && some(l.m))
+            at = int64_t(l.tile) * tune::kSoftTile + a.first[tile.line * a.chunks + l.tile] - tile.base;
+        p.template write_one<Out, STREAM>(out, at, others_of(l.m));
         return;
     }
-    float s = 0.0f;
-    for (int i = lane_id(); i < a.chunks; i += 64)
-        s += st[2 * i + 1] * soft_term<true>(st[2 * i], m, c);
-    const float inv = inverse(wave_reduce<OpSum>(s));
-    if (needs_guard(m, c))
-        p.template write<Out, STREAM, true>(out, m, c, inv);
+    const float inv = inverse(l.s);
+    if (needs_guard(l.m, c))
+        p.template write<Out, STREAM, true>(out, l.m, c, inv);
     else
-        p.template write<Out, STREAM, false>(out, m, c, inv);
+        p.template write<Out, STREAM, false>(out, l.m, c, inv);
 }
 
 // Second launch.
@@ -472,6 +521,8 @@ int run_softmax(const SoftmaxLaunch &L)
     } else {
         const dim3 grid(uint32_t(L.plan.grid)), block(L.plan.block);
         launch_timed(k_soft_stats<In>, grid, block, 0, L.stream, L.ev_begin, L.ev_end, L.a);
+        if (L.plan.fold)
+            launch_timed(k_soft_fold, dim3(uint32_t(L.a.lines)), block, 0, L.stream, nullptr, nullptr, L.a);
         if (L.plan.stream_out)
             launch_timed(k_soft_write<In, Out, true>, grid, block, 0, L.stream, nullptr, nullptr, L.a);
         else

@@ -141,6 +141,33 @@ def test_softmax_in_place_and_broadcast(n):
     check_softmax(rk.softmax(one, temperature=torch.tensor(t).to(DEV)), x[:1].expand(4, n), t)
 
 
+@pytest.mark.parametrize("n", [1048576, 1048577, 3000001])
+def test_softmax_lines_of_many_tiles(n):
+    rk = _rk()
+    x = (torch.randn(4, n, generator=gen(n)) * 3).to(BF16)
+    x[1, : n - 7] = -INF
+    x[3, n // 2] = 60.0
+    t = [0.9, 1.0, 1.7, 0.0]
+    got = rk.softmax(x.to(DEV), temperature=torch.tensor(t).to(DEV), out_dtype=F32)
+    check_softmax(got, x, t)
+
+
+def test_softmax_of_nothing():
+    rk = _rk()
+    assert rk.softmax(torch.zeros(0, 9, device=DEV)).shape == (0, 9)
+    assert rk.softmax(torch.zeros(9, 0, device=DEV)).shape == (9, 0)
+
+
+def test_verify_of_nothing():
+    rk = _rk()
+    z = torch.zeros(0, device=DEV)
+    t, a = rk.draft_verify(torch.zeros(0, 9, device=DEV), None, torch.zeros(0, dtype=torch.int64, device=DEV), z, z, max_draft=3)
+    assert t.shape == (0, 4) and a.shape == (0,)
+    with pytest.raises(rk.RkError, match="invalid"):
+        rk.draft_verify(torch.zeros(1, 0, device=DEV), None, torch.zeros(0, dtype=torch.int64, device=DEV), z,
+                        torch.zeros(1, device=DEV))
+
+
 def test_softmax_same_bits_every_time():
     rk = _rk()
     x = torch.randn(9, 60001, generator=gen(1)).to(DEV)

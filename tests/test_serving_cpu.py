@@ -132,6 +132,14 @@ def test_plans():
         line = n <= 32768
         assert p.kernel == (rk.RK_KERNEL_SOFTMAX_LINE if line else rk.RK_KERNEL_SOFTMAX_SPLIT)
         assert p.launches == (1 if line else 2) and (p.workspace_bytes == 0) == line
+    p = rk.rk_plan_softmax(0, 0, 10 ** 8, 3)
+    assert p.launches == 3 and p.workspace_bytes >= 3 * (p.split + 1) * 12
+    for n, lines in ((2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (10 ** 9, 10 ** 5)):   # beyond the threads of a launch
+        with pytest.raises(rk.RkError, match="unsupported"):
+            rk.rk_plan_softmax(0, 0, n, lines)
+    assert rk.rk_plan_softmax(0, 0, 2 ** 31 - 1, 3).grid == 3 * -(-(2 ** 31 - 1) // 8192)
+    with pytest.raises(rk.RkError, match="unsupported"):
+        rk.rk_plan_draft_verify(0, 131072, 2 ** 30, 256)
     p = rk.rk_plan_draft_verify(0, 131072, 64, 256)
     assert p.kernel == rk.RK_KERNEL_DRAFT_VERIFY and p.launches == 1
     assert p.workspace_bytes >= 64 * -(-131072 // p.tile_outputs) * 8
