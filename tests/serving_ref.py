@@ -37,9 +37,10 @@ def softmax_error(x, t, want, eps_out, tiny_out):
     so z is off by at most 4 * 2^-24 |z| and its power of two by ln 2 times
     that, under 3 |z| 2^-24 relative; the power itself by 2^-23.  The sum is
     off by the mean of its terms' errors (sum p |z| <= log2 n < 20, so under
-    60 * 2^-24) and by its additions: 32 in a row in a thread, 6 and 3 levels,
-    and one for each chunk of 8192, under 64 * 2^-24 together.  Reciprocal and
-    product add 2 * 2^-24.  Results under 2^-126 are flushed."""
+    60 * 2^-24) and by its additions: 32 in a row in a thread, 6 levels of a
+    wave, 4 of a block, up to 8 tiles of a split line in a row and 8 levels for
+    these, under 64 * 2^-24 together.  Reciprocal and product add 2 * 2^-24.
+    Results under 2^-126 are flushed."""
     with np.errstate(all="ignore"):
         m = np.max(np.where(np.isnan(x), -np.inf, x), axis=1, keepdims=True, initial=-np.inf)
         z = np.abs(x - m) / np.abs(np.asarray(t, np.float64))[:, None] * np.log2(np.e)
