@@ -38,12 +38,23 @@ constexpr int kVerifyBlocksPerCu = 16;    // grid cap = CUs * this (256 x 131072
 // ---- block tables and slot maps
 constexpr int kScanBlock = 1024;          // threads of the one block that scans a slot map's many requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
-constexpr int kMoveEach = 4;              // ids a lane moves at a time
-constexpr int kMoveBlocksPerCu = 4;       // grid cap = CUs * this (two launches: past a wave a request)
-constexpr int kMoveLdsRequests = 4096;    // requests a one-launch call takes
+// Ids a lane moves at a time.  2048 requests moving 840,000 ids each way: 1
+// 14.0 us, 2 11.5, 4 10.6, 8 12 and more; but a step of decoding, which moves
+// few, 5.2 us with 1, 6.2 with 2, 8.2 with 4: it takes 1.
+constexpr int kMoveEach = 4;
+// Grid cap = CUs * this (two launches: past a wave a request), or what their
+// LDS lets run at once: every block scans all requests.  2048 requests: 2 20.8
+// us, 4 14.0, 8 16.0; 4096 (48 KB of LDS): 3 10.4, 4 14.4.
+constexpr int kMoveBlocksPerCu = 4;
+// Requests a one-launch call takes, 12 bytes of LDS each.  Against two
+// launches: 64 requests 4.1 / 5.6 us, 1024 5.8 / 6.9, 2048 7.2 / 10.0.
+constexpr int kMoveLdsRequests = 4096;
 constexpr int kSlotBlock = 256;
-constexpr int kSlotLdsRequests = 4096;    // requests a block keeps in LDS (12 bytes each)
-constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this
+// Requests a slot map's blocks keep in LDS (12 bytes each), against a launch of
+// its own that scans them: 256 requests 3.9 / 5.2 us, 1024 4.0 / 7.1, 4096 7.0 / 10.7.
+constexpr int kSlotLdsRequests = 4096;
+constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this, or what their LDS lets run at once
+constexpr int kLdsBytes = 160 << 10;      // of a CU
 // Outputs beyond the eight L2s together are stored past the caches (3.1M tokens,
 // 50 MB: 13.7 us with plain stores, 12.1 us without); smaller ones stay there
 // for the kernels that write the cache.
@@ -62,6 +73,13 @@ struct Divider {
     int shift;
 };
 Divider make_divider(uint32_t d);
+
+// Blocks of `lds` bytes that a CU runs at once, at most `most`.
+constexpr int64_t resident(int64_t lds, int64_t most)
+{
+    const int64_t fit = tune::kLdsBytes / (lds > 0 ? lds : 1);
+    return fit < 1 ? 1 : fit < most ? fit : most;
+}
 
 // ------------------------------------------------------------------ softmax
 
@@ -166,6 +184,9 @@ struct TablesArgs {
     TablesPlan *plan;
     Divider waves;            // waves that move one request's blocks
 };
+// LDS of a one-launch call's block: three words a request, two more, and its scans' sums.
+constexpr int64_t tables_lds_bytes(int64_t req) { return (3 * req + 2) * 4; }
+constexpr int64_t kTablesLdsFixed = 256;
 constexpr int64_t tables_ws_bytes(int64_t req) { return int64_t(sizeof(TablesTotals)) + (req + 1) * int64_t(sizeof(TablesPlan)); }
 
 struct TablesLaunch {
@@ -190,6 +211,8 @@ struct SlotArgs {
     int32_t *positions, *requests, *starts;
     int64_t per_block;        // tokens of a block
 };
+constexpr int64_t slots_lds_bytes(int64_t req) { return (req + 1) * 12; }
+constexpr int64_t kSlotsLdsFixed = 256;
 struct SlotLaunch {
     SlotArgs a;
     int slot_dtype;

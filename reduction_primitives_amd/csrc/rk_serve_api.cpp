@@ -291,8 +291,9 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
     int64_t grid, waves = 1;
     if (one_launch) {                         // what can move, dealt to all waves
         const int64_t most = n_req * int64_t(max_blocks);
+        const int64_t fit = int64_t(cus) * resident(tables_lds_bytes(n_req) + kTablesLdsFixed, tune::kMoveBlocksPerCu);
         grid = (most + ids * block_waves - 1) / (ids * block_waves);
-        grid = grid < 1 ? 1 : grid < cap ? grid : cap;
+        grid = grid < 1 ? 1 : grid < fit ? grid : fit;
     } else {                                  // a wave a request, more where requests are few and their lines long
         const int64_t useful = (int64_t(max_blocks) + ids - 1) / ids;
         waves = n_req > 0 ? cap * block_waves / n_req : 1;
@@ -363,7 +364,10 @@ int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int bl
                 return RK_ERR_INVALID_ARGUMENT;
     }
     const int cus = host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus;
-    const int64_t step = int64_t(tune::kSlotBlock) * (16 / ssz), most = int64_t(cus) * tune::kSlotBlocksPerCu;
+    const int64_t step = int64_t(tune::kSlotBlock) * (16 / ssz);
+    const int64_t most = int64_t(cus) * (n_req <= tune::kSlotLdsRequests
+                                          ? resident(slots_lds_bytes(n_req) + kSlotsLdsFixed, tune::kSlotBlocksPerCu)
+                                          : tune::kSlotBlocksPerCu);
     int64_t per = (capacity + most - 1) / most;
     per = (per + step - 1) / step * step;
     per = per < step ? step : per;

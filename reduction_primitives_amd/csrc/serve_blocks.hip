@@ -181,7 +181,7 @@ __device__ __forceinline__ int wave_owner(const uint32_t *off, int req, uint32_t
 // read these.
 __global__ __launch_bounds__(tune::kMoveBlock) void k_tables(TablesArgs a)
 {
-    constexpr int B = tune::kMoveBlock, E = tune::kMoveEach;
+    constexpr int B = tune::kMoveBlock;
     __shared__ uint64_t part[2][B / 64], part_over[B / 64];
     extern __shared__ uint32_t give0[];
     const int req = int(a.req);
@@ -236,40 +236,49 @@ __global__ __launch_bounds__(tune::kMoveBlock) void k_tables(TablesArgs a)
         return a.table[b * a.ts + first[b] + (g - give0[b])];
     };
     const int64_t moves = r.taken + r.given;
-    const int64_t wave = blockIdx.x * (B / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    for (int64_t base = wave * (64 * E); base < moves; base += int64_t(threads) * E) {
-        // the requests that the wave's ids can belong to: takes first, then gives
-        const int64_t end = base + 64 * E < moves ? base + 64 * E : moves;
-        int t_lo = 0, t_hi = 0, g_lo = 0, g_hi = 0;
-        if (base < r.taken) {
-            t_lo = wave_owner(take0, req, uint32_t(base));
-            t_hi = wave_owner(take0, req, uint32_t((end < r.taken ? end : r.taken) - 1)) + 1;
-        }
-        if (end > r.taken) {
-            g_lo = wave_owner(give0, req, uint32_t((base > r.taken ? base : r.taken) - r.taken));
-            g_hi = wave_owner(give0, req, uint32_t(end - 1 - r.taken)) + 1;
-        }
-        int32_t id[E];
-        int32_t *to[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int64_t i = base + 64 * e + lane_id();
-            to[e] = nullptr;
-            if (i < r.taken) {
-                const int b = owner(take0, t_lo, t_hi, uint32_t(i));
-                to[e] = a.table + (b * a.ts + first[b] + (i - take0[b]));
-                id[e] = i < r.there ? a.ring[wrap(r.head + i, a.ring_size)] : given_id(uint32_t(i - r.there), 0, req);
-            } else if (i < end) {
-                const uint32_t g = uint32_t(i - r.taken);
-                to[e] = a.ring + wrap(r.head + r.there + g, a.ring_size);   // (head + there + given <= head + size)
-                id[e] = given_id(g, g_lo, g_hi);
+    const auto deal = [&](auto each) {
+        constexpr int E = decltype(each)::value;
+        const int64_t wave = blockIdx.x * (B / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+        for (int64_t base = wave * (64 * E); base < moves; base += int64_t(threads) * E) {
+            // the requests that the wave's ids can belong to: takes first, then gives
+            const int64_t end = base + 64 * E < moves ? base + 64 * E : moves;
+            int t_lo = 0, t_hi = 0, g_lo = 0, g_hi = 0;
+            if (base < r.taken) {
+                t_lo = wave_owner(take0, req, uint32_t(base));
+                t_hi = wave_owner(take0, req, uint32_t((end < r.taken ? end : r.taken) - 1)) + 1;
             }
-        }
+            if (end > r.taken) {
+                g_lo = wave_owner(give0, req, uint32_t((base > r.taken ? base : r.taken) - r.taken));
+                g_hi = wave_owner(give0, req, uint32_t(end - 1 - r.taken)) + 1;
+            }
+            int32_t id[E];
+            int32_t *to[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (to[e])
-                *to[e] = id[e];
-    }
+            for (int e = 0; e < E; ++e) {
+                const int64_t i = base + 64 * e + lane_id();
+                to[e] = nullptr;
+                if (i < r.taken) {
+                    const int b = owner(take0, t_lo, t_hi, uint32_t(i));
+                    to[e] = a.table + (b * a.ts + first[b] + (i - take0[b]));
+                    id[e] = i < r.there ? a.ring[wrap(r.head + i, a.ring_size)] : given_id(uint32_t(i - r.there), 0, req);
+                } else if (i < end) {
+                    const uint32_t g = uint32_t(i - r.taken);
+                    to[e] = a.ring + wrap(r.head + r.there + g, a.ring_size);   // (head + there + given <= head + size)
+                    id[e] = given_id(g, g_lo, g_hi);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (to[e])
+                    *to[e] = id[e];
+        }
+    };
+    // a step of decoding moves few ids: one a lane, so that all are under way at once; else several,
+    // which share the search for the requests
+    if (moves <= int64_t(threads))
+        deal(std::integral_constant<int, 1>());
+    else
+        deal(std::integral_constant<int, tune::kMoveEach>());
 }
 
 // Two launches, for outputs that are the inputs and for more requests: one
@@ -565,7 +574,7 @@ int run_slots(const SlotLaunch &L)
 {
     const dim3 grid(uint32_t(L.grid)), block(tune::kSlotBlock);
     if (L.a.req <= tune::kSlotLdsRequests) {
-        const size_t lds = (size_t(L.a.req) + 1) * 12;
+        const size_t lds = size_t(slots_lds_bytes(L.a.req));
         if (L.stream_out)
             launch_timed(k_slots<Slot, true, true>, grid, block, lds, L.stream, L.ev_begin, L.ev_end, L.a);
         else
@@ -583,7 +592,7 @@ int launch_tables(const TablesLaunch &L)
 {
     const dim3 grid(uint32_t(L.grid)), block(tune::kMoveBlock);
     if (L.one_launch) {
-        launch_timed(k_tables, grid, block, (size_t(L.a.req) * 3 + 2) * 4, L.stream, L.ev_begin, L.ev_end, L.a);
+        launch_timed(k_tables, grid, block, size_t(tables_lds_bytes(L.a.req)), L.stream, L.ev_begin, L.ev_end, L.a);
     } else {
         if (L.a.req <= 1024)
             launch_timed(k_tables_scan<256>, dim3(1), dim3(256), 0, L.stream, L.ev_begin, L.ev_end, L.a);
