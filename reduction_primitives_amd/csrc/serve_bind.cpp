@@ -35,6 +35,11 @@ struct Refused {};
 
 const char *type_name(at::ScalarType t) { return c10::toString(t); }
 
+struct Buffer {
+    void *at;
+    size_t bytes;
+};
+
 // One call: its name, and the device of its first operand, made the current
 // one for the call.
 struct Call {
@@ -100,6 +105,17 @@ struct Call {
         return t;
     }
 
+    // None: none is needed.
+    Buffer workspace(PyObject *o) const
+    {
+        if (o == Py_None)
+            return Buffer{nullptr, 0};
+        const at::Tensor &t = here("workspace", o);
+        if (!t.is_contiguous())
+            refuse("%s: %s takes a contiguous tensor", name, "workspace");
+        return Buffer{t.data_ptr(), t.nbytes()};
+    }
+
     int prob_code(const char *what, const at::Tensor &t) const
     {
         switch (t.scalar_type()) {
@@ -163,13 +179,11 @@ PyObject *softmax(PyObject *const *a)
     const at::Tensor &out = c.lines("out", a[3]);
     if (out.size(0) != lines || out.size(1) != n)
         refuse("%s: %s takes x's shape and out_dtype", c.name, "out");
-    const at::Tensor &ws = c.here("workspace", a[4]);
-    if (!ws.is_contiguous())
-        refuse("%s: %s takes a contiguous tensor", c.name, "workspace");
+    const Buffer ws = c.workspace(a[4]);
     const int to = c.prob_code("out", out);
     const auto *tp = static_cast<const float *>(c.flat_or_null("temperature", a[2], lines, at::kFloat));
-    return status(p_softmax(in, to, x.data_ptr(), n, lines, x.stride(0), tp, out.data_ptr(), out.stride(0), ws.data_ptr(),
-                            ws.nbytes(), handle(a[0])));
+    return status(p_softmax(in, to, x.data_ptr(), n, lines, x.stride(0), tp, out.data_ptr(), out.stride(0), ws.at,
+                            ws.bytes, handle(a[0])));
 }
 
 PyObject *draft_verify(PyObject *const *a)
@@ -193,9 +207,7 @@ PyObject *draft_verify(PyObject *const *a)
         q = t.data_ptr();
         qs = t.stride(0);
     }
-    const at::Tensor &ws = c.here("workspace", a[10]);
-    if (!ws.is_contiguous())
-        refuse("%s: %s takes a contiguous tensor", c.name, "workspace");
+    const Buffer ws = c.workspace(a[10]);
     const at::ScalarType ids = drafted.scalar_type();
     const auto *xp = c.flat("drafted", a[3], drafts, ids);
     const auto *up = static_cast<const float *>(c.flat("u", a[4], drafts, at::kFloat));
@@ -204,7 +216,7 @@ PyObject *draft_verify(PyObject *const *a)
     auto *tp = c.flat("tokens", a[8], req * (int64_t(max_draft) + 1), ids);
     auto *ap = static_cast<int32_t *>(c.flat("accepted", a[9], req, at::kInt));
     return status(p_draft_verify(code, tok, p.data_ptr(), p.stride(0), q, qs, vocab, req, drafts, max_draft, sp, xp, up, rp,
-                                 tp, ap, ws.data_ptr(), ws.nbytes(), handle(a[0])));
+                                 tp, ap, ws.at, ws.bytes, handle(a[0])));
 }
 
 PyObject *block_tables(PyObject *const *a)
@@ -215,9 +227,7 @@ PyObject *block_tables(PyObject *const *a)
     const at::Tensor &state = c.here("state", a[6]);
     if (state.scalar_type() != at::kLong || !state.is_contiguous() || state.numel() < 2)
         refuse("%s: %s takes int64 head and tail", c.name, "state");
-    const at::Tensor &ws = c.here("workspace", a[9]);
-    if (!ws.is_contiguous())
-        refuse("%s: %s takes a contiguous tensor", c.name, "workspace");
+    const Buffer ws = c.workspace(a[9]);
     const int64_t width = table.size(1);
     if (width > 0x7fffffff)
         return status(RK_ERR_UNSUPPORTED);
@@ -228,7 +238,7 @@ PyObject *block_tables(PyObject *const *a)
     auto *op = static_cast<int32_t *>(c.flat("held_out", a[7], req, at::kInt));
     auto *sp = static_cast<int64_t *>(c.flat("state_out", a[8], 4, at::kLong));
     return status(p_block_tables(lp, req, block, hp, op, static_cast<int32_t *>(table.data_ptr()), table.stride(0), int(width),
-                                 rp, places, static_cast<const int64_t *>(state.data_ptr()), sp, ws.data_ptr(), ws.nbytes(),
+                                 rp, places, static_cast<const int64_t *>(state.data_ptr()), sp, ws.at, ws.bytes,
                                  handle(a[0])));
 }
 

@@ -7,8 +7,7 @@
 // block number i of those it takes comes from place head + T_b + i.  A place
 // at or behind the old tail holds a block given back in this very call: it
 // is read from the giver's table row, never from the ring, so no block waits
-// for another's store.  A wave (or several) moves a request's ids, which lie
-// next to each other in the ring and in the table.
+// for another's store.
 //
 // slot_map.  starts_b, the exclusive sum of the new tokens, is scanned by
 // every block for itself (a few thousand counts cost less than a launch);
@@ -23,7 +22,6 @@ __device__ __forceinline__ int blocks_of(int len, const Divider &d)
 {
     return len > 0 ? int(divide(uint32_t(len - 1), d)) + 1 : 0;
 }
-
 
 // v modulo size (1 <= size < 2^31), not negative.  A 64-bit remainder takes
 // over a hundred instructions, so counters that fit 32 bits do without.
@@ -177,8 +175,8 @@ __device__ __forceinline__ int wave_owner(const uint32_t *off, int req, uint32_t
 // their offsets in LDS; the ids that move are then dealt to the waves in equal
 // shares, whatever requests they belong to.  A wave finds the requests at its
 // ends together, its lanes theirs by bisection between these (bisection among
-// all 2048 took 4 us more).  Only for outputs apart from the inputs: other blocks may still
-// read these.
+// all 2048 took 4 us more).  Only for outputs apart from the inputs: other
+// blocks may still read these.
 __global__ __launch_bounds__(tune::kMoveBlock) void k_tables(TablesArgs a)
 {
     constexpr int B = tune::kMoveBlock;

@@ -44,14 +44,20 @@ def _handle(name, what, t, stream):
 def _empty(shape, dtype, like, stream):
     """A tensor on like's device that belongs to the call's stream, so that the
     caching allocator hands its bytes to no other stream's work too early."""
-    with torch.cuda.device(like.device), (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _workspace(size, args, like, stream):
-    with torch.cuda.device(like.device):
+    """A workspace of size(*args) bytes on like's device, None where that is 0."""
+    if like.get_device() == torch.cuda.current_device():
         n = size(*args)
-    return _empty(max(n, 256), torch.uint8, like, stream)
+    else:
+        with torch.cuda.device(like.device):
+            n = size(*args)
+    return _empty(n, torch.uint8, like, stream) if n else None
 
 
 def _code(name, what, dtype):

@@ -519,6 +519,63 @@ def test_slots_of_no_requests_and_given_outputs():
     assert starts[0] == -5 and (starts[11:] == -5).all()
 
 
+# ------------------------------------------------------- far addresses
+
+def test_lines_past_2_31_elements():
+    """Lines whose places pass 2^31 elements and 2^32 bytes: strides are 64-bit."""
+    rk = _rk()
+    n, far = 40001, (1 << 31) + 77
+    buf = torch.empty(far + n, dtype=BF16, device=DEV)
+    x = (torch.randn(2, n, generator=gen(1)) * 3).to(BF16)
+    view = buf.as_strided((2, n), (far, 1))
+    view.copy_(x)
+    check_softmax(rk.softmax(view, out_dtype=F32), x, [1.0] * 2)
+    short = buf.as_strided((2, 300), (far, 1))
+    check_softmax(rk.softmax(short, out=short), x[:, :300], [1.0] * 2)
+    d = drafts(2, 1, 1, n, BF16, ragged=False)
+    view.copy_(d["p"])
+    on = [d[k].to(DEV) for k in ("q", "drafted", "u", "r")]
+    for u in (0.0, 1.0):                            # the near line, the far one
+        d["u"].fill_(u)
+        on[2].fill_(u)
+        check_verify(d, rk.draft_verify(view, *on))
+    del view, short
+    table = buf.view(torch.int32)[: far // 2 + 9].as_strided((2, 4), (far // 2, 1))
+    table.copy_(torch.tensor([[5, 6, -1, -1], [7, -1, -1, -1]]).int())
+    i = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    lens, held, ring, state = i(16, 64), i(2, 1), i(1, 2, 3, 4, -1), torch.tensor([0, 4, 0, 0])
+    want = ref.block_tables(lens.tolist(), 16, held.tolist(), table.cpu().numpy(), ring.numpy(), [0, 4])
+    dev = [t.to(DEV) for t in (held, ring, state)]
+    rk.block_tables(lens.to(DEV), 16, dev[0], table, dev[1], dev[2])
+    for got, w in zip((dev[0], table, dev[1], dev[2]), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    s = rk.slot_map(lens.to(DEV), i(3, 20).to(DEV), 16, table, dev[0], 100, capacity=23)
+    w = ref.slot_map(lens.tolist(), [3, 20], 16, want[1], want[0], 100, 23)
+    assert all(np.array_equal(g.cpu().numpy(), v) for g, v in zip(s, w))
+
+
+def test_tables_of_many_entries():
+    """A table of over 2^31 entries takes two launches with 64-bit sums."""
+    rk = _rk()
+    req, width = 2100, 1 << 20
+    lens = torch.full((req,), 5, dtype=torch.int32)
+    lens[7], lens[9] = width, 0
+    held = torch.zeros(req, dtype=torch.int32)
+    table = torch.empty(req, width, dtype=torch.int32, device=DEV)
+    size = req + width + 10
+    ring = torch.arange(size, dtype=torch.int32, device=DEV)
+    ho, so = torch.empty_like(held, device=DEV), torch.empty(4, dtype=torch.int64, device=DEV)
+    rk.block_tables(lens.to(DEV), 1, held.to(DEV), table, ring, torch.tensor([0, size], device=DEV), held_out=ho, state_out=so)
+    taken = min(size, int(lens.sum()))
+    assert so.tolist() == [taken, size, int(lens.sum()) - taken, 0]
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), lens.long().cumsum(0)])
+    got = (torch.minimum(off[1:], torch.tensor(size)) - torch.minimum(off[:-1], torch.tensor(size))).int()
+    assert torch.equal(ho.cpu(), got)
+    for b in (0, 7, 8, 10, req - 1):
+        n = int(got[b])
+        assert torch.equal(table[b, :n].cpu(), torch.arange(int(off[b]), int(off[b]) + n, dtype=torch.int32))
+
+
 # ------------------------------------------------------- streams and a whole step
 
 def test_other_stream_and_injected_failure():
