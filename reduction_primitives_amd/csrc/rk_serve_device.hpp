@@ -15,7 +15,14 @@ namespace rk {
 template <int WORDS> struct Words {
     typedef uint32_t T __attribute__((ext_vector_type(WORDS)));
     typedef uint32_t Any __attribute__((ext_vector_type(WORDS), aligned(2)));
-    __device__ __forceinline__ static T load(const void *p) { return *static_cast<const Any *>(p); }
+    template <bool STREAM = false>
+    __device__ __forceinline__ static T load(const void *p)
+    {
+        if constexpr (STREAM)                              // what is read once
+            return __builtin_nontemporal_load(static_cast<const Any *>(p));
+        else
+            return *static_cast<const Any *>(p);
+    }
     template <bool STREAM>
     __device__ __forceinline__ static void store(void *p, T v)
     {

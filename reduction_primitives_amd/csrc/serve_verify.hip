@@ -119,7 +119,9 @@ __device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, con
 // on weigh nothing: a vector that would pass the line's end is read from n - V
 // instead and its first entries, which belong to others, dropped.
 // FAST: the vectors do not pass the line's end, l.x is not among them, and
-// infinities (which weigh nothing) come out as infinities.
+// infinities (which weigh nothing) come out as infinities.  These are the
+// lines' bulk, read once and past the caches (256 x 7 x 131072 f32, captured:
+// 36.7 us without that, 32.9 with).
 template <class In, bool FAST, class S>
 struct Loaded {
     static constexpr int V = InTraits<In>::vec;
@@ -131,9 +133,9 @@ struct Loaded {
     // left: entries of the line after base
     __device__ __forceinline__ void load(const S *lp, const S *lq, int i, int64_t left)
     {
-        p = load16(lp + at(i, left));
+        p = Words<4>::load<FAST>(lp + at(i, left));
         if (lq)
-            q = load16(lq + at(i, left));
+            q = Words<4>::load<FAST>(lq + at(i, left));
     }
 
     // x: l.x after base
