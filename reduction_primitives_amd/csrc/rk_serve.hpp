@@ -35,6 +35,12 @@ constexpr int64_t kSoftStreamBytes = int64_t(32) << 20;
 constexpr int kVerifyBlock = 256;
 constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums at a time
 constexpr int kVerifyBlocksPerCu = 16;    // grid cap = CUs * this (256 x 131072 f32: 8 36.6 us, 16 35.5)
+// Up to a request a CU and this many blocks a CU the last block of a request
+// finishes it; beyond, a second launch does, whose blocks do not wait behind
+// those that still read.  One launch against two, x 131072 f32: 64 requests 12.5 /
+// 13.1 us, 128 19.2 / 19.5, 192 25.0 / 24.6, 256 32.1 / 30.5; bf16: 64 9.8 / 10.7, 128
+// 15.1 / 14.9, 256 26.6 / 22.4; x 32000 f32: 64 8.0 / 9.5, 256 13.1 / 13.4, 384 19.6 / 17.7.
+constexpr int kVerifyFusedBlocksPerCu = 8;
 // ---- block tables and slot maps
 constexpr int kScanBlock = 1024;          // threads of the one block that scans a slot map's many requests
 constexpr int kMoveBlock = 256;           // threads of the blocks that move block ids
@@ -125,7 +131,7 @@ struct VerifyPlan {
     int chunks = 0;           // blocks of a line
     int64_t grid = 0;
     int launches = 0;
-    bool fused_ok = false;    // the arrival counters of all requests fit a slot
+    bool fused_ok = false;    // the last block of a request finishes it
     size_t ws_bytes = 0;
 };
 

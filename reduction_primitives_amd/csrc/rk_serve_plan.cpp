@@ -63,14 +63,16 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
     constexpr int waves = tune::kVerifyBlock / 64;
     p->tiles = (n + tune::kVerifyTile - 1) / tune::kVerifyTile;
     // a wave a tile while the blocks fit the chip at once; beyond that, more tiles a wave
-    const int64_t most = int64_t(cus > 0 ? cus : tune::kDefaultCus) * tune::kVerifyBlocksPerCu;
+    cus = cus > 0 ? cus : tune::kDefaultCus;
+    const int64_t most = int64_t(cus) * tune::kVerifyBlocksPerCu;
     int64_t chunks = (p->tiles + waves - 1) / waves, fit = req > 0 ? most / req : chunks;
     fit = fit < 1 ? 1 : fit;
     p->chunks = int(chunks < fit ? chunks : fit);
     p->grid = req * p->chunks;
     if (p->grid > kMaxThreads / tune::kVerifyBlock)
         return ST_UNSUPPORTED;
-    p->fused_ok = req * arrive_counters(p->chunks) <= kArriveCapacity;
+    p->fused_ok = req * arrive_counters(p->chunks) <= kArriveCapacity && req <= cus &&
+                  p->grid <= int64_t(cus) * tune::kVerifyFusedBlocksPerCu;
     p->launches = req == 0 ? 0 : p->chunks == 1 || p->fused_ok ? 1 : 2;
     p->ws_bytes = round_up_256(size_t(req) * size_t(p->tiles) * 8);
     return ST_OK;

@@ -144,6 +144,9 @@ def test_plans():
     assert p.kernel == rk.RK_KERNEL_DRAFT_VERIFY and p.launches == 1
     assert p.workspace_bytes >= 64 * -(-131072 // p.tile_outputs) * 8
     assert rk.rk_plan_draft_verify(0, 131072, 5000, 256).split == 1         # a block a request fills the chip
+    assert rk.rk_plan_draft_verify(0, 131072, 256, 256).launches == 2       # many blocks: finished apart
+    assert rk.rk_plan_draft_verify(0, 32000, 257, 256).launches == 2        # many requests
+    assert rk.rk_plan_draft_verify(0, 32000, 256, 256).launches == 1
     assert rk.rk_plan_draft_verify(0, 100, 1, 256).split == 1
     prev = rk.rk_debug_set_fused_finish(0)
     try:
