@@ -135,6 +135,13 @@ struct VerifyPlan {
     size_t ws_bytes = 0;
 };
 
+// What is known of a request once its kept drafts are.
+struct VerifyDrawn {
+    int64_t lo;               // its first draft
+    int64_t x;                // the token turned down (-1: none)
+    int count, kept;          // its drafts, and how many are kept
+};
+
 struct VerifyArgs {
     const void *p, *q;        // q NULL: drafts without probabilities
     int64_t ps, qs;           // line strides
@@ -147,6 +154,7 @@ struct VerifyArgs {
     void *tokens;
     int32_t *accepted;
     double *sums;             // [req][tiles]
+    VerifyDrawn *drawn;       // [req], for a second launch
     int64_t tiles;
     int chunks;
     int slot;                 // >= 0: the last block of a request finishes it

@@ -233,6 +233,7 @@ int rk_draft_verify(int prob_dtype, int token_dtype, const void *p, int64_t p_st
     L.a.tokens = tokens;
     L.a.accepted = accepted;
     L.a.sums = static_cast<double *>(workspace);
+    L.a.drawn = reinterpret_cast<VerifyDrawn *>(L.a.sums + n_req * pl.tiles);
     L.a.tiles = pl.tiles;
     L.a.chunks = pl.chunks;
     // A captured call takes the second launch: it then shares no counters

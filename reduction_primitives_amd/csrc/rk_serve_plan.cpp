@@ -74,7 +74,7 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
     p->fused_ok = req * arrive_counters(p->chunks) <= kArriveCapacity && req <= cus &&
                   p->grid <= int64_t(cus) * tune::kVerifyFusedBlocksPerCu;
     p->launches = req == 0 ? 0 : p->chunks == 1 || p->fused_ok ? 1 : 2;
-    p->ws_bytes = round_up_256(size_t(req) * size_t(p->tiles) * 8);
+    p->ws_bytes = round_up_256(size_t(req) * (size_t(p->tiles) * 8 + sizeof(VerifyDrawn)));
     return ST_OK;
 }
 

@@ -43,18 +43,11 @@ __device__ __forceinline__ T wave_uniform(T v)
     return move_words(v, [](uint32_t w) { return uint32_t(__builtin_amdgcn_readfirstlane(int(w))); });
 }
 
-// What the whole block knows of its request.
-struct Drawn {
-    int64_t lo;               // its first draft
-    int count, kept;          // its drafts, and how many are kept
-    int64_t x;                // the token turned down (-1: none)
-};
-
 template <class In, class Tok>
-__device__ __forceinline__ Drawn accept(const VerifyArgs &a, int64_t b)
+__device__ __forceinline__ VerifyDrawn accept(const VerifyArgs &a, int64_t b)
 {
     using S = typename InTraits<In>::S;
-    Drawn d;
+    VerifyDrawn d;
     int64_t lo = b * a.max_draft, hi = lo + a.max_draft;
     if (a.starts) {
         lo = a.starts[b];
@@ -104,7 +97,7 @@ template <class S> struct Lines {
 };
 
 template <class S>
-__device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, const Drawn &d)
+__device__ __forceinline__ Lines<S> lines_of(const VerifyArgs &a, int64_t b, const VerifyDrawn &d)
 {
     Lines<S> l;
     l.p = static_cast<const S *>(a.p) + (d.lo + d.kept + b) * a.ps;
@@ -362,7 +355,7 @@ __device__ __forceinline__ void sum_tiles(const VerifyArgs &a, int64_t b, const 
 
 // Draws the request's next token.
 template <class In, class Tok>
-__device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Drawn &d)
+__device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const VerifyDrawn &d)
 {
     using S = typename InTraits<In>::S;
     Lines<S> l = lines_of<S>(a, b, d);
@@ -383,7 +376,7 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Dra
 // What is known before the next token is: the kept tokens, how many they are,
 // and -1 behind the next one.
 template <class Tok>
-__device__ __forceinline__ void write_kept(const VerifyArgs &a, int64_t b, const Drawn &d)
+__device__ __forceinline__ void write_kept(const VerifyArgs &a, int64_t b, const VerifyDrawn &d)
 {
     Tok *out = static_cast<Tok *>(a.tokens) + b * (int64_t(a.max_draft) + 1);
     for (int i = int(threadIdx.x); i <= a.max_draft; i += kB)
@@ -399,10 +392,13 @@ __global__ __launch_bounds__(kB) void k_verify(VerifyArgs a)
     using S = typename InTraits<In>::S;
     const int64_t b = blockIdx.x / uint32_t(a.chunks);
     const int c = int(blockIdx.x % uint32_t(a.chunks));
-    const Drawn d = accept<In, Tok>(a, b);
+    const VerifyDrawn d = accept<In, Tok>(a, b);
     const Lines<S> l = lines_of<S>(a, b, d);
-    if (c == 0)
+    if (c == 0) {
         write_kept<Tok>(a, b, d);
+        if (a.slot < 0 && threadIdx.x == 0)
+            a.drawn[b] = d;                   // for the second launch
+    }
     sum_tiles<In, true>(a, b, l, int64_t(c) * (kB / 64), int64_t(a.chunks) * (kB / 64));
     if (a.chunks > 1) {
         if (a.slot < 0)
@@ -421,7 +417,7 @@ template <class In, class Tok>
 __global__ __launch_bounds__(kB) void k_verify_finish(VerifyArgs a)
 {
     const int64_t b = blockIdx.x;
-    finish<In, Tok>(a, b, accept<In, Tok>(a, b));
+    finish<In, Tok>(a, b, a.drawn[b]);
 }
 
 template <class In, class Tok>
