@@ -13,14 +13,14 @@ namespace tune {
 // ---- softmax of lines
 // A line of up to kSoftLanes * kSoftPer entries is one block's (a wave's up to
 // 64 * kSoftPer), in one launch; longer ones are split over two.  Measured,
-// one block against split: 5 x 8192 f32 3.4 / 4.9 us, 512 x 8192 8.3 / 10.9,
-// 128 x 20000 6.6 / 9.3, 512 x 32768 bf16 19.5 / 20.8, 5 x 32768 5.5 / 5.2;
+// one block against split: 5 x 8192 f32 3.4 / 5.2 us, 512 x 8192 8.2 / 11.1,
+// 128 x 20000 6.5 / 9.5, 512 x 32768 bf16 to f32 20.0 / 21.4, 5 x 32768 5.5 / 5.4;
 // with 64 entries a thread 5 x 65536 took 10.9 us against 5.4.
 constexpr int kSoftPer = 32;              // entries a thread holds of a line kept in registers
 constexpr int kSoftLanes = 1024;          // most threads that share such a line
 constexpr int kSoftBlock = 256;           // threads of a split line's blocks
 // Entries of a wave's tile of a split line.  4096: 5 x 131072 f32 6.7 us,
-// 320 x 131072 bf16 to f32 49.2; 2048: 5.6, 49.1; 1024: 5.6, 49.8.
+// 320 x 131072 bf16 to f32 49.1; 2048: 5.7, 50.6; 1024: 5.6, 50.5.
 constexpr int kSoftTile = 2048;
 // Every wave of the writing launch folds its line's statistics, 64 tiles at a
 // time, for itself; past this many tiles (a million entries) a launch between
@@ -28,13 +28,13 @@ constexpr int kSoftTile = 2048;
 constexpr int kSoftFoldTiles = 512;
 // Outputs beyond the eight L2s together (32 MB) are stored past the caches, so
 // the input stays there for its second reading: 320 x 131072 bf16 to f32 (168
-// MB out) 60.2 us with plain stores, 48.4 us with streaming ones.  Smaller
+// MB out) 59.5 us with plain stores, 48.2 us with streaming ones.  Smaller
 // ones stay cached for whoever reads the probabilities next.
 constexpr int64_t kSoftStreamBytes = int64_t(32) << 20;
 // ---- draft verification
 constexpr int kVerifyBlock = 256;
 constexpr int kVerifyTile = 2048;         // vocabulary entries one wave sums at a time
-constexpr int kVerifyBlocksPerCu = 16;    // grid cap = CUs * this (256 x 131072 f32: 8 36.6 us, 16 35.5)
+constexpr int kVerifyBlocksPerCu = 16;    // grid cap = CUs * this (256 x 131072 f32: 8 34.7 us, 16 and 32 32.7)
 // Up to a request a CU and this many blocks a CU the last block of a request
 // finishes it; beyond, a second launch does, whose blocks do not wait behind
 // those that still read.  One launch against two, x 131072 f32: 64 requests 12.5 /
@@ -62,7 +62,7 @@ constexpr int kSlotLdsRequests = 4096;
 constexpr int kSlotBlocksPerCu = 8;       // grid cap = CUs * this, or what their LDS lets run at once
 constexpr int kLdsBytes = 160 << 10;      // of a CU
 // Outputs beyond the eight L2s together are stored past the caches (3.1M tokens,
-// 50 MB: 13.7 us with plain stores, 12.1 us without); smaller ones stay there
+// 50 MB: 11.9 us with plain stores, 11.1 us without); smaller ones stay there
 // for the kernels that write the cache.
 constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
 }  // namespace tune
