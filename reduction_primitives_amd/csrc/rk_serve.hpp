@@ -18,6 +18,10 @@ namespace tune {
 // with 64 entries a thread 5 x 65536 took 10.9 us against 5.4.
 constexpr int kSoftPer = 32;              // entries a thread holds of a line kept in registers
 constexpr int kSoftLanes = 1024;          // most threads that share such a line
+// Lines of up to this many entries share a wave, 16 lanes each.  Against a wave
+// a line: 5 x 64 f32 2.2 / 2.4 us, 16384 x 64 3.4 / 6.7, 100000 x 64 10.2 / 28.8, x 256 38.1 /
+// 40.0 (bf16 19.0 / 33.3), x 512 74.1 / 71.0, 5 x 512 2.8 / 2.5.
+constexpr int kSoftRowEntries = 256;
 constexpr int kSoftBlock = 256;           // threads of a split line's blocks
 // Entries of a wave's tile of a split line.  4096: 5 x 131072 f32 6.7 us,
 // 320 x 131072 bf16 to f32 49.1; 2048: 5.7, 50.6; 1024: 5.6, 50.5.

@@ -30,9 +30,9 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
     p->launches = 1;
     p->kernel = VK_SOFT_LINE;
     if (n <= 64 * tune::kSoftPer) {
-        p->lanes = 64;
+        p->lanes = n <= tune::kSoftRowEntries ? 16 : 64;
         p->block = 256;
-        p->grid = (lines + 3) / 4;
+        p->grid = (lines + 256 / p->lanes - 1) / (256 / p->lanes);
     } else if (n <= tune::kSoftLanes * tune::kSoftPer) {
         p->lanes = 256;
         while (p->lanes * tune::kSoftPer < n)

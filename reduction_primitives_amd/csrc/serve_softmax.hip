@@ -2,8 +2,8 @@
 //
 //   p_i = exp((x_i - m) / t) / s,   m = max_j x_j,   s = sum_j exp((x_j - m) / t)
 //
-// Two forms.  A line of up to 32 entries a thread of one block (a wave for the
-// shortest, 1024 threads for the longest) is read once, kept in registers, and
+// Two forms.  A line of up to 32 entries a thread of one block (a quarter of a
+// wave for the shortest, 1024 threads for the longest) is read once, kept in registers, and
 // written: one launch, each byte moved once.  Of a longer one the first launch
 // leaves every tile's largest entry m_c and s_c = sum exp((x_j - m_c) / t), a
 // tile a wave, with no barrier between the waves; the second folds them,
@@ -93,13 +93,20 @@ __device__ __forceinline__ T wave_reduce_rows(T v)
     return v;
 }
 
-// Reduction over the LANES threads that share a line: a wave, or a block whose
-// waves meet in LDS (`part`, one value a wave, a buffer of its own per use).
+// Reduction over the LANES threads that share a line: a quarter of a wave, a
+// wave, or a block whose waves meet in LDS (`part`, one value a wave, a buffer of its own per use).
 template <class Op, int LANES, class T>
 __device__ __forceinline__ T line_all(T v, T *part)
 {
     constexpr int NW = LANES / 64;
-    v = wave_reduce<Op>(v);
+    if constexpr (LANES == 16) {              // a DPP row: no lane of another line takes part
+        v = Op::apply(v, dpp_move<kDppQuadXor1>(v));
+        v = Op::apply(v, dpp_move<kDppQuadXor2>(v));
+        v = Op::apply(v, dpp_move<kDppRowHalfMirror>(v));
+        v = Op::apply(v, dpp_move<kDppRowMirror>(v));
+    } else {
+        v = wave_reduce<Op>(v);
+    }
     if constexpr (NW > 1) {
         if (lane_id() == 0)
             part[threadIdx.x >> 6] = v;
@@ -288,12 +295,14 @@ __global__ __launch_bounds__(BLOCK) void k_soft_line(SoftmaxArgs a)
     constexpr int V = vec_of<In, Out>(), U = tune::kSoftPer / V;
     using P = Piece<In, V, LANES, U, false>;
     using O = typename OutTraits<Out>::S;
-    __shared__ float part[2][LANES / 64];
-    __shared__ int parti[LANES / 64];
+    constexpr int NW = LANES > 64 ? LANES / 64 : 1;
+    __shared__ float part[2][NW];
+    __shared__ int parti[NW];
+    const int in_block = int(threadIdx.x / LANES);
     const int64_t line = int64_t(blockIdx.x) * (BLOCK / LANES) +
-                         __builtin_amdgcn_readfirstlane(int(threadIdx.x / LANES));
+                         (LANES < 64 ? in_block : __builtin_amdgcn_readfirstlane(in_block));
     if (line >= a.lines)
-        return;                               // (whole waves, and only where LANES = 64: no barrier is missed)
+        return;                               // (all of a line's lanes, and only where LANES <= 64: no barrier is missed)
     const float t = a.t ? a.t[line] : 1.0f;
     P p;
     p.load(static_cast<const typename P::S *>(a.x) + line * a.xs, int(a.n), int(threadIdx.x % LANES));
@@ -512,6 +521,7 @@ int run_softmax(const SoftmaxLaunch &L)
 {
     if (L.plan.kernel == VK_SOFT_LINE) {
         switch (L.plan.lanes) {
+        case 16: launch_line<In, Out, 16, 256>(L); break;
         case 64: launch_line<In, Out, 64, 256>(L); break;
         case 256: launch_line<In, Out, 256, 256>(L); break;
         case 512: launch_line<In, Out, 512, 512>(L); break;

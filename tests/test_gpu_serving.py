@@ -51,7 +51,7 @@ def check_softmax(got, x, t):
             assert np.array_equal(got64[i], want[i], equal_nan=True)
 
 
-SOFT_N = [1, 2, 7, 8, 63, 65, 257, 511, 2047, 2048, 2049, 4097, 8191, 8192, 8193, 16383, 16385, 32767, 32768, 32769, 50001, 65536, 65537, 131072, 200003]
+SOFT_N = [1, 2, 7, 8, 63, 65, 255, 256, 257, 511, 2047, 2048, 2049, 4097, 8191, 8192, 8193, 16383, 16385, 32767, 32768, 32769, 50001, 65536, 65537, 131072, 200003]
 
 
 @pytest.mark.parametrize("n", SOFT_N)
@@ -66,14 +66,14 @@ def test_softmax_sizes(n, din, dout):
     check_softmax(got, x, t)
 
 
-@pytest.mark.parametrize("lines,n", [(1, 1), (1, 131072), (2, 50000), (64, 300), (700, 33), (513, 4097), (300, 9000), (260, 20000)])
+@pytest.mark.parametrize("lines,n", [(1, 1), (17, 256), (63, 255), (1001, 16), (130, 257), (1, 131072), (2, 50000), (64, 300), (700, 33), (513, 4097), (300, 9000), (260, 20000)])
 def test_softmax_line_counts(lines, n):
     rk = _rk()
     x = torch.randn(lines, n, generator=gen(lines)) * 2
     check_softmax(rk.softmax(x.to(DEV)), x, [1.0] * lines)
 
 
-@pytest.mark.parametrize("n", [5, 1000, 9001, 40000, 140001])
+@pytest.mark.parametrize("n", [5, 200, 1000, 9001, 40000, 140001])
 @pytest.mark.parametrize("dt", [F32, F16, BF16])
 def test_softmax_masks_and_odd_values(n, dt):
     rk = _rk()
