@@ -799,3 +799,37 @@ def test_captured_steps():
         eager.run()
         torch.cuda.synchronize()
         eager.check(w)
+
+
+def test_two_threads_on_two_streams():
+    """Steps of two host threads at once, each on a stream of its own: calls of
+    different streams share no counters, and no workspace here."""
+    import threading
+    steps = [Step(req=40, k=3, n=20011, block=16, width=30, seed=4), Step(req=33, k=5, n=33333, block=8, width=30, seed=5)]
+    failed = []
+
+    def work(s, seed):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(6):
+                    s.inputs(seed + i)
+                    torch.cuda.current_stream().synchronize()
+                    was = s.cpu()
+                    first = None
+                    for _ in range(20):                # the same verification again and again, beside the other thread's
+                        t, a = _rk().draft_verify(s.p, s.q, s.drafted, s.u, s.r, workspace=s.ws[1])
+                        first = (t, a) if first is None else first
+                        if not (torch.equal(t, first[0]) and torch.equal(a, first[1])):
+                            failed.append("results differ")
+                    s.run()
+                    torch.cuda.current_stream().synchronize()
+                    s.check(was)
+        except BaseException as e:                     # noqa: BLE001  (shown by the test's own thread)
+            failed.append(repr(e))
+    threads = [threading.Thread(target=work, args=(s, 100 * i)) for i, s in enumerate(steps)]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
