@@ -71,7 +71,7 @@ constexpr int kLdsBytes = 160 << 10;      // of a CU
 constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
 }  // namespace tune
 
-enum ServeKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2, VK_VERIFY = 3 };
+enum SoftmaxKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2 };
 
 // Division of 0 <= x < 2^31 by d >= 1 as a multiplication: with l the bits
 // of d - 1 and m = floor(2^(31+l) / d) + 1, x / d = (x * m) >> (31 + l).

@@ -24,7 +24,9 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
         return ST_UNSUPPORTED;
     if (n > kMaxLine || lines > kMaxLines)
         return ST_UNSUPPORTED;
-    p->vec = 16 / dtype_size(in_dtype);
+    // 16 bytes of the wider type (the first launch of a split line reads 16 bytes of input)
+    const int in_vec = 16 / dtype_size(in_dtype), out_vec = 16 / dtype_size(out_dtype);
+    p->vec = in_vec < out_vec ? in_vec : out_vec;
     if (n == 0 || lines == 0)
         return ST_OK;
     p->launches = 1;
@@ -42,6 +44,7 @@ int plan_softmax(int in_dtype, int out_dtype, int64_t n, int64_t lines, SoftmaxP
     } else {
         constexpr int waves = tune::kSoftBlock / 64;
         p->kernel = VK_SOFT_SPLIT;
+        p->vec = in_vec;
         p->block = tune::kSoftBlock;
         p->chunks = int((n + tune::kSoftTile - 1) / tune::kSoftTile);
         p->grid = lines * ((p->chunks + waves - 1) / waves);

@@ -157,6 +157,17 @@ def test_plans():
     assert rk.rk_block_tables_workspace_size(0) > 0
 
 
+def test_softmax_plans_name_the_loads():
+    """Elements of a load in the first launch: 16 bytes of the wider type where
+    it writes too, of the input where it only reads."""
+    rk = _rk()
+    f32, f16 = rk.RK_F32, rk.RK_F16
+    for n, loads in ((1000, {(f32, f32): 4, (f16, f32): 4, (f32, f16): 4, (f16, f16): 8}),
+                     (50000, {(f32, f32): 4, (f16, f32): 8, (f32, f16): 4, (f16, f16): 8})):
+        for (din, dout), vec in loads.items():
+            assert rk.rk_plan_softmax(din, dout, n, 3).vec == vec
+
+
 def test_plain_forms():
     """The plain forms themselves, on values worked out by hand."""
     p = np.array([[0.5, 0.25, 0.25, 0.0]] * 3)
