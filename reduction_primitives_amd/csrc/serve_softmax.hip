@@ -33,20 +33,25 @@ __device__ __forceinline__ float scale_of(float t)
 // exp((x - m) / t).  v_exp_f32 is good to 1 ulp and its argument is rounded
 // three times with the factor's own, an error of 3 |argument| 2^-24 in the
 // result.  With m finite and a factor above 0 a masked entry gives 0 by
-// itself, as -inf's power of two; GUARD sets it to 0 where that fails.
+// itself, as -inf's power of two; GUARD sets it to 0 where that fails, and
+// halves the two before it subtracts them: x - m passes the largest float
+// where m is beyond half its last place, which a large t makes up for.
 template <bool GUARD>
 __device__ __forceinline__ float soft_term(float x, float m, float c)
 {
-    const float e = __builtin_amdgcn_exp2f((x - m) * c);
-    if constexpr (GUARD)
+    if constexpr (GUARD) {
+        const float e = __builtin_amdgcn_exp2f((x * 0.5f - m * 0.5f) * c * 2.0f);
         return x == -std::numeric_limits<float>::infinity() ? 0.0f : e;
-    else
-        return e;
+    } else {
+        return __builtin_amdgcn_exp2f((x - m) * c);
+    }
 }
+
+constexpr float kHalfLastPlace = 0x1p103f;    // of the largest float
 
 __device__ __forceinline__ bool needs_guard(float m, float c)
 {
-    return !(m > -std::numeric_limits<float>::infinity() && c > 0.0f);
+    return !(m > -std::numeric_limits<float>::infinity() && m < kHalfLastPlace && c > 0.0f);
 }
 
 // Outputs: rounded to nearest even by gfx950's own conversions.

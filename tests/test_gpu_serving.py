@@ -104,6 +104,22 @@ def test_softmax_masks_and_odd_values(n, dt):
     assert got[9, 0] == 1
 
 
+@pytest.mark.parametrize("n", [5, 200, 1000, 9001, 40000, 140001])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_softmax_differences_past_the_largest_float(n, dt):
+    """x - m is -inf in float32, (x - m) / t is not."""
+    rk = _rk()
+    low, high = torch.finfo(dt).min, torch.finfo(dt).max
+    t = [INF, 2.0 ** 127, 2.0 ** 124, 1.0, INF]
+    x = torch.zeros(len(t), n, dtype=dt)
+    x[:, ::2] = low
+    x[:, n // 2] = high
+    x[:, n - 1] = low
+    x[4, 1] = -INF
+    check_softmax(rk.softmax(x.to(DEV), temperature=torch.tensor(t).to(DEV)), x, t)
+    check_softmax(rk.softmax(x.to(DEV), temperature=torch.tensor(t).to(DEV), out_dtype=F32), x, t)
+
+
 @pytest.mark.parametrize("n", [77, 8200, 33333, 70003])
 @pytest.mark.parametrize("din,dout", [(F32, F32), (F16, F32), (BF16, BF16), (F32, F16)])
 @pytest.mark.parametrize("offset,pad", [(1, 0), (3, 5), (0, 24)])
