@@ -448,7 +448,7 @@ typedef enum {
                                    transposed or permuted view): tiles of lines x scan positions
                                    staged through LDS, look-back along the scan dim (+ a clearing
                                    launch) */
-    RK_KERNEL_SOFTMAX_LINE = 14, /* softmax: a line in the registers of a wave or a block, one launch */
+    RK_KERNEL_SOFTMAX_LINE = 14, /* softmax: a line in the registers of a quarter wave, a wave or a block, one launch */
     RK_KERNEL_SOFTMAX_SPLIT = 15, /* softmax: tiles of a line, statistics first, then the line (two launches) */
     RK_KERNEL_DRAFT_VERIFY = 16   /* draft verification: a wave per tile of a request's line */
 } rk_kernel;
