@@ -364,6 +364,9 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, int64_t b, const Ver
     const double *sums = a.sums + b * a.tiles;
     int64_t token = find<In>(l, a.n, sums, a.tiles, r);
     if (token < 0 && (l.q || l.x >= 0)) {     // the draft leaves nothing of the target: draw from the target
+        // All waves have read the same sums, so all are here or none.  Each has read them for itself,
+        // and none may still be doing so when they are written anew.
+        __syncthreads();
         l.q = nullptr;
         l.x = -1;
         sum_tiles<In, false>(a, b, l, 0, kB / 64);
