@@ -84,6 +84,21 @@ struct Divider {
 };
 Divider make_divider(uint32_t d);
 
+// The last i of [lo, hi) with start(i) <= t, where start does not fall and
+// start(lo) <= t.  (lo + hi passes 2^31 from 2^30 requests on.)
+template <class Start>
+constexpr int last_start(const Start &start, int lo, int hi, int64_t t)
+{
+    while (hi - lo > 1) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (start(mid) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
 // Blocks of `lds` bytes that a CU runs at once, at most `most`.
 constexpr int64_t resident(int64_t lds, int64_t most)
 {

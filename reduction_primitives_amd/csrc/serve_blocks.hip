@@ -484,7 +484,7 @@ __global__ __launch_bounds__(tune::kSlotBlock) void k_slots(SlotArgs a)
     const int req = int(a.req);
     const int64_t from = int64_t(blockIdx.x) * a.per_block;
     const int64_t to = from + a.per_block < a.capacity ? from + a.per_block : a.capacity;
-    const Kept kept{lds, reinterpret_cast<int32_t *>(lds + req + 1), reinterpret_cast<int32_t *>(lds + 2 * (req + 1))};
+    const Kept kept{lds, reinterpret_cast<int32_t *>(lds + req + 1), reinterpret_cast<int32_t *>(lds + 2 * (a.req + 1))};
     if (threadIdx.x == 0) {
         s_lo = 0;
         s_hi = req - 1;
@@ -502,17 +502,7 @@ __global__ __launch_bounds__(tune::kSlotBlock) void k_slots(SlotArgs a)
         Slot slot[T];
         int pos[T], who[T], off[T];
         int32_t id[T];
-        int b = s0;
-        if (t < total) {                      // start(lo) <= t < start(hi)
-            int hi = s1;
-            while (hi - b > 1) {
-                const int mid = (b + hi) >> 1;
-                if (start(mid) <= t)
-                    b = mid;
-                else
-                    hi = mid;
-            }
-        }
+        int b = t < total ? last_start(start, s0, s1, t) : s0;    // start(s0) <= t < start(s1)
         int64_t begin = start(b), end = t < total ? start(b + 1) : begin;
 #pragma unroll
         for (int k = 0; k < T; ++k) {

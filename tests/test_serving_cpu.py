@@ -225,3 +225,39 @@ int main() {
                     os.path.join(csrc, "rk_serve_plan.cpp"), os.path.join(csrc, "rk_plan.cpp"), "-o", exe], check=True)
     run = subprocess.run([exe], capture_output=True, text=True, timeout=100)
     assert run.returncode == 0, run.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_slot_map_search_stays_in_range(tmp_path):
+    """The search for a token's request among as many requests as rk_slot_map
+    takes: only places of the range are looked at, and the last request that
+    begins at or before the token is found, empty ones before it passed by."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "reduction_primitives_amd", "csrc")
+    src = tmp_path / "s.cpp"
+    src.write_text('''
+#include "rk_serve.hpp"
+#include <cstdio>
+#include <cstdlib>
+#include <initializer_list>
+int main() {
+    const int sizes[] = {1, 2, 3, 4097, 1 << 30, (1 << 30) + 1, 0x7ffffffe};
+    for (int req : sizes)
+        for (int empty : {1, 3})              // of every `empty` requests all but the last have no token
+            for (int64_t t = 0; t < req / empty; t = t < 5 || t > req / empty - 9 ? t + 1 : t + (req / empty - 8 - t + 1) / 2) {
+                const auto start = [&](int i) {
+                    if (i < 0 || i >= req) { std::printf("looked at %d of %d\\n", i, req); std::exit(1); }
+                    return int64_t(i) / empty;
+                };
+                const int b = rk::last_start(start, 0, req, t);
+                const int64_t want = (t + 1) * empty - 1;
+                if (b != (want < req ? want : req - 1)) { std::printf("%lld of %d: %d\\n", (long long)t, req, b); return 1; }
+            }
+    return 0;
+}
+''')
+    exe = str(tmp_path / "s")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I" + csrc, str(src),
+                    "-o", exe], check=True)
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0, run.stdout + run.stderr
