@@ -60,3 +60,35 @@ def test_verify_draws_from_the_target_where_the_draft_leaves_nothing(req, n, dt,
         check_spread(d, at, run_verify(big))
     finally:
         rk.rk_debug_set_fused_finish(prev)
+
+
+def verify_paths(req, n):
+    """(blocks a request, tiles, launches with the fused finish and without)."""
+    rk = _rk()
+    plan = rk.rk_plan_draft_verify(rk.RK_F32, n, req)
+    prev = rk.rk_debug_set_fused_finish(0)
+    try:
+        apart = rk.rk_plan_draft_verify(rk.RK_F32, n, req).launches
+    finally:
+        rk.rk_debug_set_fused_finish(prev)
+    return plan.split, -(-n // plan.tile_outputs), plan.launches, apart
+
+
+@pytest.mark.parametrize("req,n,paths", [
+    (64, 9000, (2, 5, 1, 2)), (250, 9000, (2, 5, 1, 2)), (20, 40001, (5, 20, 1, 2)),    # the last block finishes, or a second launch
+    (1, 100000, (13, 49, 1, 2)),
+    (600, 9000, (2, 5, 2, 2)), (256, 70001, (9, 35, 2, 2)),                             # a second launch by itself
+    (4200, 8200, (1, 5, 1, 1)),                                                         # one block, a wave with two tiles
+    (1500, 18001, (2, 9, 2, 2)), (900, 33000, (4, 17, 2, 2)),                           # several blocks, the same
+])
+def test_verify_launch_paths(req, n, paths):
+    rk = _rk()
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert verify_paths(req, n) == paths
+    d, big, at = spread_drafts(req * 7 + n, req, 2, n, False, m=80 if req > 1000 else 400)
+    check_spread(d, at, run_verify(big))
+    prev = rk.rk_debug_set_fused_finish(0)
+    try:
+        check_spread(d, at, run_verify(big))
+    finally:
+        rk.rk_debug_set_fused_finish(prev)
