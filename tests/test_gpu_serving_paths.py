@@ -92,3 +92,83 @@ def test_verify_launch_paths(req, n, paths):
         check_spread(d, at, run_verify(big))
     finally:
         rk.rk_debug_set_fused_finish(prev)
+
+
+# ------------------------------------------------------------------ slot maps
+
+def slots_of(lens, fresh, block, table, held, n_blocks, capacity):
+    """The plain slot map of valid inputs, all tokens at once."""
+    lens, fresh, table, held = (t.numpy().astype(np.int64) for t in (lens, fresh, table, held))
+    starts = np.concatenate([[0], fresh.cumsum()])
+    total = min(int(starts[-1]), capacity)
+    who = np.repeat(np.arange(len(lens)), fresh)[:total]
+    pos = (lens - fresh)[who] + np.arange(total) - starts[who]
+    j = pos // block
+    entry = table[who, np.minimum(j, table.shape[1] - 1)]
+    there = (j < held[who]) & (j < table.shape[1]) & (entry >= 0) & (entry < n_blocks)
+    slots, positions, requests = (np.full(capacity, v, np.int64) for v in (-1, 0, -1))
+    slots[:total], positions[:total], requests[:total] = np.where(there, entry * block + pos % block, -1), pos, who
+    return slots, positions, requests, starts
+
+
+def prompts(seed, req, tokens, block, spare):
+    """A batch of at least `tokens` new tokens, every 50th request without any
+    and some table entries that name no block."""
+    g = gen(seed)
+    mean = tokens // req
+    fresh = torch.randint(mean // 2, 2 * mean + 2, (req,), generator=g)
+    fresh[::50] = 0
+    lens = fresh + torch.randint(0, 70, (req,), generator=g)
+    width = -(-int(lens.max()) // block)
+    table = torch.randint(-1, req * width, (req, width), generator=g)
+    held = (lens + block - 1) // block - (torch.rand(req, generator=g) < 0.1).long()
+    n_blocks = req * width - 5
+    cap = int(fresh.sum()) + spare
+    assert cap > tokens
+    return lens.int(), fresh.int(), block, table.int(), held.clamp(min=0).int(), n_blocks, cap
+
+
+@pytest.mark.parametrize("req", [70, 4096, 4097, 9001])
+@pytest.mark.parametrize("dtype,tokens", [(torch.int64, 2_200_000), (torch.int32, 2_900_000)])
+def test_slots_past_the_caches(req, dtype, tokens):
+    """Outputs of more than 32 MB, at any element, behind which nothing is
+    written, ended inside a vector."""
+    rk = _rk()
+    lens, fresh, block, table, held, n_blocks, cap = prompts(req, req, tokens, 16, 1001)
+    cap += 1 - cap % 2
+    size = torch.empty(0, dtype=dtype).element_size()
+    assert cap * (size + 8) > 32 << 20
+    bufs = [torch.full((cap + 9,), -5, dtype=t, device=DEV) for t in (dtype, torch.int32, torch.int32)]
+    at = (1, 3, 2)
+    slots, positions, requests = (b[i:i + cap] for b, i in zip(bufs, at))
+    got = rk.slot_map(lens.to(DEV), fresh.to(DEV), block, table.to(DEV), held.to(DEV), n_blocks, slots=slots,
+                      positions=positions, requests=requests)
+    for name, g, w in zip(("slots", "positions", "requests", "starts"), got,
+                          slots_of(lens, fresh, block, table, held, n_blocks, cap)):
+        assert np.array_equal(g.cpu().numpy(), w), name
+    for b, i in zip(bufs, at):
+        assert (b[:i] == -5).all() and (b[i + cap:] == -5).all()
+
+
+@pytest.mark.parametrize("req,tokens,dtype", [(9, 300, torch.int64), (9, 300, torch.int32), (5000, 20000, torch.int64),
+                                              (300, 4_300_000, torch.int64), (4500, 8_500_000, torch.int32)])
+@pytest.mark.parametrize("given", ["", "positions", "requests"])
+def test_slots_without_positions_or_requests(req, tokens, dtype, given):
+    """The C call takes NULL for either."""
+    rk = _rk()
+    lens, fresh, block, table, held, n_blocks, cap = prompts(req, req, tokens, 16, 5)
+    on = [t.to(DEV) for t in (lens, fresh, table, held)]
+    slots = torch.full((cap + 1,), -5, dtype=dtype, device=DEV)
+    more = {k: torch.full((cap + 1,), -5, dtype=torch.int32, device=DEV) for k in ("positions", "requests")}
+    starts = torch.empty(req + 1, dtype=torch.int32, device=DEV)
+    rc = rk.rk_slot_map(on[0].data_ptr(), on[1].data_ptr(), req, block, on[2].data_ptr(), table.shape[1], table.shape[1],
+                        on[3].data_ptr(), n_blocks, rk.RK_I64 if dtype == torch.int64 else rk.RK_I32, cap, slots.data_ptr(),
+                        *(more[k].data_ptr() if k == given else None for k in ("positions", "requests")), starts.data_ptr(),
+                        torch.cuda.current_stream().cuda_stream)
+    assert rc == rk.RK_OK
+    want = dict(zip(("slots", "positions", "requests", "starts"), slots_of(lens, fresh, block, table, held, n_blocks, cap)))
+    assert np.array_equal(slots[:cap].cpu().numpy(), want["slots"]) and slots[cap] == -5
+    assert np.array_equal(starts.cpu().numpy(), want["starts"])
+    for k, t in more.items():
+        assert np.array_equal(t[:cap].cpu().numpy(), want[k]) if k == given else (t == -5).all()
+        assert t[cap] == -5
