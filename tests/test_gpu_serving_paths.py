@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import serving_ref as ref
-from tests.test_gpu_serving import BF16, DEV, F32, _rk, drafts, gen, np64, run_verify
+from tests.test_gpu_serving import BF16, DEV, F32, _rk, check_tables, drafts, gen, np64, pool, run_verify
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +172,64 @@ def test_slots_without_positions_or_requests(req, tokens, dtype, given):
     for k, t in more.items():
         assert np.array_equal(t[:cap].cpu().numpy(), want[k]) if k == given else (t == -5).all()
         assert t[cap] == -5
+
+
+# --------------------------------------------------------------- block tables
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_tables_odd_values_in_either_form(in_place):
+    """What the one-launch form (outputs apart) has code of its own for."""
+    # more blocks come back than the ring has room for
+    check_tables(*pool(3, 40, 8, 16, 30, turnover=1.0, size=33), in_place=in_place)
+    check_tables(*pool(13, 700, 8, 16, 0, turnover=1.0, size=1), in_place=in_place)
+    # too few free ones, so that blocks given back are taken in the same call
+    check_tables(*pool(14, 900, 21, 16, 7, turnover=0.8), in_place=in_place)
+    check_tables(*pool(15, 4096, 5, 8, 100, turnover=0.9), in_place=in_place)
+    # lengths over the table's width, negative ones, held out of range
+    for seed, req in ((4, 30), (16, 1500)):
+        lens, block, held, table, ring, state = pool(seed, req, 6, 16, 400)
+        lens[::3], lens[1::7] = 16 * 6 + 33, -5
+        lens[5] = 2 ** 31 - 1
+        held[2], held[9] = -3, 77
+        check_tables(lens, block, held, table, ring, state, in_place=in_place)
+    lens, block, held, table, ring, state = pool(17, 30, 6, 1, 400)
+    lens[:] = 2 ** 31 - 1                          # the blocks beyond the tables' width pass 2^32
+    check_tables(lens, block, held, table, ring, state, in_place=in_place)
+    # head far along, and the state of an empty ring
+    for head in (2 ** 32 - 3, 2 ** 40 + 17):
+        check_tables(*pool(5, 30, 6, 16, 200, head=head), in_place=in_place)
+    check_tables(*pool(6, 30, 6, 16, 0), in_place=in_place)
+    # nothing to do
+    lens, block, held, table, ring, state = pool(7, 20, 6, 16, 50)
+    check_tables((held * block).to(torch.int32), block, held, table, ring, state, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("req", [50, 4097])
+def test_tables_inside_wider_rows_in_either_form(in_place, req):
+    rk = _rk()
+    lens, block, held, table, ring, state = pool(8, req, 9, 16, 10 * req)
+    wide = torch.full((req + 10, 13), -77, dtype=torch.int32)
+    wide[:req, 2:11] = table
+    d, dh, dr, ds = wide.to(DEV), held.to(DEV), ring.to(DEV), state.to(DEV)
+    want = ref.block_tables(lens.tolist(), block, held.tolist(), table.numpy(), ring.numpy(), state[:2].tolist())
+    apart = {} if in_place else dict(held_out=torch.empty_like(dh), state_out=torch.empty_like(ds))
+    after, now = rk.block_tables(lens.to(DEV), block, dh, d[:req, 2:11], dr, ds, **apart)
+    wide[:req, 2:11] = torch.from_numpy(want[1])
+    assert torch.equal(d.cpu(), wide)
+    for got, w in zip((after, dr, now), (want[0], want[2], want[3])):
+        assert np.array_equal(got.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_tables_run_out_and_go_on_in_either_form(in_place):
+    lens = torch.tensor([64, 64, 64, 64], dtype=torch.int32)
+    held = torch.tensor([4, 0, 1, 0], dtype=torch.int32)
+    table = torch.full((4, 5), -1, dtype=torch.int32)
+    table[0, :4], table[2, 0] = torch.tensor([1, 2, 3, 4]).int(), 5
+    ring = torch.tensor([9, 8, 7, 6, 10, 11, 12], dtype=torch.int32)
+    h, t, r, s = check_tables(lens, 16, held, table, ring, torch.tensor([12, 17, 0, 0]), in_place=in_place)
+    assert h.tolist() == [4, 4, 2, 0] and s.tolist() == [17, 17, 6, 0]
+    lens[0] = 0
+    h, t, r, s = check_tables(lens, 16, h, t, r, s, in_place=in_place)
+    assert h.tolist() == [0, 4, 4, 2] and s.tolist() == [21, 21, 2, 0]
