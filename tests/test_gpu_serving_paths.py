@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from tests import serving_ref as ref
-from tests.test_gpu_serving import BF16, DEV, F32, _rk, check_tables, drafts, gen, np64, pool, run_verify
+from tests.test_gpu_serving import (BF16, DEV, F16, F32, INF, _rk, check_softmax, check_tables, drafts, gen, np64, pool,
+                                    run_verify)
 
 pytestmark = pytest.mark.gpu
 
@@ -233,3 +234,35 @@ def test_tables_run_out_and_go_on_in_either_form(in_place):
     lens[0] = 0
     h, t, r, s = check_tables(lens, 16, h, t, r, s, in_place=in_place)
     assert h.tolist() == [0, 4, 4, 2] and s.tolist() == [21, 21, 2, 0]
+
+
+# -------------------------------------------------------------------- softmax
+
+@pytest.mark.parametrize("n,lines", [(131071, 68), (40003, 215), (2100001, 5)])
+@pytest.mark.parametrize("din,dout,in_place", [(F32, F32, False), (BF16, F32, False), (F16, F16, False), (F32, BF16, False),
+                                               (F32, F32, True), (BF16, BF16, True)])
+def test_softmax_past_the_caches(n, lines, din, dout, in_place):
+    """Outputs of more than 32 MB, lines at any element, between which nothing
+    is written; masked and greedy lines among them."""
+    rk = _rk()
+    lines *= 4 // torch.empty(0, dtype=dout).element_size()
+    assert lines * n * torch.empty(0, dtype=dout).element_size() > 32 << 20
+    x = torch.randn(lines, n, generator=gen(n)).mul_(3).to(din)
+    x[1, : n - 5] = -INF
+    x[2, ::2] = torch.finfo(din).min
+    x[lines - 1] = -INF
+    t = [(1.0, 0.7, 2.0, 0.0)[i % 4] for i in range(lines)]
+    buf = torch.full((lines * (n + 3) + 1,), 7.0, dtype=din, device=DEV)
+    view = buf.as_strided((lines, n), (n + 3, 1), 1)
+    view.copy_(x)
+    if in_place:
+        obuf, out = buf, view
+    else:
+        obuf = torch.full((lines * (n + 1) + 3,), 7.0, dtype=dout, device=DEV)
+        out = obuf.as_strided((lines, n), (n + 1, 1), 3)
+    assert rk.softmax(view, temperature=torch.tensor(t).to(DEV), out=out) is out
+    for i in range(0, lines, 40):                  # (the plain form's float64 lines, a few at a time)
+        check_softmax(out[i:i + 40], x[i:i + 40], t[i:i + 40])
+    touched = torch.zeros_like(obuf, dtype=torch.bool)
+    touched.as_strided(out.shape, out.stride(), out.storage_offset()).fill_(True)
+    assert (obuf[~touched] == 7.0).all()
