@@ -312,9 +312,10 @@ size_t rk_softmax_workspace_size(int in_dtype, int out_dtype, int64_t n, int64_t
  * Statistics are float32 and the result is rounded once to out_dtype; both
  * dtypes are f32, bf16 or f16.  An entry of -inf is masked: 0 at every
  * temperature; a line of nothing else gives zeros.  t <= 0 puts 1 on the
- * first largest entry, 0 elsewhere.  A NaN in the line, a NaN temperature, or
- * +inf with t > 0, makes the whole line NaN.  Exponentials below 2^-126 count
- * as 0, temperatures between 0 and 4.24e-39 as that (1 / t is a float32).
+ * first largest entry, 0 elsewhere.  A NaN in the line, a NaN temperature
+ * (masked entries or not), or +inf with t > 0, makes the whole line NaN.
+ * Exponentials below 2^-126 count as 0, temperatures between 0 and 4.24e-39
+ * as that (1 / t is a float32).
  *   x_stride    elements between lines (>= 0; 0 reads one line for all)
  *   out         device pointer; may be x itself with the same stride and
  *               element size, or other columns of the same rows; any other

@@ -12,8 +12,8 @@
 //
 // Sums and statistics are float32; the one rounding to the output's type is
 // the store's.  An entry of -inf counts as masked (0 whatever the temperature
-// is); a line of nothing else gives zeros.  NaN, or +inf at t > 0, makes the
-// line NaN.  t <= 0 puts 1 on the first largest entry.
+// is); a line of nothing else gives zeros.  NaN, a NaN temperature, or +inf at
+// t > 0, makes the line NaN.  t <= 0 puts 1 on the first largest entry.
 #define RK_UNIT unit_serve_softmax
 #include "rk_serve_device.hpp"
 
@@ -288,8 +288,9 @@ struct Piece {
 __device__ __forceinline__ float others_of(float m) { return m == m ? 0.0f : m; }
 __device__ __forceinline__ bool some(float m) { return m > -std::numeric_limits<float>::infinity(); }
 
-// The factor 1 / s; s = 0 where all entries are masked.
-__device__ __forceinline__ float inverse(float s) { return s == 0.0f ? 0.0f : 1.0f / s; }
+// The factor 1 / s; s = 0 where all entries are masked: they get 0, or, at a
+// NaN temperature (c, its factor, is NaN then), 0 * inf.
+__device__ __forceinline__ float inverse(float s, float c) { return s == 0.0f && c == c ? 0.0f : 1.0f / s; }
 
 // A line in the registers of LANES threads, BLOCK / LANES lines a block.  One
 // block works on a line whose exponentials take a CU's VALUs longer than its
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(BLOCK) void k_soft_line(SoftmaxArgs a)
         return s;
     };
     const float s = needs_guard(m, c) ? exponentials(std::true_type()) : exponentials(std::false_type());
-    const float inv = inverse(line_all<OpSum, LANES>(s, part[1]));
+    const float inv = inverse(line_all<OpSum, LANES>(s, part[1]), c);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (!p.any(u))
@@ -496,7 +497,7 @@ __device__ __forceinline__ void tile_write(const SoftmaxArgs &a, const Tile &til
         p.template write_one<Out, STREAM>(out, at, others_of(l.m));
         return;
     }
-    const float inv = inverse(l.s);
+    const float inv = inverse(l.s, c);
     if (needs_guard(l.m, c))
         p.template write<Out, STREAM, true>(out, l.m, c, inv);
     else

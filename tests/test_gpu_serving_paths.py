@@ -266,3 +266,14 @@ def test_softmax_past_the_caches(n, lines, din, dout, in_place):
     touched = torch.zeros_like(obuf, dtype=torch.bool)
     touched.as_strided(out.shape, out.stride(), out.storage_offset()).fill_(True)
     assert (obuf[~touched] == 7.0).all()
+
+
+@pytest.mark.parametrize("n", [5, 200, 1000, 9001, 40000, 1048577])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_softmax_nan_temperature(n, dt):
+    """A NaN temperature makes any line NaN, one whose mask leaves nothing too."""
+    x = torch.full((4, n), -INF, dtype=dt)
+    x[1, n // 2] = 1.0
+    x[2] = torch.randn(n, generator=gen(n)).to(dt)
+    t = [float("nan")] * 3 + [1.0]
+    check_softmax(_rk().softmax(x.to(DEV), temperature=torch.tensor(t).to(DEV)), x, t)
