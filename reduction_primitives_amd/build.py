@@ -14,6 +14,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -106,14 +107,19 @@ def _compile(src_name: str, force: bool):
     return obj, "\n".join(noise) or None
 
 
-def _build_binding(force: bool) -> None:
-    """Compile serve_bind.cpp, a host-only Python module over torch's headers."""
+def _build_binding(force: bool) -> str | None:
+    """Compile serve_bind.cpp, a host-only Python module over torch's headers.
+    Returns why it was not, where there is no torch: the library stands
+    without it."""
     src = os.path.join(CSRC, "serve_bind.cpp")
     if not force and not _stale(BINDING, src):
-        return
+        return None
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        return f"{BINDING} is not built, the serving operators cannot be called from Python: {e}"
     root = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
     cmd = ["g++"] + HOST_FLAGS + ["-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -124,11 +130,12 @@ def _build_binding(force: bool) -> None:
     if proc.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, BINDING)
+    return None
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     """Compile every unit (only stale ones unless force), link librk.so and
-    build the Python module."""
+    build the Python module (without torch: the library alone, and a warning)."""
     os.makedirs(OUT_DIR, exist_ok=True)
     units = KERNEL_UNITS + HIP_HOST_UNITS + PURE_UNITS
     jobs = jobs or min(len(units), max(1, min(os.cpu_count() or 1, 16)))
@@ -139,7 +146,6 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
             objs.append(obj)
             if msg and verbose:
                 print(msg, file=sys.stderr)
-        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         tmp = LIB + ".tmp"
@@ -149,6 +155,9 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if proc.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{proc.stdout}\n{proc.stderr}")
         os.replace(tmp, LIB)
+    left_out = binding.result()
+    if left_out:
+        warnings.warn(left_out)
     return LIB
 
 

@@ -261,3 +261,28 @@ int main() {
                     "-o", exe], check=True)
     run = subprocess.run([exe], capture_output=True, text=True, timeout=100)
     assert run.returncode == 0, run.stdout + run.stderr
+
+
+def _build_in(tmp_path, monkeypatch):
+    """The build module with every product under tmp_path, and of the
+    library's units the plain C++ ones alone (seconds to compile)."""
+    from reduction_primitives_amd import build as b
+    monkeypatch.setattr(b, "OUT_DIR", str(tmp_path / "_build"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "librk.so"))
+    monkeypatch.setattr(b, "BINDING", str(tmp_path / "_serving.so"))
+    monkeypatch.setattr(b, "KERNEL_UNITS", [])
+    monkeypatch.setattr(b, "HIP_HOST_UNITS", [])
+    return b
+
+
+def test_library_builds_without_torch(tmp_path, monkeypatch):
+    """The C ABI needs no torch: without it librk.so is built all the same,
+    and said to stand without the Python module."""
+    import sys
+    b = _build_in(tmp_path, monkeypatch)
+    if not os.path.exists(b.HIPCC):
+        pytest.skip("needs hipcc")
+    monkeypatch.setitem(sys.modules, "torch", None)        # import torch: ImportError
+    with pytest.warns(UserWarning, match="_serving.so"):
+        assert b.build() == b.LIB
+    assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
