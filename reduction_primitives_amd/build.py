@@ -111,15 +111,20 @@ def _build_binding(force: bool) -> str | None:
     """Compile serve_bind.cpp, a host-only Python module over torch's headers.
     Returns why it was not, where there is no torch: the library stands
     without it."""
-    src = os.path.join(CSRC, "serve_bind.cpp")
-    if not force and not _stale(BINDING, src):
-        return None
     import sysconfig
 
     try:
         import torch
     except ImportError as e:
         return f"{BINDING} is not built, the serving operators cannot be called from Python: {e}"
+    src = os.path.join(CSRC, "serve_bind.cpp")
+    # what the module holds to beside its source: torch's C++ ABI and headers, Python's ABI
+    made_for = f"{torch.__version__} in {os.path.dirname(torch.__file__)}, {sys.implementation.cache_tag}\n"
+    note = os.path.join(OUT_DIR, "_serving.txt")
+    if not force and not _stale(BINDING, src) and os.path.exists(note):
+        with open(note) as f:
+            if f.read() == made_for:
+                return None
     root = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
     cmd = ["g++"] + HOST_FLAGS + ["-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -130,6 +135,8 @@ def _build_binding(force: bool) -> str | None:
     if proc.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, BINDING)
+    with open(note, "w") as f:
+        f.write(made_for)
     return None
 
 

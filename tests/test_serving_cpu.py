@@ -286,3 +286,28 @@ def test_library_builds_without_torch(tmp_path, monkeypatch):
     with pytest.warns(UserWarning, match="_serving.so"):
         assert b.build() == b.LIB
     assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
+
+
+def test_python_module_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
+    """_serving.so holds to torch's C++ ABI and Python's: one that was built
+    for others is not taken, however new it is."""
+    import sys
+    import types
+    b = _build_in(tmp_path, monkeypatch)
+    os.makedirs(b.OUT_DIR)
+    compiled = []
+
+    def run(cmd, **kw):
+        compiled.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("module")
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    builds = lambda: (b._build_binding(False), len(compiled))[1]  # noqa: E731
+    assert builds() == 1 and builds() == 1
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert builds() == 2 and builds() == 2
+    monkeypatch.setattr(sys.implementation, "cache_tag", "cpython-399")
+    assert builds() == 3 and builds() == 3
+    monkeypatch.setitem(sys.modules, "torch", None)        # (nothing to build it with, and one is there)
+    assert builds() == 3
