@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -170,8 +171,19 @@ void *handle(PyObject *o)
 
 PyObject *status(int rc) { return PyLong_FromLong(rc); }
 
+// Softmax has no backward pass: where gradients are recorded, what requires
+// them is refused rather than left without.
+void no_gradient(const char *name, const char *what, PyObject *o)
+{
+    if (THPVariable_Check(o) && c10::GradMode::is_enabled() && THPVariable_Unpack(o).requires_grad())
+        refuse("%s: %s requires grad and the call has no gradient: detach it, or call under no_grad", name, what);
+}
+
 PyObject *softmax(PyObject *const *a)
 {
+    no_gradient("softmax", "x", a[1]);
+    no_gradient("softmax", "temperature", a[2]);
+    no_gradient("softmax", "out", a[3]);
     Call c("softmax", "x", a[1]);
     const at::Tensor &x = c.lines("x", a[1]);
     const int in = c.prob_code("x", x);

@@ -70,7 +70,8 @@ def softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, strea
     """softmax(x / temperature) along the lines of the 2-d tensor x
     (rk_softmax).  temperature: float32, one per line; a value <= 0 picks the
     first largest entry.  `out` defaults to a new tensor of out_dtype (x's
-    dtype); it may be x itself.  Returns out."""
+    dtype); it may be x itself.  Returns out.  There is no backward pass:
+    tensors that require grad are refused where gradients are recorded."""
     handle = _handle("softmax", "x", x, stream)
     if out is None:
         out = _empty(x.shape, out_dtype or x.dtype, x, stream)

@@ -277,3 +277,19 @@ def test_softmax_nan_temperature(n, dt):
     x[2] = torch.randn(n, generator=gen(n)).to(dt)
     t = [float("nan")] * 3 + [1.0]
     check_softmax(_rk().softmax(x.to(DEV), temperature=torch.tensor(t).to(DEV)), x, t)
+
+
+def test_softmax_refuses_to_drop_gradients():
+    rk = _rk()
+    x = torch.zeros(2, 8, device=DEV).requires_grad_()
+    t = torch.ones(2, device=DEV)
+    y = torch.zeros(2, 8, device=DEV)
+    for call in (lambda: rk.softmax(x), lambda: rk.softmax(x * 2, temperature=t), lambda: rk.softmax(y, out=x),
+                 lambda: rk.softmax(y, temperature=t.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+        with torch.no_grad():
+            assert torch.equal(call(), torch.full_like(y, 0.125))
+    assert torch.equal(rk.softmax(x.detach()), torch.full_like(y, 0.125))
+    with torch.inference_mode():
+        assert torch.equal(rk.softmax(x), torch.full_like(y, 0.125))

@@ -311,3 +311,17 @@ def test_python_module_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
     assert builds() == 3 and builds() == 3
     monkeypatch.setitem(sys.modules, "torch", None)        # (nothing to build it with, and one is there)
     assert builds() == 3
+
+
+def test_softmax_refuses_to_drop_gradients():
+    """The call has no backward pass: its module says so, where gradients are
+    recorded, before it looks at devices."""
+    call = _rk().softmax.__globals__["_calls"].softmax
+    x, t = torch.zeros(2, 8), torch.ones(2)
+    leaf = lambda v: v.clone().requires_grad_()  # noqa: E731
+    for what, args in (("x", (leaf(x), None, x)), ("temperature", (x, leaf(t), x)), ("out", (x, t, leaf(x))),
+                       ("x", (leaf(x) * 2, t, x))):
+        with pytest.raises(ValueError, match=what + " requires grad and the call has no gradient"):
+            call(0, *args, None)
+        with torch.no_grad(), pytest.raises(ValueError, match="not on a GPU"):     # (refused for that alone)
+            call(0, *args, None)
