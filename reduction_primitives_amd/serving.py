@@ -77,7 +77,7 @@ def softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, strea
         out = _empty(x.shape, out_dtype or x.dtype, x, stream)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise ValueError("softmax: out takes x's shape and out_dtype")
-    if workspace is None:
+    if workspace is None and x.dim() == 2:        # (other dims are refused below)
         codes = _code("softmax", "x", x.dtype), _code("softmax", "out", out.dtype)
         workspace = _workspace(N.rk_softmax_workspace_size, (*codes, x.shape[-1], x.shape[0]), x, stream)
     rc = _calls.softmax(handle, x, temperature, out, workspace)
@@ -104,7 +104,7 @@ def draft_verify(p, q, drafted, u, r, starts=None, max_draft=None, tokens=None, 
         tokens = _empty((r.numel(), max_draft + 1), drafted.dtype, p, stream)
     if accepted is None:
         accepted = _empty((r.numel(),), torch.int32, p, stream)
-    if workspace is None:
+    if workspace is None and p.dim() == 2:
         workspace = _workspace(N.rk_draft_verify_workspace_size,
                                (_code("draft_verify", "p", p.dtype), p.shape[-1], r.numel()), p, stream)
     rc = _calls.draft_verify(handle, p, q, drafted, u, r, starts, max_draft, tokens, accepted, workspace)

@@ -293,3 +293,12 @@ def test_softmax_refuses_to_drop_gradients():
     assert torch.equal(rk.softmax(x.detach()), torch.full_like(y, 0.125))
     with torch.inference_mode():
         assert torch.equal(rk.softmax(x), torch.full_like(y, 0.125))
+
+
+def test_tensors_of_no_dims_are_refused():
+    rk = _rk()
+    x, i, f = torch.zeros((), device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV), torch.zeros(1, device=DEV)
+    with pytest.raises(ValueError, match="two dims"):
+        rk.softmax(x)
+    with pytest.raises(ValueError, match="two dims"):
+        rk.draft_verify(x, None, i, f[:0], f)
