@@ -349,8 +349,9 @@ size_t rk_draft_verify_workspace_size(int prob_dtype, int64_t vocab, int64_t n_r
  *   tokens      n_req lines of max_draft + 1: the kept tokens, the drawn one
  *               (-1 where the target's line weighs nothing), -1 behind it
  *   accepted    n_req int32: how many drafts each request kept
- * prob_dtype: f32, bf16 or f16, of p and q; they need not sum to 1, and what
- * is not a positive finite number weighs nothing.  token_dtype: i32 or i64, of drafted and
+ * prob_dtype: f32, bf16 or f16, of p and q; they need not sum to 1.  A weight,
+ * p_i or p_i - q_i, that is not a positive finite number counts as 0, also
+ * p_i(x) in the comparison above.  token_dtype: i32 or i64, of drafted and
  * tokens.  A drafted token outside [0, vocab) is turned down.  starts is
  * clamped into [0, n_draft], and drafts beyond max_draft are ignored.  No
  * output may overlap an input.  vocab >= 1.  workspace: workspace_bytes >=
@@ -450,7 +451,8 @@ typedef enum {
                                    staged through LDS, look-back along the scan dim (+ a clearing
                                    launch) */
     RK_KERNEL_SOFTMAX_LINE = 14, /* softmax: a line in the registers of a quarter wave, a wave or a block, one launch */
-    RK_KERNEL_SOFTMAX_SPLIT = 15, /* softmax: tiles of a line, statistics first, then the line (two launches) */
+    RK_KERNEL_SOFTMAX_SPLIT = 15, /* softmax: tiles of a line, statistics first, then the line (two launches,
+                                    three beyond 2^20 entries) */
     RK_KERNEL_DRAFT_VERIFY = 16   /* draft verification: a wave per tile of a request's line */
 } rk_kernel;
 

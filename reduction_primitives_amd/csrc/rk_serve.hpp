@@ -173,7 +173,7 @@ struct VerifyArgs {
     void *tokens;
     int32_t *accepted;
     double *sums;             // [req][tiles]
-    VerifyDrawn *drawn;       // [req], for a second launch
+    VerifyDrawn *drawn;       // [req], written for a second launch
     int64_t tiles;
     int chunks;
     int slot;                 // >= 0: the last block of a request finishes it
@@ -213,14 +213,14 @@ struct TablesArgs {
     int64_t ring_size;
     const int64_t *state;
     int64_t *state_out;
-    TablesTotals *totals;     // the workspace: the totals, then a plan for every request and the end
+    TablesTotals *totals;     // the workspace: the totals, then a plan for every request
     TablesPlan *plan;
     Divider waves;            // waves that move one request's blocks
 };
 // LDS of a one-launch call's block: three words a request, two more, and its scans' sums.
 constexpr int64_t tables_lds_bytes(int64_t req) { return (3 * req + 2) * 4; }
 constexpr int64_t kTablesLdsFixed = 256;
-constexpr int64_t tables_ws_bytes(int64_t req) { return int64_t(sizeof(TablesTotals)) + (req + 1) * int64_t(sizeof(TablesPlan)); }
+constexpr int64_t tables_ws_bytes(int64_t req) { return int64_t(sizeof(TablesTotals)) + req * int64_t(sizeof(TablesPlan)); }
 
 struct TablesLaunch {
     TablesArgs a;

@@ -333,7 +333,6 @@ __global__ __launch_bounds__(B) void k_tables_scan(TablesArgs a)
         }
     }
     if (threadIdx.x == 0) {
-        a.plan[a.req] = TablesPlan{gives, takes, 0, 0};
         *a.totals = TablesTotals{gives, takes, head, tail};
         write_state(a, r, head, tail, gives, takes, beyond);
     }

@@ -302,3 +302,35 @@ def test_tensors_of_no_dims_are_refused():
         rk.softmax(x)
     with pytest.raises(ValueError, match="two dims"):
         rk.draft_verify(x, None, i, f[:0], f)
+
+
+# ---------------------------------------------------------------- workspaces
+
+def guarded(n):
+    """A workspace of n bytes and the buffer of twos around it."""
+    buf = torch.full((n + 1024,), 2, dtype=torch.uint8, device=DEV)
+    return buf[512:512 + n], lambda: bool((buf[:512] == 2).all()) and bool((buf[512 + n:] == 2).all())
+
+
+def test_workspaces_are_as_large_as_said():
+    """Sizes whose bytes fill the multiple of 256 that is asked for."""
+    rk = _rk()
+    for req in (20, 148, 1300):                    # 32 + 24 req: 512, 3584, 31232
+        assert (32 + 24 * req) % 256 == 0
+        ws, whole = guarded(rk.rk_block_tables_workspace_size(req))
+        lens, block, held, table, ring, state = (t.to(DEV) if isinstance(t, torch.Tensor) else t for t in pool(req, req, 9, 16, 5 * req))
+        want = ref.block_tables(lens.tolist(), block, held.tolist(), table.cpu().numpy(), ring.cpu().numpy(), state[:2].tolist())
+        rk.block_tables(lens, block, held, table, ring, state, workspace=ws)
+        for got, w in zip((held, table, ring, state), want):
+            assert np.array_equal(got.cpu().numpy(), w)
+        assert whole()
+    for req, n in ((16, 9000), (600, 9000), (4200, 8200), (64, 40001)):
+        d, big, at = spread_drafts(n + req, req, 1, n, True, m=60)
+        ws, whole = guarded(rk.rk_draft_verify_workspace_size(rk.RK_F32, n, req))
+        check_spread(d, at, run_verify(big, workspace=ws))
+        assert whole()
+    for lines, n in ((64, 64 * 2048), (64, 40000), (2, 513 * 2048), (3, 1048577)):
+        x = torch.randn(lines, n, generator=gen(n))
+        ws, whole = guarded(rk.rk_softmax_workspace_size(rk.RK_F32, rk.RK_F32, n, lines))
+        check_softmax(rk.softmax(x.to(DEV), workspace=ws), x, [1.0] * lines)
+        assert whole()
