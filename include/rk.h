@@ -90,12 +90,14 @@
  * variable RK_DEBUG is set.
  *
  * Waits inside a launch: block 0 of a whole-array pass waits for the other
- * blocks' partials, and a scan tile waits for its predecessors' prefixes.  No
+ * blocks' partials, and a scan tile (a linear recurrence's among them) waits
+ * for its predecessors' prefixes.  No
  * block waits on the block that waits for it, so these waits end; as a
  * safety net each is bounded (about a second).  A wait that gives up stores
  * no result (out keeps its previous contents; a scan's outputs after that
  * tile are wrong) and is counted: HOST mode then returns RK_ERR_HIP, and
- * rk_stream_timeouts reports the count for OVERWRITE, FOLD and scan calls.
+ * rk_stream_timeouts reports the count for OVERWRITE, FOLD, scan and
+ * recurrence calls.
  */
 #ifndef RK_H
 #define RK_H
@@ -414,6 +416,201 @@ int rk_block_tables(const int32_t *lens, int64_t n_req, int block_size, const in
 int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int block_size, const int32_t *table,
                 int64_t table_stride, int max_blocks, const int32_t *held, int64_t n_blocks, int slot_dtype,
                 int64_t capacity, void *slots, int32_t *positions, int32_t *requests, int32_t *starts, void *stream);
+
+/* Bytes of device workspace rk_beam_select needs on the current device (0 for
+ * invalid arguments and for no requests). */
+size_t rk_beam_select_workspace_size(int dtype, int64_t vocab, int64_t n_req, int beams, int count);
+
+/*
+ * Beam search's selection.  Request b has `beams` lines of logits, b * beams and
+ * on, and a score for each.  Token v of line l is a candidate with
+ *   s = scores[l] + x_v - log sum_w exp(x_w)        (over the line's vocabulary)
+ * and the `count` candidates with the largest s are kept, largest first; of equal
+ * ones (s in float64) the one of the lower line, then of the larger logit, then
+ * the lower token comes first.  Logits of -inf are masked, and a line of nothing
+ * else, or of score -inf, has no candidate.
+ *   logits      n_req * beams lines of vocab entries, f32, bf16 or f16
+ *   scores      a float32 for every line
+ *   ended       a byte for every line, or NULL: where it is not 0 the line is not
+ *               read; its one candidate is end_token (0 <= end_token < vocab) at
+ *               the line's score as it is
+ *   best        n_req * count float32: the kept candidates' s, rounded once (to
+ *               -inf below float32's range)
+ *   tokens      n_req * count of token_dtype, i32 or i64
+ *   parents     n_req * count int32: their lines (rows of rk_fork_blocks' table,
+ *               sources of rk_linear_recurrence)
+ * Behind a request's last candidate: -inf, -1, -1.  A request with a score of NaN
+ * or +inf, or with a NaN or +inf among the logits of a line that is read, gets
+ * NaN, -1, -1 throughout.  The sum's exponentials are float32 and its terms of
+ * 2^-126 of the largest and less count as 0.  count <= 64, beams <= 4096.  No
+ * output may overlap an input or another.  workspace: workspace_bytes >=
+ * rk_beam_select_workspace_size bytes, aligned to 8; calls that may overlap need
+ * one each.  Returns an rk_status.
+ */
+int rk_beam_select(int dtype, int token_dtype, const void *logits, int64_t stride, int64_t vocab, int64_t n_req, int beams,
+                   const float *scores, const uint8_t *ended, int64_t end_token, int count, float *best, void *tokens,
+                   int32_t *parents, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace rk_fork_blocks needs (0 for invalid arguments). */
+size_t rk_fork_blocks_workspace_size(int64_t n_rows, int64_t n_out, int max_blocks, int64_t n_blocks);
+
+/*
+ * Makes the rows of a block table those of other rows: row r of the new table is
+ * what row parents[r] was, and rows that no row goes on from are given up.  Rows
+ * may share blocks.  A row that goes on in several keeps its blocks in the first
+ * of them, r the lowest.  The others share with it the lens / block_size blocks
+ * that are full; of the next one, partly filled, each takes a block of its own
+ * from the front of the ring of free blocks (as in rk_block_tables), in the order
+ * of r, and pairs[r] says what is to be copied (rk_copy_blocks); blocks behind it
+ * they do not have.  Blocks that no new row names go, in order of the old rows
+ * that first name them and of position, to the ring's end; fresh blocks come from
+ * these last.  Where free blocks run out a row is left without its partly filled
+ * block, and is counted as missing: its tokens there are lost.
+ *   parents     n_out int32; -1, or anything outside [0, n_rows): an empty row
+ *   lens        n_rows int32: tokens of the old rows (negative: 0)
+ *   held        n_rows int32: blocks of the old rows (clamped into [0, max_blocks])
+ *   table       n_rows lines of max_blocks int32.  Ids outside [0, n_blocks) are
+ *               passed on, but never given back.  No free block may be among them.
+ *   ring, state, state_out  as in rk_block_tables: ring in place; state_out (4
+ *               int64: head, tail, rows left without a block, blocks that found no
+ *               place in the ring) may be state
+ *   table_out   n_out lines of max_blocks int32; entries behind held_out are left
+ *               as they were
+ *   held_out, lens_out  n_out int32: blocks and tokens of the new rows
+ *   pairs       n_out pairs of int32: (source, fresh block), or (-1, -1)
+ * n_rows and n_out times max_blocks < 2^31 - 1.  What is written may not overlap
+ * anything else.  workspace: workspace_bytes >= rk_fork_blocks_workspace_size
+ * bytes, aligned to 8; calls that may overlap need one each.  Returns an
+ * rk_status.
+ */
+int rk_fork_blocks(const int32_t *parents, int64_t n_out, const int32_t *lens, int64_t n_rows, int block_size,
+                   const int32_t *held, const int32_t *table, int64_t table_stride, int max_blocks, int32_t *ring,
+                   int64_t ring_size, const int64_t *state, int64_t n_blocks, int32_t *table_out, int64_t table_out_stride,
+                   int32_t *held_out, int32_t *lens_out, int32_t *pairs, int64_t *state_out, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace rk_compact_blocks needs (0 for invalid arguments). */
+size_t rk_compact_blocks_workspace_size(int64_t n_blocks);
+
+/*
+ * Brings the blocks in use to the lowest ids.  With u different blocks of
+ * [0, n_blocks) named by the table's lines (the held[b] first entries of line b),
+ * the k-th lowest id of them that is >= u is moved to the k-th lowest id below u
+ * that is not named.  Blocks that no line names are free afterwards, whatever
+ * held them before: the ring is made anew, u .. n_blocks - 1 at its places 0 and
+ * on (places behind them are left as they were).
+ *   table       n_rows lines of max_blocks int32; ids outside [0, n_blocks) are
+ *               passed on
+ *   table_out   the same lines with the new ids; entries behind held are left as
+ *               they were.  May be table itself.
+ *   ring        ring_size >= n_blocks int32
+ *   pairs       max_pairs >= n_blocks / 2 pairs of int32: (id before, id
+ *               afterwards) of each move, in order, then (-1, -1): what
+ *               rk_copy_blocks is to copy
+ *   state_out   4 int64: head (0), tail (n_blocks - u), moves, 0
+ * Everything else that is written may not overlap anything.  workspace:
+ * workspace_bytes >= rk_compact_blocks_workspace_size bytes, aligned to 16; calls
+ * that may overlap need one each.  Returns an rk_status.
+ */
+int rk_compact_blocks(const int32_t *held, int64_t n_rows, const int32_t *table, int64_t table_stride, int max_blocks,
+                      int64_t n_blocks, int32_t *table_out, int64_t table_out_stride, int32_t *ring, int64_t ring_size,
+                      int32_t *pairs, int64_t max_pairs, int64_t *state_out, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/* A cache: n_blocks blocks of block_bytes bytes, block_stride bytes apart. */
+typedef struct {
+    void *data;
+    int64_t block_stride, block_bytes, n_blocks;
+} rk_block_cache;
+
+/*
+ * Copies blocks inside caches: for every pair (source, destination) of n_pairs
+ * (device int32), block `destination` of each cache becomes what block `source`
+ * is.  A pair with an id outside [0, n_blocks) of a cache is left out there.  No
+ * block may be the destination of one pair and named by another; a block may be
+ * the source of several.  (rk_fork_blocks and rk_compact_blocks leave such pairs.)
+ * Blocks may start and end at any byte.  caches: host memory, read during the
+ * call; they must not overlap each other or pairs (what they hold between blocks
+ * is left alone, and may be another cache's).  Returns an rk_status.
+ */
+int rk_copy_blocks(const rk_block_cache *caches, int n_caches, const int32_t *pairs, int64_t n_pairs, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence: the scan of a recurrent layer, and its gradient.
+ * Tokens of `channels` contiguous elements; asynchronous, kernels only, so
+ * the calls may be captured (they use no per-stream slot).
+ * ---------------------------------------------------------------------- */
+
+/* What is taken for the gate a of a token and channel: the value itself, its
+ * exponential, or its logistic function 1 / (1 + exp(-gate)). */
+typedef enum { RK_GATE_VALUE = 0, RK_GATE_LOG = 1, RK_GATE_SIGMOID = 2 } rk_gate;
+
+/* Tokens of one or several sequences: token t of sequence b is the channels
+ * from data + b * seq_stride + t * token_stride on (elements).  The strides of
+ * what is only read may be 0.  `data` is written only where a call says so. */
+typedef struct {
+    void *data;
+    int64_t seq_stride, token_stride;
+} rk_rows;
+
+/* Bytes of device workspace rk_linear_recurrence and its backward pass need for
+ * tensors of any strides (0 where a call takes one launch, and for invalid
+ * arguments).  packed: whether `starts` is given. */
+size_t rk_linear_recurrence_workspace_size(int x_dtype, int gate_dtype, int64_t n_seq, int64_t tokens, int64_t channels,
+                                           int packed);
+
+/*
+ * For every sequence and channel, from the sequence's own state h_0,
+ *   h_t = a_t h_(t-1) + w_t x_t        w = 1, or 1 - a with `blend`
+ * Token t's h goes to `out`, the last one's, in float32, to state_out.
+ *   x_dtype     f32, bf16 or f16, of x and out; gate_dtype: the same or f32
+ *   kind        rk_gate: a is the gate, exp(gate) or the logistic function of it
+ *   state       n_states lines of channels float32, or NULL (zeros)
+ *   sources     n_seq int32: the line of state each sequence starts from (zeros
+ *               where it names none), or NULL: line b for sequence b, n_seq lines
+ *   starts      n_seq + 1 device int32: the sequences are the tokens [starts[b],
+ *               starts[b + 1]) of `tokens` in all (seq_stride is not used).  They
+ *               must not fall, and are clamped into [0, tokens].  Tokens of no
+ *               sequence are left as they were in out.  NULL: n_seq sequences of
+ *               `tokens` tokens each.
+ *   out         may be x or gate itself, or other columns of the same rows; no
+ *               other overlap
+ *   state_out   n_seq lines of channels float32: the last state, or the first one
+ *               of a sequence without tokens.  May be state, without sources.
+ * States, gates and their products are float32 and h is rounded once.  Nothing
+ * passes from one sequence to another.  (Runs of up to 4096 tokens are folded
+ * into one factor: a product of that many gates that leaves float32's range
+ * makes a state infinite or NaN that need not be, unless the state before the
+ * run is 0.)  Equal inputs give equal bits.  workspace: workspace_bytes >=
+ * rk_linear_recurrence_workspace_size bytes, aligned to 8 (may be NULL only if
+ * that size is 0); calls that may overlap need one each.  Returns an rk_status.
+ */
+int rk_linear_recurrence(int x_dtype, int gate_dtype, int kind, int blend, const rk_rows *gate, const rk_rows *x,
+                         const float *state, int64_t n_states, const int32_t *sources, const int32_t *starts,
+                         int64_t n_seq, int64_t tokens, int64_t channels, const rk_rows *out, float *state_out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of rk_linear_recurrence (without sources).  With d_t the gradient of
+ * token t's output and, after the last token, u = dstate_out (NULL: zeros),
+ *   g_t = d_t + u_(t+1)      u_t = a_t g_t      dx_t = w_t g_t
+ *   da_t = g_t h_(t-1), or g_t (h_(t-1) - x_t) with blend
+ *   dgate_t = da_t, da_t a_t or da_t a_t (1 - a_t) by kind
+ * and dstate = u of the first token (of a sequence without tokens: dstate_out).
+ *   x           read with blend only, else it may be NULL
+ *   out         what the forward pass returned (h_(t-1) is taken from it, the
+ *               first token's from state)
+ *   dgate, dx   of gate_dtype and x_dtype; either may be an input but `out` itself,
+ *               or other columns of the same rows.  Tokens of no sequence are
+ *               left as they were.
+ *   dstate      n_seq lines of channels float32, or NULL; apart from all else
+ * The rest is as with rk_linear_recurrence.  Returns an rk_status.
+ */
+int rk_linear_recurrence_backward(int x_dtype, int gate_dtype, int kind, int blend, const rk_rows *gate, const rk_rows *x,
+                                  const rk_rows *out, const rk_rows *dout, const float *state, const float *dstate_out,
+                                  const int32_t *starts, int64_t n_seq, int64_t tokens, int64_t channels,
+                                  const rk_rows *dgate, const rk_rows *dx, float *dstate, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of an rk_status value. */
 const char *rk_status_string(int status);

@@ -7,8 +7,11 @@ tensors into those calls (``reduce_all2`` for a two-input source) -- pick dtype 
 workspace with torch, pass the current HIP stream.  All arithmetic happens
 in the library's kernels; there is no fallback path.
 
-``softmax``, ``draft_verify``, ``block_tables`` and ``slot_map`` (serving.py,
-loaded at their first use) are the serving operators' face in the same way.
+``softmax``, ``draft_verify``, ``block_tables``, ``slot_map``, ``beam_select``,
+``fork_blocks``, ``compact_blocks`` and ``copy_blocks`` (serving.py,
+loaded at their first use) are the serving operators' face in the same way,
+``linear_recurrence`` and ``linear_recurrence_backward`` (recurrence.py) the
+recurrent layers'.
 """
 from __future__ import annotations
 
@@ -24,10 +27,12 @@ from ._native import (  # noqa: F401
     RK_KERNEL_DRAFT_VERIFY, RK_KERNEL_SCAN_TRANSPOSE, RK_KERNEL_SOFTMAX_LINE, RK_KERNEL_SOFTMAX_SPLIT, RK_KERNEL_THREAD,
     RK_KERNEL_TILED, RK_MAP2_ABSDIFF, RK_MAP2_MUL, RK_MAP2_SQDIFF,
     RK_MAP_ABS, RK_MAP_IDENTITY, RK_MAP_SQUARE,
-    RK_MODE_FOLD, RK_MODE_HOST, RK_MODE_OVERWRITE, RK_OK, RK_OP_MAX, RK_OP_MIN, RK_OP_SUM,
+    RK_GATE_LOG, RK_GATE_SIGMOID, RK_GATE_VALUE, RK_MODE_FOLD, RK_MODE_HOST, RK_MODE_OVERWRITE, RK_OK, RK_OP_MAX, RK_OP_MIN, RK_OP_SUM,
     RkError, load, rk_block_tables, rk_block_tables_workspace_size, rk_debug_device_info, rk_debug_fail_launches, rk_debug_force_wait_timeout,
     rk_debug_set_finish_tag, rk_debug_set_fused_finish, rk_debug_set_launch_events, rk_stream_timeouts,
     rk_debug_stream_read, rk_draft_verify, rk_draft_verify_workspace_size, rk_plan_all, rk_plan_all2, rk_plan_dims,
+    rk_beam_select, rk_beam_select_workspace_size, rk_compact_blocks, rk_compact_blocks_workspace_size, rk_copy_blocks,
+    rk_fork_blocks, rk_fork_blocks_workspace_size, rk_linear_recurrence, rk_linear_recurrence_backward, rk_linear_recurrence_workspace_size,
     rk_plan_draft_verify,
     rk_plan_info, rk_plan_scan, rk_plan_softmax, rk_reduce_all, rk_reduce_all2, rk_reduce_dims, rk_reduce_dims_no_workspace,
     rk_scan, rk_scan_dims,
@@ -300,14 +305,17 @@ def plan_dims(dtype, shape, strides, dims, acc=None, ptr=0, num_cus=0) -> dict:
     return d
 
 
-_SERVING = ("softmax", "draft_verify", "block_tables", "slot_map")
+_SERVING = ("softmax", "draft_verify", "block_tables", "slot_map", "beam_select", "fork_blocks", "compact_blocks", "copy_blocks")
+_RECURRENCE = ("linear_recurrence", "linear_recurrence_backward")
 
 
 def __getattr__(name):
-    # the serving operators' module loads torch and librk.so; this package
-    # does not, so that it can be imported to build the library
-    if name in _SERVING:
-        from . import serving
-        globals().update({n: getattr(serving, n) for n in _SERVING})
-        return globals()[name]
+    # the serving and recurrence operators' modules load torch and librk.so; this
+    # package does not, so that it can be imported to build the library
+    for names, module in ((_SERVING, "serving"), (_RECURRENCE, "recurrence")):
+        if name in names:
+            from importlib import import_module
+            m = import_module("." + module, __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

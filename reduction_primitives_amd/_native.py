@@ -19,6 +19,7 @@ RK_MAP_IDENTITY, RK_MAP_SQUARE, RK_MAP_ABS = 0, 1, 2
 RK_MAP2_MUL, RK_MAP2_SQDIFF, RK_MAP2_ABSDIFF = 0, 1, 2
 RK_F32, RK_BF16, RK_F16, RK_F64, RK_I32, RK_I64 = 0, 1, 2, 3, 4, 5
 RK_MODE_OVERWRITE, RK_MODE_FOLD, RK_MODE_HOST = 0, 1, 2
+RK_GATE_VALUE, RK_GATE_LOG, RK_GATE_SIGMOID = 0, 1, 2
 (RK_KERNEL_NONE, RK_KERNEL_ALL, RK_KERNEL_ALL_STRIDED, RK_KERNEL_THREAD, RK_KERNEL_TILED,
  RK_KERNEL_COLUMNS, RK_KERNEL_ROW, RK_KERNEL_GENERIC, RK_KERNEL_ALL2, RK_KERNEL_SCAN_TILE,
  RK_KERNEL_SCAN_ROWWAVE, RK_KERNEL_SCAN_LINES, RK_KERNEL_SCAN_COLUMNS, RK_KERNEL_SCAN_TRANSPOSE,
@@ -37,7 +38,10 @@ EXPORTS = ("rk_workspace_size", "rk_reduce_all", "rk_reduce_all2", "rk_reduce_di
            "rk_reduce_dims_no_workspace",
            "rk_softmax_workspace_size", "rk_softmax", "rk_draft_verify_workspace_size", "rk_draft_verify",
            "rk_block_tables_workspace_size", "rk_block_tables", "rk_slot_map",
-           "rk_plan_softmax", "rk_plan_draft_verify")
+           "rk_plan_softmax", "rk_plan_draft_verify",
+           "rk_beam_select_workspace_size", "rk_beam_select", "rk_fork_blocks_workspace_size", "rk_fork_blocks",
+           "rk_compact_blocks_workspace_size", "rk_compact_blocks", "rk_copy_blocks",
+           "rk_linear_recurrence_workspace_size", "rk_linear_recurrence", "rk_linear_recurrence_backward")
 
 
 class rk_plan_info(ctypes.Structure):
@@ -45,6 +49,15 @@ class rk_plan_info(ctypes.Structure):
                 ("block", ctypes.c_int), ("split", ctypes.c_int), ("vec", ctypes.c_int),
                 ("tile_outputs", ctypes.c_int), ("n_out", ctypes.c_int64),
                 ("reduce_len", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class rk_block_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("block_bytes", ctypes.c_int64),
+                ("n_blocks", ctypes.c_int64)]
+
+
+class rk_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
 class RkError(RuntimeError):
@@ -132,6 +145,28 @@ def load() -> ctypes.CDLL:
     lib.rk_plan_softmax.restype = i32
     lib.rk_plan_draft_verify.argtypes = [i32, i64, i64, i32, ctypes.POINTER(rk_plan_info)]
     lib.rk_plan_draft_verify.restype = i32
+    lib.rk_beam_select_workspace_size.argtypes = [i32, i64, i64, i32, i32]
+    lib.rk_beam_select_workspace_size.restype = sz
+    lib.rk_beam_select.argtypes = [i32, i32, vp, i64, i64, i64, i32, vp, vp, i64, i32, vp, vp, vp, vp, sz, vp]
+    lib.rk_beam_select.restype = i32
+    lib.rk_fork_blocks_workspace_size.argtypes = [i64, i64, i32, i64]
+    lib.rk_fork_blocks_workspace_size.restype = sz
+    lib.rk_fork_blocks.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.rk_fork_blocks.restype = i32
+    lib.rk_compact_blocks_workspace_size.argtypes = [i64]
+    lib.rk_compact_blocks_workspace_size.restype = sz
+    lib.rk_compact_blocks.argtypes = [vp, i64, vp, i64, i32, i64, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp]
+    lib.rk_compact_blocks.restype = i32
+    lib.rk_copy_blocks.argtypes = [ctypes.POINTER(rk_block_cache), i32, vp, i64, vp]
+    lib.rk_copy_blocks.restype = i32
+    rows = ctypes.POINTER(rk_rows)
+    lib.rk_linear_recurrence_workspace_size.argtypes = [i32, i32, i64, i64, i64, i32]
+    lib.rk_linear_recurrence_workspace_size.restype = sz
+    lib.rk_linear_recurrence.argtypes = [i32, i32, i32, i32, rows, rows, vp, i64, vp, vp, i64, i64, i64, rows, vp, vp, sz, vp]
+    lib.rk_linear_recurrence.restype = i32
+    lib.rk_linear_recurrence_backward.argtypes = [i32, i32, i32, i32, rows, rows, rows, rows, vp, vp, vp, i64, i64, i64, rows,
+                                                  rows, vp, vp, sz, vp]
+    lib.rk_linear_recurrence_backward.restype = i32
     _lib = lib
     return lib
 
@@ -263,6 +298,68 @@ def rk_slot_map(lens, fresh, n_req, block_size, table, table_stride, max_blocks,
                 capacity, slots, positions, requests, starts, stream) -> int:
     return load().rk_slot_map(lens, fresh, n_req, block_size, table, table_stride, max_blocks, held, n_blocks,
                               slot_dtype, capacity, slots, positions, requests, starts, stream)
+
+
+def rk_beam_select_workspace_size(dtype, vocab, n_req, beams, count) -> int:
+    return int(load().rk_beam_select_workspace_size(dtype, vocab, n_req, beams, count))
+
+
+def rk_beam_select(dtype, token_dtype, logits, stride, vocab, n_req, beams, scores, ended, end_token, count, best, tokens,
+                   parents, workspace, workspace_bytes, stream) -> int:
+    return load().rk_beam_select(dtype, token_dtype, logits, stride, vocab, n_req, beams, scores, ended, end_token, count, best,
+                                 tokens, parents, workspace, workspace_bytes, stream)
+
+
+def rk_fork_blocks_workspace_size(n_rows, n_out, max_blocks, n_blocks) -> int:
+    return int(load().rk_fork_blocks_workspace_size(n_rows, n_out, max_blocks, n_blocks))
+
+
+def rk_fork_blocks(parents, n_out, lens, n_rows, block_size, held, table, table_stride, max_blocks, ring, ring_size, state,
+                   n_blocks, table_out, table_out_stride, held_out, lens_out, pairs, state_out, workspace, workspace_bytes,
+                   stream) -> int:
+    return load().rk_fork_blocks(parents, n_out, lens, n_rows, block_size, held, table, table_stride, max_blocks, ring,
+                                 ring_size, state, n_blocks, table_out, table_out_stride, held_out, lens_out, pairs, state_out,
+                                 workspace, workspace_bytes, stream)
+
+
+def rk_compact_blocks_workspace_size(n_blocks) -> int:
+    return int(load().rk_compact_blocks_workspace_size(n_blocks))
+
+
+def rk_compact_blocks(held, n_rows, table, table_stride, max_blocks, n_blocks, table_out, table_out_stride, ring, ring_size,
+                      pairs, max_pairs, state_out, workspace, workspace_bytes, stream) -> int:
+    return load().rk_compact_blocks(held, n_rows, table, table_stride, max_blocks, n_blocks, table_out, table_out_stride, ring,
+                                    ring_size, pairs, max_pairs, state_out, workspace, workspace_bytes, stream)
+
+
+def rk_copy_blocks(caches, pairs, n_pairs, stream) -> int:
+    """caches: (address, block_stride, block_bytes, n_blocks) each."""
+    at = (rk_block_cache * max(len(caches), 1))(*(rk_block_cache(*c) for c in caches))
+    return load().rk_copy_blocks(at, len(caches), pairs, n_pairs, stream)
+
+
+def rk_linear_recurrence_workspace_size(x_dtype, gate_dtype, n_seq, tokens, channels, packed) -> int:
+    return int(load().rk_linear_recurrence_workspace_size(x_dtype, gate_dtype, n_seq, tokens, channels, packed))
+
+
+def _rows(r):
+    return None if r is None else ctypes.byref(rk_rows(*r))
+
+
+def rk_linear_recurrence(x_dtype, gate_dtype, kind, blend, gate, x, state, n_states, sources, starts, n_seq, tokens,
+                         channels, out, state_out, workspace, workspace_bytes, stream) -> int:
+    """gate, x, out: (address, seq_stride, token_stride) or None."""
+    return load().rk_linear_recurrence(x_dtype, gate_dtype, kind, blend, _rows(gate), _rows(x), state, n_states, sources,
+                                       starts, n_seq, tokens, channels, _rows(out), state_out, workspace, workspace_bytes,
+                                       stream)
+
+
+def rk_linear_recurrence_backward(x_dtype, gate_dtype, kind, blend, gate, x, out, dout, state, dstate_out, starts, n_seq,
+                                  tokens, channels, dgate, dx, dstate, workspace, workspace_bytes, stream) -> int:
+    """gate, x, out, dout, dgate, dx: (address, seq_stride, token_stride) or None."""
+    return load().rk_linear_recurrence_backward(x_dtype, gate_dtype, kind, blend, _rows(gate), _rows(x), _rows(out),
+                                                _rows(dout), state, dstate_out, starts, n_seq, tokens, channels,
+                                                _rows(dgate), _rows(dx), dstate, workspace, workspace_bytes, stream)
 
 
 def rk_plan_softmax(in_dtype, out_dtype, n, lines) -> rk_plan_info:

@@ -1,0 +1,8 @@
+// recur_f32.hip -- the gated linear recurrence for one type of inputs (f32).
+#define RK_UNIT unit_recur_f32
+#include "rk_recur_kernels.hpp"
+
+namespace rk {
+int launch_recur_f32(const RecurLaunch &L) { return launch_recur_x<float>(L); }
+int take_recur_timeouts_f32(uint64_t *count) { return take_recur_timeouts(count); }
+}  // namespace rk

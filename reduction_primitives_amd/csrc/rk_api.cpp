@@ -581,6 +581,9 @@ int rk_stream_timeouts(void *stream, uint64_t *count)
         if (rc != RK_OK)
             return rc;
     }
+    for (auto take : {take_recur_timeouts_f32, take_recur_timeouts_bf16, take_recur_timeouts_f16})
+        if (take(count) != ST_OK)
+            return RK_ERR_HIP;
     return RK_OK;
 }
 
@@ -1083,6 +1086,7 @@ int device_cus() { return ::device_cus(); }
 int stream_slot(void *stream) { return arrive_slot(static_cast<hipStream_t>(stream)); }
 bool fused_finish() { return g_fused_finish.load(std::memory_order_relaxed); }
 bool injected_launch_failure() { return ::injected_launch_failure(); }
+int64_t forced_wait() { return g_force_wait.load(std::memory_order_relaxed); }
 bool debug_enabled() { return ::debug_enabled(); }
 void launch_events(void **begin, void **end)
 {

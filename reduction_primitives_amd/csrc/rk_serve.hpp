@@ -69,6 +69,21 @@ constexpr int kLdsBytes = 160 << 10;      // of a CU
 // 50 MB: 11.9 us with plain stores, 11.1 us without); smaller ones stay there
 // for the kernels that write the cache.
 constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
+// ---- beam selection
+constexpr int kBeamBlock = 256;
+constexpr int kBeamTile = 2048;           // vocabulary entries of a wave's tile
+constexpr int kBeamWavesPerCu = 8;        // waves of the first launch = CUs * this, or a wave a tile
+constexpr int kBeamMost = 64;             // candidates kept of a request: a lane each
+constexpr int kBeamLines = 4096;          // beams of a request, 12 bytes of LDS each
+// ---- forked, compacted and copied blocks
+constexpr int kPageBlock = 256;
+constexpr int kPageSeg = 1024;            // table entries a wave goes through at a time
+constexpr int kPageLdsRows = 4096;        // rows (old and new each) that every block plans for itself in LDS
+constexpr int kPageBlocksPerCu = 8;       // grid cap = CUs * this
+constexpr int kCompactChunk = 4096;       // ids whose flags a block packs
+constexpr int kCopyCaches = 64;           // caches of a launch
+constexpr int kCopyBlocksPerCu = 16;      // blocks of a launch = CUs * this, or one a pair of a chunk
+constexpr int kCopyChunk = 16384;         // bytes of a cache's block that a thread block copies at a time
 }  // namespace tune
 
 enum SoftmaxKernel { VK_NONE = 0, VK_SOFT_LINE = 1, VK_SOFT_SPLIT = 2 };
@@ -254,5 +269,120 @@ struct SlotLaunch {
     void *stream, *ev_begin, *ev_end;
 };
 int launch_slots(const SlotLaunch &L);
+
+// --------------------------------------------------------------- beam search
+
+struct BeamPlan {
+    int64_t chunks = 0;       // waves of a line
+    int64_t per_wave = 0;     // entries of a wave
+    int64_t items = 0, grid = 0;
+    size_t ws_bytes = 0;
+};
+
+struct BeamArgs {
+    const void *x;
+    int64_t stride, n;        // of lines; vocabulary
+    int64_t req;
+    int beams, count;
+    const float *scores;
+    const uint8_t *ended;     // or NULL
+    int64_t end_token;
+    int64_t chunks, per_wave, items;
+    double *sums;             // of every item (a wave's part of a line)
+    float *tops, *best_x;     // the largest entry; the count largest
+    int32_t *best_at;
+    float *best;
+    void *tokens;
+    int32_t *parents;
+};
+
+int plan_beams(int dtype, int64_t n, int64_t req, int64_t beams, int64_t count, int cus, BeamPlan *p);
+
+struct BeamLaunch {
+    BeamPlan plan;
+    BeamArgs a;
+    int dtype, token_dtype;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_beams(const BeamLaunch &L);
+
+// ------------------------------------------- forked, compacted, copied blocks
+
+struct ForkArgs {
+    const int32_t *parents, *lens, *held;
+    int64_t rows, rows_out;
+    Divider block;
+    const int32_t *table;
+    int64_t ts;
+    int max_blocks, segs;     // entries of a line, and waves that go through it
+    int32_t *ring;
+    int64_t ring_size;
+    const int64_t *state;
+    int64_t n_blocks;
+    int32_t *table_out;
+    int64_t tos;
+    int32_t *held_out, *lens_out, *pairs;
+    int64_t *state_out;
+    // workspace
+    int32_t *child;           // [rows]: the first child, none: INT32_MAX
+    int32_t *gives, *takes;   // [rows], [rows_out]: blocks given back; then (many rows) those given and taken before
+    int32_t *parts;           // [rows][segs]: blocks given back by a segment
+    uint32_t *owner;          // [n_blocks]: 0 where a row goes on naming the block, else the first entry naming it, + 1
+    int64_t *totals;          // [4]: given back, wanted; head and tail of the ring before the call
+};
+
+struct ForkLaunch {
+    ForkArgs a;
+    bool in_lds;              // every block plans all rows for itself
+    int64_t grid;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_fork(const ForkLaunch &L);
+size_t fork_ws_bytes(int64_t rows, int64_t rows_out, int64_t max_blocks, int64_t n_blocks);
+
+struct CompactArgs {
+    const int32_t *held, *table;
+    int64_t rows, ts;
+    int max_blocks, segs;
+    int64_t n_blocks;
+    int32_t *table_out;
+    int64_t tos;
+    int32_t *ring, *pairs;
+    int64_t max_pairs;
+    int64_t *state_out;
+    // workspace
+    uint8_t *used;            // [chunks * kCompactChunk]
+    uint64_t *bits;           // [chunks * kCompactChunk / 64]
+    uint16_t *before;         // of each word: blocks in use of its chunk before it
+    int32_t *chunk;           // [chunks + 1]: blocks in use in a chunk; then before it (at last: all)
+    int64_t chunks;
+};
+
+struct CompactLaunch {
+    CompactArgs a;
+    int64_t grid;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_compact(const CompactLaunch &L);
+size_t compact_ws_bytes(int64_t n_blocks);
+
+struct CopyCache {
+    char *data;
+    int64_t stride, bytes;    // of blocks
+    int64_t blocks;
+};
+struct CopyArgs {
+    CopyCache cache[tune::kCopyCaches];
+    int caches;
+    const int32_t *pairs;
+    int64_t n_pairs;
+    int chunks, parts;        // thread blocks of a cache's block; of 256 pairs
+};
+struct CopyLaunch {
+    CopyArgs a;
+    int64_t grid_x;
+    void *stream, *ev_begin, *ev_end;
+};
+int launch_copy(const CopyLaunch &L);
 
 }  // namespace rk

@@ -7,46 +7,12 @@
 #include <cstdio>
 #include <cstring>
 
+#include "rk_checks.hpp"
 #include "rk_host.hpp"
 #include "rk_serve.hpp"
 
-namespace {
-
 using namespace rk;
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-    uintptr_t from, to;       // bytes [from, to)
-};
-
-Span span(const void *p, int64_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p && bytes > 0 ? a + uintptr_t(bytes) : a};
-}
-
-Span line_span(const void *p, int64_t n, int64_t lines, int64_t stride, int size)
-{
-    return span(p, n > 0 && lines > 0 ? ((lines - 1) * stride + n) * size : 0);
-}
-
-bool overlap(const Span &a, const Span &b) { return a.from < b.to && b.from < a.to; }
-
-// Lines fit the address space: lines * stride * 8 bytes stay far below 2^63.
-bool lines_fit(int64_t n, int64_t lines, int64_t stride)
-{
-    constexpr int64_t most = int64_t(1) << 48;
-    return stride >= 0 && stride <= most && n <= most && (lines <= 1 || stride == 0 || lines <= most / stride);
-}
-
-bool capturing(hipStream_t st)
-{
-    hipStreamCaptureStatus s = hipStreamCaptureStatusNone;
-    return hipStreamIsCapturing(st, &s) != hipSuccess || s != hipStreamCaptureStatusNone;
-}
-
-}  // namespace
+using namespace rk::checks;
 
 extern "C" {
 
@@ -401,6 +367,298 @@ int rk_slot_map(const int32_t *lens, const int32_t *fresh, int64_t n_req, int bl
     if (host::injected_launch_failure())
         return RK_ERR_HIP;
     return launch_slots(L);
+}
+
+size_t rk_beam_select_workspace_size(int dtype, int64_t vocab, int64_t n_req, int beams, int count)
+{
+    BeamPlan p;
+    return plan_beams(dtype, vocab, n_req, beams, count, host::device_cus(), &p) == ST_OK ? p.ws_bytes : 0;
+}
+
+int rk_beam_select(int dtype, int token_dtype, const void *logits, int64_t stride, int64_t vocab, int64_t n_req, int beams,
+                   const float *scores, const uint8_t *ended, int64_t end_token, int count, float *best, void *tokens,
+                   int32_t *parents, void *workspace, size_t workspace_bytes, void *stream)
+{
+    BeamPlan p;
+    const int rc = plan_beams(dtype, vocab, n_req, beams, count, host::device_cus(), &p);
+    if (rc)
+        return rc;
+    if (!dtype_known(token_dtype) || (ended && (end_token < 0 || end_token >= vocab)))
+        return RK_ERR_INVALID_ARGUMENT;
+    if (token_dtype != I32 && token_dtype != I64)
+        return RK_ERR_UNSUPPORTED;
+    if (n_req == 0)
+        return RK_OK;
+    const int64_t lines = n_req * beams, kept = n_req * count;
+    const int xsz = dtype_size(dtype), tsz = dtype_size(token_dtype);
+    if (!lines_fit(vocab, lines, stride) || !logits || !scores || !best || !tokens || !parents)
+        return RK_ERR_INVALID_ARGUMENT;
+    if (!aligned(logits, xsz) || !aligned(scores, 4) || !aligned(best, 4) || !aligned(tokens, tsz) || !aligned(parents, 4))
+        return RK_ERR_INVALID_ARGUMENT;
+    if (!workspace || !aligned(workspace, 8) || workspace_bytes < p.ws_bytes)
+        return RK_ERR_INVALID_ARGUMENT;
+    const Span out[] = {span(best, kept * 4), span(tokens, kept * tsz), span(parents, kept * 4),
+                        span(workspace, int64_t(p.ws_bytes))};
+    const Span in[] = {line_span(logits, vocab, lines, stride, xsz), span(scores, lines * 4), span(ended, lines)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span &s : in)
+            if (overlap(out[i], s))
+                return RK_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return RK_ERR_INVALID_ARGUMENT;
+    }
+    if (host::debug_enabled())
+        std::fprintf(stderr, "rk_beam_select: vocab=%lld requests=%lld beams=%d count=%d chunks=%lld ws=%zu\n", (long long)vocab,
+                     (long long)n_req, beams, count, (long long)p.chunks, p.ws_bytes);
+    BeamLaunch L;
+    std::memset(static_cast<void *>(&L), 0, sizeof L);
+    L.plan = p;
+    L.a.x = logits;
+    L.a.stride = stride;
+    L.a.n = vocab;
+    L.a.req = n_req;
+    L.a.beams = beams;
+    L.a.count = count;
+    L.a.scores = scores;
+    L.a.ended = ended;
+    L.a.end_token = end_token;
+    L.a.chunks = p.chunks;
+    L.a.per_wave = p.per_wave;
+    L.a.items = p.items;
+    L.a.sums = static_cast<double *>(workspace);
+    L.a.tops = reinterpret_cast<float *>(L.a.sums + p.items);
+    L.a.best_x = L.a.tops + p.items;
+    L.a.best_at = reinterpret_cast<int32_t *>(L.a.best_x + p.items * count);
+    L.a.best = best;
+    L.a.tokens = tokens;
+    L.a.parents = parents;
+    L.dtype = dtype;
+    L.token_dtype = token_dtype;
+    L.stream = stream;
+    host::launch_events(&L.ev_begin, &L.ev_end);
+    if (host::injected_launch_failure())
+        return RK_ERR_HIP;
+    return launch_beams(L);
+}
+
+size_t rk_fork_blocks_workspace_size(int64_t n_rows, int64_t n_out, int max_blocks, int64_t n_blocks)
+{
+    return n_rows < 0 || n_out < 0 || max_blocks < 0 || n_blocks < 0 || n_rows > 0x7fffffff || n_out > 0x7fffffff ||
+                   n_blocks > 0x7fffffff || n_rows * max_blocks > 0x7fffffff
+               ? 0 : fork_ws_bytes(n_rows, n_out, max_blocks, n_blocks);
+}
+
+int rk_fork_blocks(const int32_t *parents, int64_t n_out, const int32_t *lens, int64_t n_rows, int block_size,
+                   const int32_t *held, const int32_t *table, int64_t table_stride, int max_blocks, int32_t *ring,
+                   int64_t ring_size, const int64_t *state, int64_t n_blocks, int32_t *table_out, int64_t table_out_stride,
+                   int32_t *held_out, int32_t *lens_out, int32_t *pairs, int64_t *state_out, void *workspace,
+                   size_t workspace_bytes, void *stream)
+{
+    if (n_out < 0 || n_rows < 0 || block_size < 1 || max_blocks < 0 || ring_size < 1 || n_blocks < 0)
+        return RK_ERR_INVALID_ARGUMENT;
+    if (n_out > 0x7ffffffe || n_rows > 0x7ffffffe || ring_size > 0x7fffffff || n_blocks > 0x7fffffff ||
+        n_rows * max_blocks > 0x7ffffffe || n_out * max_blocks > 0x7ffffffe)
+        return RK_ERR_UNSUPPORTED;
+    if (!lines_fit(max_blocks, n_rows, table_stride) || !lines_fit(max_blocks, n_out, table_out_stride) ||
+        (n_out > 1 && table_out_stride < max_blocks))
+        return RK_ERR_INVALID_ARGUMENT;
+    const int64_t ws = int64_t(fork_ws_bytes(n_rows, n_out, max_blocks, n_blocks));
+    if (!ring || !state || !state_out || !workspace || !aligned(workspace, 8) || workspace_bytes < size_t(ws))
+        return RK_ERR_INVALID_ARGUMENT;
+    if ((n_rows > 0 && (!lens || !held || (max_blocks > 0 && !table))) ||
+        (n_out > 0 && (!parents || !held_out || !lens_out || !pairs || (max_blocks > 0 && !table_out))))
+        return RK_ERR_INVALID_ARGUMENT;
+    if (!aligned(parents, 4) || !aligned(lens, 4) || !aligned(held, 4) || !aligned(table, 4) || !aligned(ring, 4) ||
+        !aligned(state, 8) || !aligned(state_out, 8) || !aligned(table_out, 4) || !aligned(held_out, 4) ||
+        !aligned(lens_out, 4) || !aligned(pairs, 4))
+        return RK_ERR_INVALID_ARGUMENT;
+    // state_out may be state; nothing else may overlap what is written
+    const Span out[] = {span(state_out, 32), span(ring, ring_size * 4),
+                        line_span(table_out, max_blocks, n_out, table_out_stride, 4), span(held_out, n_out * 4),
+                        span(lens_out, n_out * 4), span(pairs, n_out * 8), span(workspace, ws)};
+    const Span in[] = {span(parents, n_out * 4), span(lens, n_rows * 4), span(held, n_rows * 4),
+                       line_span(table, max_blocks, n_rows, table_stride, 4)};
+    constexpr int n = sizeof out / sizeof *out;
+    for (int i = 0; i < n; ++i) {
+        if (overlap(out[i], span(state, 16)) && !(i == 0 && state_out == state))
+            return RK_ERR_INVALID_ARGUMENT;
+        for (const Span &s : in)
+            if (overlap(out[i], s))
+                return RK_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return RK_ERR_INVALID_ARGUMENT;
+    }
+    if (host::debug_enabled())
+        std::fprintf(stderr, "rk_fork_blocks: rows=%lld to %lld block=%d max_blocks=%d ring=%lld blocks=%lld\n",
+                     (long long)n_rows, (long long)n_out, block_size, max_blocks, (long long)ring_size, (long long)n_blocks);
+    ForkLaunch L;
+    std::memset(static_cast<void *>(&L), 0, sizeof L);
+    ForkArgs &a = L.a;
+    a.parents = parents;
+    a.lens = lens;
+    a.held = held;
+    a.rows = n_rows;
+    a.rows_out = n_out;
+    a.block = make_divider(uint32_t(block_size));
+    a.table = table;
+    a.ts = table_stride;
+    a.max_blocks = max_blocks;
+    a.segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
+    a.ring = ring;
+    a.ring_size = ring_size;
+    a.state = state;
+    a.n_blocks = n_blocks;
+    a.table_out = table_out;
+    a.tos = table_out_stride;
+    a.held_out = held_out;
+    a.lens_out = lens_out;
+    a.pairs = pairs;
+    a.state_out = state_out;
+    a.totals = static_cast<int64_t *>(workspace);
+    a.child = reinterpret_cast<int32_t *>(a.totals + 4);
+    a.gives = a.child + n_rows;
+    a.takes = a.gives + n_rows;
+    a.parts = a.takes + n_out;
+    a.owner = reinterpret_cast<uint32_t *>(a.parts + n_rows * a.segs);
+    L.in_lds = n_rows <= tune::kPageLdsRows && n_out <= tune::kPageLdsRows;
+    L.grid = int64_t(host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus) * tune::kPageBlocksPerCu;
+    L.stream = stream;
+    host::launch_events(&L.ev_begin, &L.ev_end);
+    if (host::injected_launch_failure())
+        return RK_ERR_HIP;
+    return launch_fork(L);
+}
+
+size_t rk_compact_blocks_workspace_size(int64_t n_blocks)
+{
+    return n_blocks < 0 || n_blocks > 0x7fffffff ? 0 : compact_ws_bytes(n_blocks);
+}
+
+int rk_compact_blocks(const int32_t *held, int64_t n_rows, const int32_t *table, int64_t table_stride, int max_blocks,
+                      int64_t n_blocks, int32_t *table_out, int64_t table_out_stride, int32_t *ring, int64_t ring_size,
+                      int32_t *pairs, int64_t max_pairs, int64_t *state_out, void *workspace, size_t workspace_bytes,
+                      void *stream)
+{
+    if (n_rows < 0 || max_blocks < 0 || n_blocks < 0 || ring_size < 1 || ring_size < n_blocks || max_pairs < n_blocks / 2)
+        return RK_ERR_INVALID_ARGUMENT;
+    if (n_rows > 0x7fffffff || n_blocks > 0x7fffffff || ring_size > 0x7fffffff || max_pairs > 0x7fffffff)
+        return RK_ERR_UNSUPPORTED;
+    if (!lines_fit(max_blocks, n_rows, table_stride) || !lines_fit(max_blocks, n_rows, table_out_stride) ||
+        (n_rows > 1 && table_out_stride < max_blocks))
+        return RK_ERR_INVALID_ARGUMENT;
+    const int64_t ws = int64_t(compact_ws_bytes(n_blocks));
+    if (!ring || !state_out || !workspace || !aligned(workspace, 16) || workspace_bytes < size_t(ws) ||
+        (n_rows > 0 && (!held || (max_blocks > 0 && (!table || !table_out)))) || (max_pairs > 0 && !pairs))
+        return RK_ERR_INVALID_ARGUMENT;
+    if (!aligned(held, 4) || !aligned(table, 4) || !aligned(table_out, 4) || !aligned(ring, 4) || !aligned(pairs, 4) ||
+        !aligned(state_out, 8))
+        return RK_ERR_INVALID_ARGUMENT;
+    const Span st = line_span(table, max_blocks, n_rows, table_stride, 4), sh = span(held, n_rows * 4);
+    const Span out[] = {line_span(table_out, max_blocks, n_rows, table_out_stride, 4), span(ring, ring_size * 4),
+                        span(pairs, max_pairs * 8), span(state_out, 32), span(workspace, ws)};
+    for (int i = 0; i < 5; ++i) {
+        if (overlap(out[i], sh) || (overlap(out[i], st) && !(i == 0 && table_out == table &&
+                                                             (n_rows <= 1 || table_out_stride == table_stride))))
+            return RK_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return RK_ERR_INVALID_ARGUMENT;
+    }
+    if (host::debug_enabled())
+        std::fprintf(stderr, "rk_compact_blocks: rows=%lld max_blocks=%d blocks=%lld\n", (long long)n_rows, max_blocks,
+                     (long long)n_blocks);
+    CompactLaunch L;
+    std::memset(static_cast<void *>(&L), 0, sizeof L);
+    CompactArgs &a = L.a;
+    a.held = held;
+    a.table = table;
+    a.rows = n_rows;
+    a.ts = table_stride;
+    a.max_blocks = max_blocks;
+    a.segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
+    a.n_blocks = n_blocks;
+    a.table_out = table_out;
+    a.tos = table_out_stride;
+    a.ring = ring;
+    a.pairs = pairs;
+    a.max_pairs = max_pairs;
+    a.state_out = state_out;
+    a.chunks = (n_blocks + tune::kCompactChunk - 1) / tune::kCompactChunk;
+    a.used = static_cast<uint8_t *>(workspace);
+    a.bits = reinterpret_cast<uint64_t *>(a.used + a.chunks * tune::kCompactChunk);
+    a.chunk = reinterpret_cast<int32_t *>(a.bits + a.chunks * (tune::kCompactChunk / 64));
+    a.before = reinterpret_cast<uint16_t *>(a.chunk + a.chunks + 1);
+    L.grid = int64_t(host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus) * tune::kPageBlocksPerCu;
+    L.stream = stream;
+    host::launch_events(&L.ev_begin, &L.ev_end);
+    if (host::injected_launch_failure())
+        return RK_ERR_HIP;
+    return launch_compact(L);
+}
+
+int rk_copy_blocks(const rk_block_cache *caches, int n_caches, const int32_t *pairs, int64_t n_pairs, void *stream)
+{
+    if (n_caches < 0 || n_pairs < 0 || (n_caches > 0 && !caches))
+        return RK_ERR_INVALID_ARGUMENT;
+    if (n_pairs > 0x7fffffff)
+        return RK_ERR_UNSUPPORTED;
+    if ((n_pairs > 0 && !pairs) || !aligned(pairs, 4))
+        return RK_ERR_INVALID_ARGUMENT;
+    int64_t longest = 0;
+    const auto of = [](const rk_block_cache &c) {
+        return span(c.data, c.n_blocks > 0 ? (c.n_blocks - 1) * c.block_stride + c.block_bytes : 0);
+    };
+    for (int i = 0; i < n_caches; ++i) {
+        const rk_block_cache &c = caches[i];
+        if (c.n_blocks < 0 || c.block_bytes < 0 || !lines_fit(c.block_bytes, c.n_blocks, c.block_stride) ||
+            (c.n_blocks > 1 && c.block_stride < c.block_bytes) || (c.n_blocks > 0 && c.block_bytes > 0 && !c.data) ||
+            overlap(of(c), span(pairs, n_pairs * 8)))
+            return RK_ERR_INVALID_ARGUMENT;
+        if (c.n_blocks > 0x7fffffff || c.block_bytes > (int64_t(1) << 29))
+            return RK_ERR_UNSUPPORTED;
+        longest = c.n_blocks > 0 && c.block_bytes > longest ? c.block_bytes : longest;
+    }
+    if (n_pairs == 0 || longest == 0)
+        return RK_OK;
+    const int cus = host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus;
+    if (host::debug_enabled())
+        std::fprintf(stderr, "rk_copy_blocks: caches=%d pairs=%lld bytes=%lld\n", n_caches, (long long)n_pairs,
+                     (long long)longest);
+    if (host::injected_launch_failure())
+        return RK_ERR_HIP;
+    for (int from = 0; from < n_caches; from += tune::kCopyCaches) {
+        CopyLaunch L;
+        std::memset(static_cast<void *>(&L), 0, sizeof L);
+        CopyArgs &a = L.a;
+        int64_t bytes = 0;
+        for (int i = from; i < n_caches && a.caches < tune::kCopyCaches; ++i) {
+            const rk_block_cache &c = caches[i];
+            a.cache[a.caches++] = CopyCache{static_cast<char *>(c.data), c.block_stride, c.block_bytes, c.n_blocks};
+            bytes = c.block_bytes > bytes ? c.block_bytes : bytes;
+        }
+        if (bytes == 0)
+            continue;
+        a.pairs = pairs;
+        a.n_pairs = n_pairs;
+        a.chunks = int((bytes + tune::kCopyChunk - 1) / tune::kCopyChunk);
+        // a thread block a pair of a cache's chunk while that leaves at most kCopyBlocksPerCu blocks a CU
+        const int64_t most = int64_t(cus) * tune::kCopyBlocksPerCu / (int64_t(a.caches) * a.chunks);
+        const int64_t group = n_pairs < tune::kPageBlock ? n_pairs : tune::kPageBlock;
+        a.parts = int(most < 1 ? 1 : most < group ? most : group);
+        int64_t groups = (n_pairs + tune::kPageBlock - 1) / tune::kPageBlock;
+        const int64_t fit = most / a.parts < 1 ? 1 : most / a.parts;
+        groups = groups < fit ? groups : fit;
+        L.grid_x = groups * a.parts;
+        L.stream = stream;
+        if (from == 0)
+            host::launch_events(&L.ev_begin, &L.ev_end);
+        const int rc = launch_copy(L);
+        if (rc)
+            return rc;
+    }
+    return RK_OK;
 }
 
 }  // extern "C"

@@ -81,6 +81,42 @@ int plan_verify(int prob_dtype, int64_t n, int64_t req, int cus, VerifyPlan *p)
     return ST_OK;
 }
 
+int plan_beams(int dtype, int64_t n, int64_t req, int64_t beams, int64_t count, int cus, BeamPlan *p)
+{
+    *p = BeamPlan();
+    if (!dtype_known(dtype) || n < 1 || req < 0 || beams < 1 || count < 1)
+        return ST_INVALID;
+    if (!prob_dtype_ok(dtype) || n > kMaxLine || beams > tune::kBeamLines || count > tune::kBeamMost ||
+        req > kMaxLines / beams)
+        return ST_UNSUPPORTED;
+    if (req == 0)
+        return ST_OK;
+    const int64_t lines = req * beams, tiles = (n + tune::kBeamTile - 1) / tune::kBeamTile;
+    int64_t waves = int64_t(cus > 0 ? cus : tune::kDefaultCus) * tune::kBeamWavesPerCu / lines;
+    waves = waves < 1 ? 1 : waves < tiles ? waves : tiles;
+    const int64_t each = (tiles + waves - 1) / waves;
+    p->chunks = (tiles + each - 1) / each;
+    p->per_wave = each * tune::kBeamTile;
+    p->items = lines * p->chunks;
+    p->grid = (p->items + tune::kBeamBlock / 64 - 1) / (tune::kBeamBlock / 64);
+    if (p->grid > kMaxThreads / tune::kBeamBlock || req > kMaxThreads / tune::kBeamBlock)
+        return ST_UNSUPPORTED;
+    p->ws_bytes = round_up_256(size_t(p->items) * (12 + 8 * size_t(count)));
+    return ST_OK;
+}
+
+size_t fork_ws_bytes(int64_t rows, int64_t rows_out, int64_t max_blocks, int64_t n_blocks)
+{
+    const int64_t segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
+    return round_up_256(32 + 4 * size_t(2 * rows + rows_out + rows * segs + n_blocks));
+}
+
+size_t compact_ws_bytes(int64_t n_blocks)
+{
+    const size_t chunks = size_t((n_blocks + tune::kCompactChunk - 1) / tune::kCompactChunk);
+    return round_up_256(chunks * (tune::kCompactChunk + tune::kCompactChunk / 64 * 10) + (chunks + 1) * 4);
+}
+
 Divider make_divider(uint32_t d)
 {
     Divider r{d, 0, 0};

@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <vector>
 
 #include "rk.h"
 
@@ -24,6 +25,12 @@ decltype(&rk_softmax) p_softmax;
 decltype(&rk_draft_verify) p_draft_verify;
 decltype(&rk_block_tables) p_block_tables;
 decltype(&rk_slot_map) p_slot_map;
+decltype(&rk_beam_select) p_beam_select;
+decltype(&rk_fork_blocks) p_fork_blocks;
+decltype(&rk_compact_blocks) p_compact_blocks;
+decltype(&rk_copy_blocks) p_copy_blocks;
+decltype(&rk_linear_recurrence) p_recurrence;
+decltype(&rk_linear_recurrence_backward) p_recurrence_backward;
 
 // Thrown with a Python error set.
 struct Refused {};
@@ -61,7 +68,7 @@ struct Call {
 
     static c10::Device device_of(const char *name, const char *what, PyObject *o)
     {
-        if (!p_slot_map) {
+        if (!p_recurrence_backward) {
             PyErr_SetString(PyExc_RuntimeError, "bind() has not been called");
             throw Refused();
         }
@@ -97,11 +104,11 @@ struct Call {
         return o == Py_None ? nullptr : flat(what, o, n, dtype);
     }
 
-    // A 2-d tensor whose lines are contiguous.
+    // A 2-d tensor whose lines are contiguous (of no elements: of any strides).
     const at::Tensor &lines(const char *what, PyObject *o) const
     {
         const at::Tensor &t = here(what, o);
-        if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
+        if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1 && t.numel() > 0))
             refuse("%s: %s takes two dims, the second contiguous", name, what);
         return t;
     }
@@ -146,6 +153,13 @@ struct Call {
     }
 };
 
+// The tokens of a recurrence: (sequences, tokens, channels), or (tokens,
+// channels) where the sequences are packed, channels contiguous.
+struct Tokens {
+    rk_rows rows;
+    const at::Tensor *t;
+};
+
 int64_t integer(PyObject *o)
 {
     const long long v = PyLong_AsLongLong(o);
@@ -171,7 +185,7 @@ void *handle(PyObject *o)
 
 PyObject *status(int rc) { return PyLong_FromLong(rc); }
 
-// Softmax has no backward pass: where gradients are recorded, what requires
+// Calls without a backward pass: where gradients are recorded, what requires
 // them is refused rather than left without.
 void no_gradient(const char *name, const char *what, PyObject *o)
 {
@@ -276,13 +290,229 @@ PyObject *slot_map(PyObject *const *a)
                              integer(a[6]), code, capacity, sp, pp, qp, tp, handle(a[0])));
 }
 
-// bind(softmax, draft_verify, block_tables, slot_map): the library's functions.
+Tokens tokens_of(const Call &c, const char *what, PyObject *o, const at::Tensor *like, at::ScalarType dtype, bool packed)
+{
+    const at::Tensor &t = c.here(what, o);
+    if (t.dim() != (packed ? 2 : 3) || (t.size(-1) > 1 && t.stride(-1) != 1))
+        refuse("%s: %s takes %s", c.name, what,
+               packed ? "two dims, tokens and contiguous channels" : "three dims, sequences, tokens and contiguous channels");
+    if (like && t.sizes() != like->sizes())
+        refuse("%s: %s takes the gate's shape", c.name, what);
+    if (t.scalar_type() != dtype)
+        refuse("%s: %s takes %s", c.name, what, type_name(dtype));
+    return Tokens{rk_rows{t.data_ptr(), packed ? 0 : t.stride(0), t.stride(-2)}, &t};
+}
+
+// What a recurrence's calls share: their extents, gates, inputs and offsets.
+struct Recurrence {
+    Tokens gate, x;
+    int x_code, gate_code, kind, blend;
+    at::ScalarType x_dtype;
+    bool packed;
+    int64_t n_seq, tokens, channels;
+    const int32_t *starts;
+
+    Recurrence(const Call &c, PyObject *gate_o, PyObject *x_o, PyObject *kind_o, PyObject *blend_o, PyObject *starts_o)
+    {
+        packed = starts_o != Py_None;
+        const at::Tensor &g = c.here("gate", gate_o), &v = c.here("x", x_o);
+        gate_code = c.prob_code("gate", g);
+        x_code = c.prob_code("x", v);
+        x_dtype = v.scalar_type();
+        gate = tokens_of(c, "gate", gate_o, nullptr, g.scalar_type(), packed);
+        x = tokens_of(c, "x", x_o, gate.t, x_dtype, packed);
+        kind = small_integer(kind_o);
+        blend = small_integer(blend_o);
+        tokens = g.size(-2);
+        channels = g.size(-1);
+        n_seq = packed ? c.here("starts", starts_o).numel() - 1 : g.size(0);
+        if (n_seq < 0)
+            refuse("%s: %s takes an offset more than sequences", c.name, "starts");
+        starts = static_cast<const int32_t *>(c.flat_or_null("starts", starts_o, n_seq + 1, at::kInt));
+    }
+
+    // A float32 line of channels for each of n sequences.
+    float *states(const Call &c, const char *what, PyObject *o, int64_t n) const
+    {
+        if (o == Py_None)
+            return nullptr;
+        const at::Tensor &t = c.here(what, o);
+        if (t.dim() != 2 || t.size(0) != n || t.size(1) != channels || t.scalar_type() != at::kFloat || !t.is_contiguous()) {
+            PyErr_Format(PyExc_ValueError, "%s: %s takes %lld contiguous float32 lines of %lld channels", c.name, what,
+                         (long long)n, (long long)channels);
+            throw Refused();
+        }
+        return static_cast<float *>(t.data_ptr());
+    }
+};
+
+// linear_recurrence(stream, gate, x, state, kind, blend, starts, sources, out, state_out, workspace)
+PyObject *linear_recurrence(PyObject *const *a)
+{
+    Call c("linear_recurrence", "gate", a[1]);
+    const Recurrence r(c, a[1], a[2], a[4], a[5], a[6]);
+    const Tokens out = tokens_of(c, "out", a[8], r.gate.t, r.x_dtype, r.packed);
+    const auto *sources = static_cast<const int32_t *>(c.flat_or_null("sources", a[7], r.n_seq, at::kInt));
+    int64_t lines = r.n_seq;
+    if (sources && a[3] != Py_None) {
+        const at::Tensor &t = c.here("state", a[3]);
+        lines = t.dim() > 0 ? t.size(0) : 0;
+    }
+    const float *state = r.states(c, "state", a[3], lines);
+    float *last = r.states(c, "state_out", a[9], r.n_seq);
+    const Buffer ws = c.workspace(a[10]);
+    return status(p_recurrence(r.x_code, r.gate_code, r.kind, r.blend, &r.gate.rows, &r.x.rows, state, lines, sources,
+                               r.starts, r.n_seq, r.tokens, r.channels, &out.rows, last, ws.at, ws.bytes, handle(a[0])));
+}
+
+// linear_recurrence_backward(stream, gate, x, out, dout, state, dstate_out, kind, blend, starts, dgate, dx, dstate, workspace)
+PyObject *linear_recurrence_backward(PyObject *const *a)
+{
+    Call c("linear_recurrence_backward", "gate", a[1]);
+    const Recurrence r(c, a[1], a[2], a[7], a[8], a[9]);
+    const Tokens out = tokens_of(c, "out", a[3], r.gate.t, r.x_dtype, r.packed),
+                 dout = tokens_of(c, "dout", a[4], r.gate.t, r.x_dtype, r.packed),
+                 dgate = tokens_of(c, "dgate", a[10], r.gate.t, r.gate.t->scalar_type(), r.packed),
+                 dx = tokens_of(c, "dx", a[11], r.gate.t, r.x_dtype, r.packed);
+    const float *state = r.states(c, "state", a[5], r.n_seq), *dlast = r.states(c, "dstate_out", a[6], r.n_seq);
+    float *dstate = r.states(c, "dstate", a[12], r.n_seq);
+    const Buffer ws = c.workspace(a[13]);
+    return status(p_recurrence_backward(r.x_code, r.gate_code, r.kind, r.blend, &r.gate.rows, &r.x.rows, &out.rows, &dout.rows,
+                                        state, dlast, r.starts, r.n_seq, r.tokens, r.channels, &dgate.rows, &dx.rows, dstate,
+                                        ws.at, ws.bytes, handle(a[0])));
+}
+
+// beam_select(stream, logits, scores, count, ended, end_token, best, tokens, parents, workspace)
+PyObject *beam_select(PyObject *const *a)
+{
+    no_gradient("beam_select", "logits", a[1]);
+    no_gradient("beam_select", "scores", a[2]);
+    Call c("beam_select", "logits", a[1]);
+    const at::Tensor &x = c.lines("logits", a[1]), &scores = c.here("scores", a[2]);
+    const int code = c.prob_code("logits", x);
+    if (scores.dim() != 2 || scores.numel() != x.size(0))
+        refuse("%s: %s takes requests times beams, a score for every line", c.name, "scores");
+    const int64_t req = scores.size(0), beams = scores.size(1);
+    const int count = small_integer(a[3]);
+    if (beams > 0x7fffffff)
+        return status(RK_ERR_UNSUPPORTED);
+    if (beams == 0 || count < 1)
+        return status(RK_ERR_INVALID_ARGUMENT);
+    const at::Tensor &tokens = c.here("tokens", a[7]);
+    const int tok = c.id_code("tokens", tokens);
+    const auto *sp = static_cast<const float *>(c.flat("scores", a[2], req * beams, at::kFloat));
+    const uint8_t *ep = nullptr;
+    if (a[4] != Py_None) {
+        const at::Tensor &e = c.here("ended", a[4]);
+        ep = static_cast<const uint8_t *>(c.flat("ended", a[4], req * beams, e.scalar_type() == at::kByte ? at::kByte : at::kBool));
+    }
+    auto *bp = static_cast<float *>(c.flat("best", a[6], req * count, at::kFloat));
+    auto *tp = c.flat("tokens", a[7], req * count, tokens.scalar_type());
+    auto *pp = static_cast<int32_t *>(c.flat("parents", a[8], req * count, at::kInt));
+    const Buffer ws = c.workspace(a[9]);
+    return status(p_beam_select(code, tok, x.data_ptr(), x.stride(0), x.size(1), req, int(beams), sp, ep, integer(a[5]), count,
+                                bp, tp, pp, ws.at, ws.bytes, handle(a[0])));
+}
+
+int64_t *state_out_of(const Call &c, PyObject *o) { return static_cast<int64_t *>(c.flat("state_out", o, 4, at::kLong)); }
+
+// fork_blocks(stream, parents, lens, block_size, held, table, ring, state, n_blocks, table_out, held_out, lens_out, pairs,
+//             state_out, workspace)
+PyObject *fork_blocks(PyObject *const *a)
+{
+    Call c("fork_blocks", "parents", a[1]);
+    const int64_t out = c.here("parents", a[1]).numel(), rows = c.here("lens", a[2]).numel(), places = c.here("ring", a[6]).numel();
+    const at::Tensor &table = c.table(a[5], rows), &to = c.lines("table_out", a[9]);
+    if (to.size(0) != out || to.size(1) != table.size(1) || to.scalar_type() != at::kInt)
+        refuse("%s: %s takes an int32 line of the table's width for every parent", c.name, "table_out");
+    const at::Tensor &state = c.here("state", a[7]);
+    if (state.scalar_type() != at::kLong || !state.is_contiguous() || state.numel() < 2)
+        refuse("%s: %s takes int64 head and tail", c.name, "state");
+    const int64_t width = table.size(1);
+    if (width > 0x7fffffff)
+        return status(RK_ERR_UNSUPPORTED);
+    const auto *par = static_cast<const int32_t *>(c.flat("parents", a[1], out, at::kInt));
+    const auto *lens = static_cast<const int32_t *>(c.flat("lens", a[2], rows, at::kInt));
+    const auto *held = static_cast<const int32_t *>(c.flat("held", a[4], rows, at::kInt));
+    auto *ring = static_cast<int32_t *>(c.flat("ring", a[6], places, at::kInt));
+    auto *ho = static_cast<int32_t *>(c.flat("held_out", a[10], out, at::kInt));
+    auto *lo = static_cast<int32_t *>(c.flat("lens_out", a[11], out, at::kInt));
+    auto *pairs = static_cast<int32_t *>(c.flat("pairs", a[12], 2 * out, at::kInt));
+    auto *so = state_out_of(c, a[13]);
+    const Buffer ws = c.workspace(a[14]);
+    return status(p_fork_blocks(par, out, lens, rows, small_integer(a[3]), held, static_cast<const int32_t *>(table.data_ptr()),
+                                table.stride(0), int(width), ring, places, static_cast<const int64_t *>(state.data_ptr()),
+                                integer(a[8]), static_cast<int32_t *>(to.data_ptr()), to.stride(0), ho, lo, pairs, so, ws.at,
+                                ws.bytes, handle(a[0])));
+}
+
+// compact_blocks(stream, held, table, ring, n_blocks, table_out, pairs, state_out, workspace)
+PyObject *compact_blocks(PyObject *const *a)
+{
+    Call c("compact_blocks", "held", a[1]);
+    const int64_t rows = c.here("held", a[1]).numel(), places = c.here("ring", a[3]).numel();
+    const at::Tensor &table = c.table(a[2], rows), &to = c.lines("table_out", a[5]), &pairs = c.here("pairs", a[6]);
+    if (to.sizes() != table.sizes() || to.scalar_type() != at::kInt)
+        refuse("%s: %s takes the table's shape, int32", c.name, "table_out");
+    if (pairs.numel() % 2)
+        refuse("%s: %s takes pairs", c.name, "pairs");
+    const int64_t width = table.size(1), most = pairs.numel() / 2;
+    if (width > 0x7fffffff)
+        return status(RK_ERR_UNSUPPORTED);
+    const auto *held = static_cast<const int32_t *>(c.flat("held", a[1], rows, at::kInt));
+    auto *ring = static_cast<int32_t *>(c.flat("ring", a[3], places, at::kInt));
+    auto *pp = static_cast<int32_t *>(c.flat("pairs", a[6], 2 * most, at::kInt));
+    auto *so = state_out_of(c, a[7]);
+    const Buffer ws = c.workspace(a[8]);
+    return status(p_compact_blocks(held, rows, static_cast<const int32_t *>(table.data_ptr()), table.stride(0), int(width),
+                                   integer(a[4]), static_cast<int32_t *>(to.data_ptr()), to.stride(0), ring, places, pp, most, so,
+                                   ws.at, ws.bytes, handle(a[0])));
+}
+
+// copy_blocks(stream, caches, pairs)
+PyObject *copy_blocks(PyObject *const *a)
+{
+    Call c("copy_blocks", "pairs", a[2]);
+    const int64_t n = c.here("pairs", a[2]).numel();
+    if (n % 2)
+        refuse("%s: %s takes pairs", c.name, "pairs");
+    const auto *pairs = static_cast<const int32_t *>(c.flat("pairs", a[2], n, at::kInt));
+    if (!PyList_Check(a[1]) && !PyTuple_Check(a[1])) {
+        PyErr_Format(PyExc_TypeError, "%s: caches takes a list or tuple of tensors", c.name);
+        throw Refused();
+    }
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[1]);
+    std::vector<rk_block_cache> caches;
+    caches.reserve(size_t(count));
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor &t = c.here("caches", PySequence_Fast_GET_ITEM(a[1], i));
+        if (t.dim() < 1)
+            refuse("%s: %s takes tensors of blocks", c.name, "caches");
+        int64_t whole = 1;                    // elements of a block, contiguous
+        for (int64_t d = t.dim() - 1; d > 0; --d) {
+            if (t.size(d) > 1 && t.stride(d) != whole)
+                refuse("%s: %s takes tensors whose blocks are contiguous", c.name, "caches");
+            whole *= t.size(d);
+        }
+        const int64_t size = int64_t(t.element_size());
+        caches.push_back(rk_block_cache{t.data_ptr(), t.stride(0) * size, whole * size, t.size(0)});
+    }
+    return status(p_copy_blocks(caches.data(), int(count), pairs, n / 2, handle(a[0])));
+}
+
+// bind(softmax, draft_verify, ...): the library's functions, in the order above.
 PyObject *bind(PyObject *const *a)
 {
     p_softmax = reinterpret_cast<decltype(p_softmax)>(handle(a[0]));
     p_draft_verify = reinterpret_cast<decltype(p_draft_verify)>(handle(a[1]));
     p_block_tables = reinterpret_cast<decltype(p_block_tables)>(handle(a[2]));
     p_slot_map = reinterpret_cast<decltype(p_slot_map)>(handle(a[3]));
+    p_beam_select = reinterpret_cast<decltype(p_beam_select)>(handle(a[4]));
+    p_fork_blocks = reinterpret_cast<decltype(p_fork_blocks)>(handle(a[5]));
+    p_compact_blocks = reinterpret_cast<decltype(p_compact_blocks)>(handle(a[6]));
+    p_copy_blocks = reinterpret_cast<decltype(p_copy_blocks)>(handle(a[7]));
+    p_recurrence = reinterpret_cast<decltype(p_recurrence)>(handle(a[8]));
+    p_recurrence_backward = reinterpret_cast<decltype(p_recurrence_backward)>(handle(a[9]));
     Py_RETURN_NONE;
 }
 
@@ -315,7 +545,10 @@ PyMethodDef method(const char *name)
     return m;
 }
 
-PyMethodDef methods[] = {method<bind, 4>("bind"), method<softmax, 5>("softmax"), method<draft_verify, 11>("draft_verify"),
+PyMethodDef methods[] = {method<bind, 10>("bind"), method<beam_select, 10>("beam_select"),
+                         method<fork_blocks, 15>("fork_blocks"), method<compact_blocks, 9>("compact_blocks"),
+                         method<copy_blocks, 3>("copy_blocks"), method<linear_recurrence, 11>("linear_recurrence"),
+                         method<linear_recurrence_backward, 14>("linear_recurrence_backward"), method<softmax, 5>("softmax"), method<draft_verify, 11>("draft_verify"),
                          method<block_tables, 10>("block_tables"), method<slot_map, 12>("slot_map"), PyMethodDef{}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", "Calls of the serving operators.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -18,24 +18,6 @@
 namespace rk {
 namespace {
 
-__device__ __forceinline__ int blocks_of(int len, const Divider &d)
-{
-    return len > 0 ? int(divide(uint32_t(len - 1), d)) + 1 : 0;
-}
-
-// v modulo size (1 <= size < 2^31), not negative.  A 64-bit remainder takes
-// over a hundred instructions, so counters that fit 32 bits do without.
-__device__ __forceinline__ int64_t ring_place(int64_t v, int64_t size)
-{
-    if (v >= 0 && v < (int64_t(1) << 32))
-        return uint32_t(v) % uint32_t(size);
-    const int64_t m = v % size;
-    return m < 0 ? m + size : m;
-}
-
-// A place of the ring, 0 <= at < 2 * size.
-__device__ __forceinline__ int64_t wrap(int64_t at, int64_t size) { return at >= size ? at - size : at; }
-
 // What one request asks for.
 struct Ask {
     int held, need, over;     // blocks it holds and gets to hold; blocks beyond the table's width
@@ -76,21 +58,6 @@ struct Asks {
             q[i].over = want - q[i].need;
             q[i].held = held[i] < 0 ? 0 : held[i] > a.max_blocks ? a.max_blocks : held[i];
         }
-    }
-};
-
-// The ring before and after the call.
-struct Ring {
-    int64_t there, head;      // blocks that were free, and the place of the first
-    int64_t given, taken;     // blocks that come and go
-
-    __device__ __forceinline__ Ring(int64_t head_, int64_t tail, int64_t size, int64_t gives, int64_t takes)
-    {
-        head = ring_place(head_, size);
-        there = tail - head_;
-        there = there < 0 ? 0 : there > size ? size : there;
-        given = gives < size - there ? gives : size - there;
-        taken = takes < there + given ? takes : there + given;
     }
 };
 

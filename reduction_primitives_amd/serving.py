@@ -2,7 +2,10 @@
 
 ``softmax`` turns logits into probabilities, ``draft_verify`` verifies drafted
 tokens against them, ``block_tables`` brings block tables to the requests'
-lengths and ``slot_map`` lays out the next batch.  Like the reductions and scans
+lengths and ``slot_map`` lays out the next batch.  ``beam_select`` chooses the
+beams a search goes on with, ``fork_blocks`` gives them the block tables of the
+beams they come from, ``copy_blocks`` copies the blocks that are then theirs alone,
+and ``compact_blocks`` brings the blocks in use together.  Like the reductions and scans
 of the package they marshal torch tensors into the C ABI (include/rk.h has
 each call's definition); everything stays on the device, so a step of them
 can be captured into a HIP graph.
@@ -23,7 +26,8 @@ _lib = N.load()
 from . import _serving as _calls  # noqa: E402  (checks tensors and passes their addresses to the library)
 
 _calls.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value
-              for f in ("rk_softmax", "rk_draft_verify", "rk_block_tables", "rk_slot_map")))
+              for f in ("rk_softmax", "rk_draft_verify", "rk_block_tables", "rk_slot_map", "rk_beam_select", "rk_fork_blocks",
+                        "rk_compact_blocks", "rk_copy_blocks", "rk_linear_recurrence", "rk_linear_recurrence_backward")))
 
 _CODES = {torch.float32: N.RK_F32, torch.bfloat16: N.RK_BF16, torch.float16: N.RK_F16}
 _current_stream = torch._C._cuda_getCurrentRawStream
@@ -155,3 +159,104 @@ def slot_map(lens, fresh, block_size, table, held, n_blocks, capacity=None, slot
     if rc:
         raise N.RkError(rc, "rk_slot_map")
     return slots, positions, requests, starts
+
+
+def beam_select(logits, scores, count=None, ended=None, end_token=None, token_dtype=None, best=None, tokens=None,
+                parents=None, workspace=None, stream=None):
+    """The best continuations of every request's beams (rk_beam_select).
+    logits: a line for each beam, those of a request one after the other;
+    scores: float32 (requests, beams); count: how many to keep (None: as many
+    as there are beams, at most 64); ended: bool (requests, beams), beams that
+    go on as they are, by end_token.  Returns (best, tokens, parents), each
+    (requests, count), best first: scores, tokens and the lines they continue.
+    There is no backward pass: tensors that require grad are refused where
+    gradients are recorded."""
+    handle = _handle("beam_select", "logits", logits, stream)
+    if ended is not None and end_token is None:
+        raise ValueError("beam_select: ended needs end_token, the token an ended beam goes on with")
+    if scores.dim() != 2:
+        raise ValueError("beam_select: scores takes requests times beams, a score for every line")
+    req, beams = scores.shape
+    if count is None:
+        count = beams
+    if count < 1 or beams < 1:
+        raise ValueError("beam_select: takes one beam and one candidate to keep at least")
+    if best is None:
+        best = _empty((req, count), torch.float32, logits, stream)
+    if tokens is None:
+        tokens = _empty((req, count), token_dtype or torch.int64, logits, stream)
+    elif token_dtype is not None and tokens.dtype is not token_dtype:
+        raise ValueError("beam_select: tokens takes token_dtype")
+    if parents is None:
+        parents = _empty((req, count), torch.int32, logits, stream)
+    if workspace is None and logits.dim() == 2:
+        workspace = _workspace(N.rk_beam_select_workspace_size,
+                               (_code("beam_select", "logits", logits.dtype), logits.shape[-1], req, beams, count), logits, stream)
+    rc = _calls.beam_select(handle, logits, scores, count, ended, 0 if end_token is None else end_token, best, tokens, parents,
+                            workspace)
+    if rc:
+        raise N.RkError(rc, "rk_beam_select")
+    return best, tokens, parents
+
+
+def fork_blocks(parents, lens, block_size, held, table, ring, state, n_blocks, table_out=None, held_out=None, lens_out=None,
+                pairs=None, state_out=None, workspace=None, stream=None):
+    """Make the rows of a block table those of their parents (rk_fork_blocks),
+    ring in place.  parents: int32, the old row each new one goes on from, -1 for
+    an empty one; lens, held: tokens and blocks of the old rows; n_blocks: the
+    blocks of the pool; state: int64 (head, tail) of the ring, and two places
+    more (4 in all) where it is updated in place, as it is unless state_out (4
+    int64) is given.  Returns (table_out, held_out, lens_out, pairs, state_out);
+    pairs: (source, fresh block) of the rows whose last block is to be copied
+    (copy_blocks)."""
+    handle = _handle("fork_blocks", "parents", parents, stream)
+    n = parents.numel()
+    width = table.shape[-1] if table.dim() == 2 else 0
+    if table_out is None:
+        table_out = _empty((n, width), torch.int32, parents, stream)
+    if held_out is None:
+        held_out = _empty((n,), torch.int32, parents, stream)
+    if lens_out is None:
+        lens_out = _empty((n,), torch.int32, parents, stream)
+    if pairs is None:
+        pairs = _empty((n, 2), torch.int32, parents, stream)
+    state_out = state if state_out is None else state_out
+    if workspace is None:
+        workspace = _workspace(N.rk_fork_blocks_workspace_size, (lens.numel(), n, min(width, 2 ** 31 - 1), n_blocks), parents, stream)
+    rc = _calls.fork_blocks(handle, parents, lens, block_size, held, table, ring, state, n_blocks, table_out, held_out, lens_out,
+                            pairs, state_out, workspace)
+    if rc:
+        raise N.RkError(rc, "rk_fork_blocks")
+    return table_out, held_out, lens_out, pairs, state_out
+
+
+def compact_blocks(held, table, ring, n_blocks, table_out=None, pairs=None, state_out=None, workspace=None, stream=None):
+    """Bring the blocks that block tables name to the lowest ids
+    (rk_compact_blocks), table (unless table_out is given) and ring in place:
+    every block no row names is free afterwards.  Returns (table_out, pairs,
+    state_out): pairs, of n_blocks // 2, holds the moves (copy_blocks) and -1
+    behind them; state_out the ring's head and tail, and the number of moves."""
+    handle = _handle("compact_blocks", "held", held, stream)
+    table_out = table if table_out is None else table_out
+    if pairs is None:
+        pairs = _empty((max(n_blocks, 0) // 2, 2), torch.int32, held, stream)
+    if state_out is None:
+        state_out = _empty((4,), torch.int64, held, stream)
+    if workspace is None:
+        workspace = _workspace(N.rk_compact_blocks_workspace_size, (n_blocks,), held, stream)
+    rc = _calls.compact_blocks(handle, held, table, ring, n_blocks, table_out, pairs, state_out, workspace)
+    if rc:
+        raise N.RkError(rc, "rk_compact_blocks")
+    return table_out, pairs, state_out
+
+
+def copy_blocks(caches, pairs, stream=None):
+    """Copy blocks inside caches (rk_copy_blocks): block pairs[i, 1] becomes
+    what block pairs[i, 0] is; pairs with an id outside a cache are left out.
+    caches: a list of tensors whose first dim counts the blocks, each block
+    contiguous; pairs: int32.  Returns caches."""
+    handle = _handle("copy_blocks", "pairs", pairs, stream)
+    rc = _calls.copy_blocks(handle, caches, pairs)
+    if rc:
+        raise N.RkError(rc, "rk_copy_blocks")
+    return caches

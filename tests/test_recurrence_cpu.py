@@ -1,0 +1,142 @@
+"""CPU tests of the gated linear recurrence: refusals, workspace sizes, and the
+plain forms the GPU tests compare with."""
+import numpy as np
+import pytest
+import torch
+
+from tests import recur_ref as ref
+
+FAKE = 0x1000000        # never dereferenced: every call below fails validation
+MB = 1 << 20
+
+
+def _rk():
+    import reduction_primitives_amd as rk
+    rk.load()
+    return rk
+
+
+BASE = dict(xd=0, gd=0, kind=2, blend=1, gate=(FAKE, 5000, 50), x=(FAKE + MB, 5000, 50), state=FAKE + 2 * MB, n_states=3,
+            sources=None, starts=None, n_seq=3, tokens=100, ch=50, out=(FAKE + 3 * MB, 5000, 50), last=FAKE + 4 * MB,
+            ws=FAKE + 8 * MB, ws_bytes=8 * MB)
+
+
+def forward(**args):
+    a = {**BASE, **args}
+    return _rk().rk_linear_recurrence(a["xd"], a["gd"], a["kind"], a["blend"], a["gate"], a["x"], a["state"], a["n_states"],
+                                      a["sources"], a["starts"], a["n_seq"], a["tokens"], a["ch"], a["out"], a["last"], a["ws"],
+                                      a["ws_bytes"], None)
+
+
+BACK = dict(dout=(FAKE + 5 * MB, 5000, 50), dlast=FAKE + 6 * MB, dgate=(FAKE + 7 * MB, 5000, 50), dx=(FAKE + 16 * MB, 5000, 50),
+            dstate=FAKE + 17 * MB)
+
+
+def backward(**args):
+    a = {**BASE, **BACK, **args}
+    return _rk().rk_linear_recurrence_backward(a["xd"], a["gd"], a["kind"], a["blend"], a["gate"], a["x"], a["out"], a["dout"],
+                                               a["state"], a["dlast"], a["starts"], a["n_seq"], a["tokens"], a["ch"], a["dgate"],
+                                               a["dx"], a["dstate"], a["ws"], a["ws_bytes"], None)
+
+
+SHARED = [
+    (dict(xd=9), 1), (dict(gd=-1), 1), (dict(xd=3, gd=3), 2), (dict(gd=1), 2), (dict(xd=1, gd=2), 2), (dict(kind=3), 1), (dict(kind=-1), 1),
+    (dict(blend=2), 1), (dict(n_seq=-1), 1), (dict(tokens=-1), 1), (dict(ch=-1), 1), (dict(n_seq=1 << 31), 2), (dict(tokens=1 << 31), 2),
+    (dict(ch=1 << 31), 2), (dict(gate=None), 1), (dict(x=None), 1), (dict(gate=(None, 5000, 50)), 1), (dict(x=(None, 5000, 50)), 1),
+    (dict(gate=(FAKE + 2, 5000, 50)), 1), (dict(x=(FAKE + 1, 5000, 50)), 1), (dict(gate=(FAKE, -1, 50)), 1), (dict(x=(FAKE, 5000, 1 << 60)), 1),
+    (dict(state=FAKE + 2), 1), (dict(starts=FAKE + 2), 1),
+]
+
+
+@pytest.mark.parametrize("args,code", SHARED + [
+    (dict(out=None), 1), (dict(out=(None, 5000, 50)), 1), (dict(last=None), 1), (dict(last=FAKE + 2), 1), (dict(sources=FAKE + 2), 1),
+    (dict(sources=FAKE + 9 * MB, state=None), 1), (dict(n_states=-1), 1),
+    (dict(out=(FAKE + 3 * MB, 5000, 49)), 1), (dict(out=(FAKE + 3 * MB, 4999, 50)), 1), (dict(out=(FAKE + 3 * MB, 0, 50)), 1),   # folded
+    (dict(out=(FAKE + 200, 5000, 50)), 1), (dict(out=(FAKE + MB + 4, 5000, 50)), 1),                # neither in place nor beside it
+    (dict(out=(FAKE, 5000, 50), xd=1), 1),                                                         # in place of a wider type
+    (dict(last=FAKE), 1), (dict(last=FAKE + 2 * MB + 4), 1), (dict(last=FAKE + 3 * MB), 1),
+    (dict(last=FAKE + 2 * MB, sources=FAKE + 9 * MB), 1),                                          # in place, but by sources
+    (dict(out=(FAKE + 2 * MB, 5000, 50)), 1),
+    (dict(tokens=1000, gate=(FAKE, 50000, 50), x=(FAKE + MB, 50000, 50), out=(FAKE + 3 * MB, 50000, 50), ws=None), 1),
+])
+def test_forward_refusals(args, code):
+    assert forward(**args) == code
+
+
+@pytest.mark.parametrize("args,code", SHARED + [
+    (dict(out=None), 1), (dict(dout=None), 1), (dict(dgate=None), 1), (dict(dx=None), 1), (dict(dx=(None, 5000, 50)), 1),
+    (dict(dlast=FAKE + 1), 1), (dict(dstate=FAKE + 1), 1), (dict(dgate=(FAKE + 7 * MB, 10, 50)), 1),
+    (dict(dgate=(FAKE + 3 * MB, 5000, 50)), 1), (dict(dx=(FAKE + 3 * MB, 5000, 50)), 1),           # the outputs of the forward pass
+    (dict(dgate=(FAKE, 5000, 50), dx=(FAKE, 5000, 50)), 1), (dict(dx=(FAKE + 7 * MB + 4, 5000, 50)), 1),
+    (dict(dstate=FAKE + 6 * MB), 1), (dict(dstate=FAKE + 2 * MB), 1), (dict(dstate=FAKE + 16 * MB), 1),
+])
+def test_backward_refusals(args, code):
+    assert backward(**args) == code
+
+
+def long(**args):
+    """Extents that need a workspace, tensors apart."""
+    rows = lambda i: (FAKE + i * 64 * MB, 50 * 20000, 50)  # noqa: E731
+    return dict(tokens=20000, gate=rows(1), x=rows(2), out=rows(3), dout=rows(4), dgate=rows(5), dx=rows(6), ws=FAKE + 1024 * MB,
+                ws_bytes=64 * MB, **args)
+
+
+@pytest.mark.parametrize("args", [dict(ws=None), dict(ws=FAKE + 1024 * MB + 4), dict(ws_bytes=1000), dict(ws=FAKE + 64 * MB),
+                                  dict(ws=FAKE + 3 * 64 * MB), dict(ws=FAKE + 2 * MB), dict(ws=FAKE + 4 * MB)])
+def test_workspaces(args):
+    assert forward(**{**long(), **args}) == 1
+    if args != dict(ws=FAKE + 4 * MB):
+        assert backward(**{**long(), **args}) == 1
+
+
+def test_workspace_sizes():
+    size = _rk().rk_linear_recurrence_workspace_size
+    assert size(0, 0, 64, 1, 2048, 0) == 0 and size(0, 0, 1, 0, 5, 0) == 0 and size(0, 0, 0, 9, 5, 0) == 0
+    assert size(9, 0, 1, 100000, 64, 0) == 0 and size(1, 2, 1, 100000, 64, 0) == 0 and size(0, 0, -1, 5, 5, 0) == 0
+    assert size(1, 1, 1, 100000, 64, 0) % 256 == 0 and size(1, 1, 1, 100000, 64, 0) >= 390 * 896
+    assert size(0, 0, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 0) == 0
+
+
+def test_calls_of_nothing():
+    assert forward(n_seq=0) == 0 and forward(ch=0) == 0 and backward(n_seq=0) == 0
+    assert backward(tokens=0, dstate=None) == 0
+
+
+def test_tensor_refusals():
+    """What the Python calls refuse before the library sees it (CPU tensors
+    among it: there is no fallback)."""
+    rk = _rk()
+    x = torch.zeros(2, 3, 4)
+    for call in (lambda: rk.linear_recurrence(x, x), lambda: rk.linear_recurrence_backward(x, x, x, x)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
+    with pytest.raises(ValueError, match="kind"):
+        rk.linear_recurrence(x, x, kind="tanh")
+    with pytest.raises(ValueError, match="no gradient"):
+        rk.linear_recurrence(x.requires_grad_(), x, out=x)
+
+
+@pytest.mark.parametrize("kind", ["value", "log", "sigmoid"])
+@pytest.mark.parametrize("blend", [False, True])
+def test_plain_gradient_is_the_slope(kind, blend):
+    """The plain backward form against differences of the plain forward one."""
+    rng = np.random.default_rng(3)
+    starts = [0, 4, 4, 9]
+    gate, x, state = rng.standard_normal((9, 3)) * 0.5 - 0.2, rng.standard_normal((9, 3)), rng.standard_normal((3, 3))
+    wo, wl = rng.standard_normal((9, 3)), rng.standard_normal((3, 3))
+
+    def value(*v):
+        out, last, _, _ = ref.forward(v[0], v[1], kind, blend, starts, v[2])
+        return (out * wo).sum() + (last * wl).sum()
+
+    base = [gate, x, state]
+    out = ref.forward(gate, x, kind, blend, starts, state)[0]
+    grads, _ = ref.backward(gate, x, out, wo, kind, blend, starts, state, wl)
+    for i, g in enumerate(grads):
+        for at in np.ndindex(g.shape):
+            step = []
+            for s in (1e-6, -1e-6):
+                moved = [b.copy() for b in base]
+                moved[i][at] += s
+                step.append(value(*moved))
+            assert abs((step[0] - step[1]) / 2e-6 - g[at]) < 1e-7
