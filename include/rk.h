@@ -90,14 +90,12 @@
  * variable RK_DEBUG is set.
  *
  * Waits inside a launch: block 0 of a whole-array pass waits for the other
- * blocks' partials, and a scan tile (a linear recurrence's among them) waits
- * for its predecessors' prefixes.  No
+ * blocks' partials, and a scan tile waits for its predecessors' prefixes.  No
  * block waits on the block that waits for it, so these waits end; as a
  * safety net each is bounded (about a second).  A wait that gives up stores
  * no result (out keeps its previous contents; a scan's outputs after that
  * tile are wrong) and is counted: HOST mode then returns RK_ERR_HIP, and
- * rk_stream_timeouts reports the count for OVERWRITE, FOLD, scan and
- * recurrence calls.
+ * rk_stream_timeouts reports the count for OVERWRITE, FOLD and scan calls.
  */
 #ifndef RK_H
 #define RK_H
@@ -578,7 +576,7 @@ size_t rk_linear_recurrence_workspace_size(int x_dtype, int gate_dtype, int64_t 
  *   state_out   n_seq lines of channels float32: the last state, or the first one
  *               of a sequence without tokens.  May be state, without sources.
  * States, gates and their products are float32 and h is rounded once.  Nothing
- * passes from one sequence to another.  (Runs of up to 4096 tokens are folded
+ * passes from one sequence to another.  (Runs of up to 2048 tokens are folded
  * into one factor: a product of that many gates that leaves float32's range
  * makes a state infinite or NaN that need not be, unless the state before the
  * run is 0.)  Equal inputs give equal bits.  workspace: workspace_bytes >=
@@ -745,7 +743,9 @@ int rk_stream_timeouts(void *stream, uint64_t *count);
  * a tag or flag that never comes and gives up after `polls` polls, as a real
  * wait would after its bound; polls < 0 restores normal waits.  Every kernel
  * still ends; the calls store no result or wrong scan outputs, and count
- * their waits for rk_stream_timeouts.  Process-wide.  Returns an rk_status. */
+ * their waits for rk_stream_timeouts.  (Linear recurrences, whose blocks do the
+ * work of one they wait for in vain, do so once in every look-back, and their
+ * results stay.)  Process-wide.  Returns an rk_status. */
 int rk_debug_force_wait_timeout(int64_t polls);
 
 /* Test hook: the next `count` reduction, scan or serving calls that pass validation

@@ -4,5 +4,4 @@
 
 namespace rk {
 int launch_recur_bf16(const RecurLaunch &L) { return launch_recur_x<bf16_in>(L); }
-int take_recur_timeouts_bf16(uint64_t *count) { return take_recur_timeouts(count); }
 }  // namespace rk

@@ -4,5 +4,4 @@
 
 namespace rk {
 int launch_recur_f16(const RecurLaunch &L) { return launch_recur_x<f16_in>(L); }
-int take_recur_timeouts_f16(uint64_t *count) { return take_recur_timeouts(count); }
 }  // namespace rk

@@ -4,5 +4,4 @@
 
 namespace rk {
 int launch_recur_f32(const RecurLaunch &L) { return launch_recur_x<float>(L); }
-int take_recur_timeouts_f32(uint64_t *count) { return take_recur_timeouts(count); }
 }  // namespace rk

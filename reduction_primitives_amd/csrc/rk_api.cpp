@@ -581,9 +581,6 @@ int rk_stream_timeouts(void *stream, uint64_t *count)
         if (rc != RK_OK)
             return rc;
     }
-    for (auto take : {take_recur_timeouts_f32, take_recur_timeouts_bf16, take_recur_timeouts_f16})
-        if (take(count) != ST_OK)
-            return RK_ERR_HIP;
     return RK_OK;
 }
 

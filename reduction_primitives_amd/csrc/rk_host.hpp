@@ -6,12 +6,6 @@
 #include <cstdint>
 
 namespace rk {
-
-// The recurrences' waits that gave up, per translation unit: added to *count and cleared.
-int take_recur_timeouts_f32(uint64_t *count);
-int take_recur_timeouts_bf16(uint64_t *count);
-int take_recur_timeouts_f16(uint64_t *count);
-
 namespace host {
 
 int device_cus();                     // compute units of the current device, 0 without one

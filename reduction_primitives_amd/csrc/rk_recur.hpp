@@ -11,16 +11,30 @@ namespace rk {
 namespace tune {
 constexpr int kRecurBlock = 256;          // threads
 constexpr int kRecurVec = 4;              // channels of a lane (1 where there are fewer)
-constexpr int kRecurStrip = 64;           // most channels of a tile
-constexpr uint32_t kRecurSpinLimit = 1u << 24;   // look-back: sleeps per wait before giving up (about a second)
+// Most channels of a tile, so that a row of it is a whole 128-byte line of 16-bit
+// elements (32: 65536 x 2048 bf16 forward 272 us against 260, 512 x 64 x 2048
+// backward 250 against 178).
+constexpr int kRecurStrip = 64;
+// Sequences of so many tokens, up to so many of them, are columns of their own:
+// the tiles that run at the same time are then mostly other sequences', not the
+// ones a tile waits for (8 x 4096 x 2048 bf16 forward 109 us, one after the other
+// 125).
+constexpr int64_t kRecurApart = 512, kRecurApartMost = 4096;
+// Polls of a look-back (a microsecond each) before its block does the work of one
+// that has not been started.
+constexpr uint32_t kRecurPatience = 4096;
 }  // namespace tune
 
-// Most tokens of a lane: 16, or 8 where its inputs of 16 would not fit the
-// registers (the backward pass reads a gate and three of x's type).
+// Most tokens of a lane: what leaves the registers for kRecurWaves waves.  The bytes
+// that blocks have on their way bound the rate: with three waves a SIMD 8 x 4096 x
+// 2048 bf16 backward took 219 us, with four 204; forward with 12 tokens, gates
+// computed twice to make room for them, 16 x 4096 x 2048 took 233 us, with 8 and
+// gates kept 207.
 constexpr int recur_rows(int x_size, int gate_size, bool backward)
 {
-    return backward && gate_size + 3 * x_size > 8 ? 8 : 16;
+    return backward && gate_size + 3 * x_size > 8 ? 4 : 8;
 }
+constexpr int kRecurWaves = 4;            // of a SIMD
 
 enum RecurKind { RECUR_VALUE = 0, RECUR_LOG = 1, RECUR_SIGMOID = 2 };
 
@@ -52,13 +66,14 @@ struct RecurArgs {
     int tile_rows;                    // tokens of a tile
     bool linked;                      // a tile may begin inside a sequence: states pass from tile to tile
     uint32_t *ws;
-    uint32_t spin_limit, force_wait;
+    uint32_t patience;
+    bool force_help;                  // every block that looks back computes the tile before its own, too (a test hook)
 };
 
-// Look-back state of a tile: a line for its flag, then the map's factor and
-// addend and the state behind the tile, a float each for every channel.
-constexpr int kRecurHeaderBytes = 256;
-constexpr int kRecurRecBytes = 128 + 3 * 4 * tune::kRecurStrip;
+// Look-back state: two words for every channel of every tile, and kRecurBatch - 1
+// tiles' more that a look-back may load with the last one's.
+constexpr int kRecurBatch = 4;            // records that a wave has on their way at a time (8 spill registers)
+constexpr int kRecurRecBytes = 2 * 8 * tune::kRecurStrip;
 
 struct RecurPlan {
     int vec = 0, lanes_log2 = 0, per_lane = 0;   // channels of a lane, lanes across, tokens of a lane

@@ -153,8 +153,11 @@ int recur(const char *name, const Request &q, bool backward)
         return RK_ERR_INVALID_ARGUMENT;
 
     // rows: all tokens one after the other, or a sequence's, the sequences apart
+    // (several tiles of a sequence: apart, so that its neighbours on the device are other sequences' and not the
+    // ones it waits for)
     const bool one = q.starts || (e.seqs * e.tokens <= 0x7fffffff && follows(q.gate, e) && follows(q.x, e) &&
-                                  follows(q.h, e) && follows(q.dout, e) && follows(q.out, e) && follows(q.dgate, e));
+                                  follows(q.h, e) && follows(q.dout, e) && follows(q.out, e) && follows(q.dgate, e) &&
+                                  (e.tokens < tune::kRecurApart || e.seqs > tune::kRecurApartMost));
     RecurPlan p;
     const int rc = plan_recur(q.x_dtype, q.gate_dtype, one ? e.seqs * e.tokens : e.tokens, one ? 1 : e.seqs,
                               q.starts ? 0 : e.tokens, q.channels, backward, host::device_cus(), &p);
@@ -224,9 +227,8 @@ int recur(const char *name, const Request &q, bool backward)
     L.a.tile_rows = p.tile_rows;
     L.a.linked = p.linked;
     L.a.ws = static_cast<uint32_t *>(q.workspace);
-    const int64_t force = host::forced_wait();
-    L.a.spin_limit = force >= 0 ? uint32_t(force) : tune::kRecurSpinLimit;
-    L.a.force_wait = force >= 0 ? 1u : 0u;
+    L.a.patience = tune::kRecurPatience;
+    L.a.force_help = host::forced_wait() >= 0;
     L.gate_dtype = q.gate_dtype;
     L.backward = backward;
     L.stream = q.stream;

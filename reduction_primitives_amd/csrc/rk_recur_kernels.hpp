@@ -23,10 +23,20 @@
 // infinity nor a NaN passes from one sequence to the next, and a tile that holds
 // a reset hands on its state without waiting.
 //
+// Nothing depends on the order in which blocks start: one that would wait for a
+// tile that no block has begun computes that tile's map itself.
+//
 // States, products of gates and sums are float32; outputs are rounded once.
+//
+// Measured: 512 x 128 tokens x 2048 bf16, where no tile waits, 166 us forward (805 MB, 4.8
+// TB/s) and 512 x 64 backward 173 us (as many bytes); 16 x 4096 207, 1 x 65536 250
+// (3.2 TB/s), 16 x 2048 backward 202.  What the tiles wait for each other is what
+// is left: four blocks a CU hide a load's latency but not that as well.  (Blocks
+// that go from tile to tile with the next one's inputs loaded ahead took 337 us for
+// 1 x 65536: three blocks a CU then, and loads that come back in order behind the
+// look-back's.)
 #pragma once
 
-#include "rk_host.hpp"
 #include "rk_recur.hpp"
 #include "rk_serve_device.hpp"
 
@@ -36,6 +46,21 @@ namespace {
 constexpr int kB = tune::kRecurBlock;
 constexpr int kWaves = kB / 64;
 constexpr int kStrip = tune::kRecurStrip;
+
+// What is decoded from `raw` before and after this is not the same to the
+// compiler, which would otherwise keep the decoded values, two or four times as
+// many registers, in place of the raw ones.
+template <class T>
+__device__ __forceinline__ void decode_anew(T &raw)
+{
+    if constexpr (sizeof(T) >= 4) {
+        asm volatile("" : "+v"(raw));
+    } else {
+        uint32_t w = raw;
+        asm volatile("" : "+v"(w));
+        raw = T(w);
+    }
+}
 
 // V elements of a row.
 template <class T, int V> struct Pack {
@@ -88,32 +113,38 @@ template <class T, int V> struct Pack {
     }
 };
 
-// exp(t) to about an ulp: t log2(e) as a sum of two floats, the smaller one's
-// power of two to first order.  (One float alone is off by |t| 2^-24.)
-__device__ __forceinline__ float exp_of(float t)
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;   // log2(e) as a sum of two floats
+
+// exp(t) from its power of two.  A product t log2(e) of one float is off by
+// |t| 2^-24: enough for gates of 16 bits (FINE false), where t itself stands for
+// all within half of its last place; else the rest of the product is made good to
+// first order.
+template <bool FINE>
+__device__ __forceinline__ float mend_exp(float e, float t, float p)
 {
-    const float p = t * 1.44269502f;
-    const float q = __builtin_fmaf(t, 1.44269502f, -p) + t * 1.92596303e-8f;   // log2(e) = 1.44269502f + 1.92596303e-8
-    const float e = __builtin_amdgcn_exp2f(p);
-    // (far out p is infinite and q a NaN, where e is 0 or inf already)
-    return __builtin_fabsf(t) < 88.0f ? __builtin_fmaf(e, q * 0.693147182f, e) : e;
+    if constexpr (!FINE)
+        return e;
+    const float q = __builtin_fmaf(t, kLog2e, -p) + t * kLog2eRest;
+    return __builtin_fabsf(t) < 88.0f ? __builtin_fmaf(e, q * 0.693147182f, e) : e;   // (farther out q may be a NaN)
 }
 
 // a and 1 - a of a gate, the difference without cancellation where the gate is
 // given by its logarithm or logit.
-template <int KIND, bool WANT_W>
+template <int KIND, bool FINE, bool WANT_W>
 __device__ __forceinline__ void gate_of(float g, float &a, float &w)
 {
     if constexpr (KIND == RECUR_SIGMOID) {
-        const float e = exp_of(-__builtin_fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + e), f = e * r;
-        const bool up = g >= 0.0f;
-        a = up ? r : f;
-        w = up ? f : r;
+        // a = 1 / (1 + e), 1 - a = e a with e = exp(-g), kept finite (a NaN stays one)
+        const float p = -g * kLog2e;
+        const float e = mend_exp<FINE>(__builtin_amdgcn_exp2f(__builtin_elementwise_minimum(p, 126.0f)), -g, p);
+        a = __builtin_amdgcn_rcpf(1.0f + e);
+        w = e * a;
     } else if constexpr (KIND == RECUR_LOG) {
-        a = exp_of(g);
+        const float p = g * kLog2e;
+        a = mend_exp<FINE>(__builtin_amdgcn_exp2f(p), g, p);
         w = 1.0f - a;
         if constexpr (WANT_W) {
-            // exp(g) - 1 = g (1 + g/2 (1 + g/3 (1 + ...))): to 2^-25 of it below 1/4 with eight terms
+            // 1 - exp(g) = -g (1 + g/2 (1 + g/3 (1 + ...))): to 2^-25 of it below 1/4 with eight terms
             float s = 1.0f + g * 0.125f;
             s = 1.0f + g * (1.0f / 7.0f) * s;
             s = 1.0f + g * (1.0f / 6.0f) * s;
@@ -180,65 +211,138 @@ __device__ __forceinline__ void last_gradient(const RecurArgs &a, int64_t b, int
         s[k] = a.dlast ? a.dlast[b * a.channels + c + k] : 0.0f;
 }
 
-struct RecurRecord {
-    char *at;
-    __device__ RecurRecord(const RecurArgs &a, int64_t col, int64_t tile)
-        : at(reinterpret_cast<char *>(a.ws) + kRecurHeaderBytes + (col * a.tiles + tile) * kRecurRecBytes) {}
-    __device__ uint32_t *flag() const { return reinterpret_cast<uint32_t *>(at); }
-    __device__ float *factor(int c) const { return reinterpret_cast<float *>(at + 128) + c; }
-    __device__ float *addend(int c) const { return reinterpret_cast<float *>(at + 128) + kStrip + c; }
-    __device__ float *after(int c) const { return reinterpret_cast<float *>(at + 128) + 2 * kStrip + c; }
-};
+// A tile's record: per channel two words of a float and a tag that says what it
+// is.  The tag travels with its value, so nobody waits for a store to arrive
+// before a flag.  Word 0: the map's addend, then the state behind the tile; word
+// 1: the map's factor.
 constexpr uint32_t kMapKnown = 1, kStateKnown = 2;
 
-__device__ __forceinline__ void publish(const RecurRecord &r, uint32_t flag)
-{
-    wait_stores();                            // the wave's values first
-    if (lane_id() == 0)
-        __hip_atomic_store(r.flag(), flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+struct RecurRecord {
+    uint64_t *at;
+    __device__ RecurRecord(const RecurArgs &a, int64_t col, int64_t tile)
+        : at(reinterpret_cast<uint64_t *>(a.ws) + (col * a.tiles + tile) * (2 * kStrip)) {}
+    __device__ __forceinline__ void put(int word, int c, float v, uint32_t tag) const
+    {
+        __hip_atomic_store(at + word * kStrip + c, uint64_t(tag) << 32 | bitcast<uint32_t>(v), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // where nothing is known yet: what the tile's own block puts later is the same, or its state
+    __device__ __forceinline__ void offer(int word, int c, float v, uint32_t tag) const
+    {
+        uint64_t nothing = 0;
+        __hip_atomic_compare_exchange_strong(at + word * kStrip + c, &nothing, uint64_t(tag) << 32 | bitcast<uint32_t>(v),
+                                             __ATOMIC_RELAXED, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ uint64_t get(int word, int c) const
+    {
+        return __hip_atomic_load(at + word * kStrip + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
+
+__device__ __forceinline__ uint32_t tag_of(uint64_t w) { return uint32_t(w >> 32); }
+__device__ __forceinline__ float value_of(uint64_t w) { return bitcast<float>(uint32_t(w)); }
+
+// kRecurBatch consecutive records' words of a channel, the first of them `i` tiles
+// before the one whose state is wanted.  (Records of a column lie one after the
+// other, so a batch takes one address; it may reach that tile's own and the next
+// ones, whose words are not looked at.)
+struct RecordBatch {
+    static constexpr int N = kRecurBatch;
+    uint64_t A[N], H[N];
+
+    __device__ __forceinline__ void load(const RecurRecord &r, int c)
+    {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            H[k] = r.get(2 * k, c);
+            A[k] = r.get(2 * k + 1, c);
+        }
+    }
+    // whether every lane has all words of the i first records
+    __device__ __forceinline__ bool there(int i) const
+    {
+        bool t = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            t = t && (k >= i || tag_of(H[k]) == kStateKnown || (tag_of(H[k]) == kMapKnown && tag_of(A[k]) == kMapKnown));
+        return __ballot(!t) == 0;
+    }
+    // the state behind them (where a tile's state has taken its addend's place, the same state)
+    __device__ __forceinline__ float go_on(float s, int i) const
+    {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < i)
+                s = tag_of(H[k]) == kStateKnown ? value_of(H[k]) : apply(value_of(A[k]), s, value_of(H[k]));
+        return s;
+    }
+};
 
 // The state that enters tile `tile`, channel c = this lane's, run by one whole
-// wave.  Every tile with a smaller number has started (tiles are numbered in
-// the order blocks start) and makes its map known without waiting; the first
-// one that has no state yet has a tile with one right before it, so a window
-// of 64 tiles always comes to hold a state with maps only behind it and the
-// wait ends.  It is bounded all the same: past the bound it is counted and the
-// wave goes on.
-__device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int64_t tile, int c)
+// wave: from the nearest tile whose state is known through the maps of those
+// behind it, in order.  Every tile makes its map known without waiting, and a
+// column's first tile its state, so this comes to an end once the blocks of the
+// tiles between have started.  They start in the order of their numbers as far as
+// the device goes by these, which nothing depends on: where a map is missing after
+// a.patience polls, *missing is its tile, whose map the waiting block computes
+// itself (else -1).  force: ask for that in any case (a test's).  *back: 0, or how
+// far the state is where that is more than a batch, which is the whole block's to
+// gather.
+__device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int64_t tile, int c, bool force,
+                                           int64_t *missing, int64_t *back)
 {
-    const int lane = lane_id();
-    const int64_t j = tile - 1 - lane;
-    uint64_t known;
-    for (uint32_t spin = 0;; ++spin) {
-        const uint32_t f = j >= 0 ? __hip_atomic_load(RecurRecord(a, col, j).flag(), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                                  : 0u;
-        known = __ballot(f == kStateKnown);
-        const uint64_t nothing = __ballot(f == 0);
-        if (known && (nothing & ((known & (0 - known)) - 1)) == 0 && !a.force_wait)
-            break;
-        if (spin >= a.spin_limit) {
-            if (lane == 0)
-                record_timeout(-1);
+    constexpr int N = RecordBatch::N;
+    const int near = tile < N ? int(tile) : N;
+    RecordBatch b;
+    uint32_t polls = 0;
+    *missing = -1;
+    *back = 0;
+    for (int64_t first = tile - 1;;) {         // 64 tiles from `first` down: what channel 0 knows of them
+        const int64_t j = first - lane_id();
+        const uint32_t f = j >= 0 ? tag_of(RecurRecord(a, col, j).get(0, 0)) : kMapKnown;
+        b.load(RecurRecord(a, col, tile - near), c);   // and all words of the nearest ones
+        const uint64_t known = __ballot(f == kStateKnown), nothing = __ballot(f == 0);
+        if (force || (nothing && polls >= a.patience)) {
+            *missing = force ? tile - 1 : first - __builtin_ctzll(nothing);
             return 0.0f;
         }
+        if (known && (nothing & ((known & (0 - known)) - 1)) == 0) {
+            const int64_t i = tile - first + __builtin_ctzll(known);
+            if (i > near) {
+                *back = i;
+                return 0.0f;
+            }
+            if (b.there(near))
+                return b.go_on(0.0f, near);    // (what comes before the known state falls to it)
+        } else if (!nothing) {
+            first -= 64;                       // maps only: the tiles before them
+            continue;
+        }
+        ++polls;
         __builtin_amdgcn_s_sleep(1);
     }
-    const int first = __builtin_ctzll(known);
-    float s = load_partial(RecurRecord(a, col, tile - 1 - first).after(c));
-    for (int i = first - 1; i >= 0; i -= 8) {
-        float A[8], H[8];
+}
+
+// The maps of `count` <= kAhead records from tile `from` on, a few from every
+// wave, to LDS: addend and factor, the factor kTaken for a state.
+constexpr int kAhead = 2 * kRecurBatch * kWaves;
+constexpr uint32_t kTaken = 0x7fc0dead;        // (a NaN that a product of gates is not without its addend being one)
+
+__device__ __forceinline__ void gather_maps(const RecurArgs &a, int64_t col, int64_t from, int count, int wave, int c,
+                                            float2 (*maps)[kStrip])
+{
+    constexpr int N = RecordBatch::N;
+#pragma unroll 1
+    for (int i = wave * N; i < count; i += kWaves * N) {
+        const int n = count - i < N ? count - i : N;
+        RecordBatch b;
+        while (b.load(RecurRecord(a, col, from + i), c), !b.there(n))
+            __builtin_amdgcn_s_sleep(1);       // (words of channels beside the first are on their way)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const RecurRecord r(a, col, tile - 1 - (i - k > 0 ? i - k : 0));
-            A[k] = load_partial(r.factor(c));
-            H[k] = load_partial(r.addend(c));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s = i - k >= 0 ? apply(A[k], s, H[k]) : s;
+        for (int k = 0; k < N; ++k)
+            if (k < n)
+                maps[i + k][c] = make_float2(value_of(b.H[k]), tag_of(b.H[k]) == kStateKnown ? bitcast<float>(kTaken) : value_of(b.A[k]));
     }
-    return s;
 }
 
 // The last states (backward: the first states' gradients) of sequences
@@ -271,149 +375,210 @@ __global__ __launch_bounds__(kB) void k_recur_empty(RecurArgs a)
     empty_sequences<BWD>(a);
 }
 
-// Zero the tile counter and the flags.
-__global__ __launch_bounds__(kB) void k_recur_clear(RecurArgs a, int64_t recs)
+// Zero the records.
+__global__ __launch_bounds__(kB) void k_recur_clear(RecurArgs a, int64_t vectors)
 {
-    const int64_t i = int64_t(blockIdx.x) * kB + threadIdx.x;
-    if (i == 0)
-        a.ws[0] = 0;
-    if (i < recs)
-        *RecurRecord(a, 0, i).flag() = 0;
+    for (int64_t i = int64_t(blockIdx.x) * kB + threadIdx.x; i < vectors; i += int64_t(gridDim.x) * kB)
+        reinterpret_cast<u32x4 *>(a.ws)[i] = u32x4{0, 0, 0, 0};
 }
 
-template <class T>
-__device__ __forceinline__ const typename InTraits<T>::S *row_at(const RecurTensor &t, int64_t seg, int64_t row, int64_t c)
-{
-    return static_cast<const typename InTraits<T>::S *>(t.p) + seg * t.bs + row * t.ts + c;
-}
+// Where a lane stands in a tile.
+template <int V, int R, bool BWD>
+struct Place {
+    int64_t seg, c0, tile0, tile_end, row0;
+    int drop, more;
+    bool whole;
 
-template <class X, class G, int V, int R, bool BWD>
-__global__ __launch_bounds__(kB, 2) void k_recur(RecurArgs a)
+    __device__ __forceinline__ Place(const RecurArgs &a, int64_t tile, uint32_t col, int tid)
+    {
+        const int LC = 1 << a.lanes_log2, rows = (kB >> a.lanes_log2) * R;
+        seg = col / uint32_t(a.strips);
+        const int64_t cl = int64_t(col % uint32_t(a.strips)) * (LC * V) + (tid & (LC - 1)) * V;
+        // a lane that would pass the last channel takes the last V ones and drops those that are not its own
+        c0 = cl + V <= a.channels ? cl : a.channels - V;
+        drop = cl - c0 < V ? int(cl - c0) : V;
+        tile0 = tile * a.tile_rows;
+        tile_end = tile0 + a.tile_rows < a.rows ? tile0 + a.tile_rows : a.rows;
+        // The lane's first row, and how many follow it in the tile (in the scan's direction); lanes behind the
+        // tile's end stay on its last row.
+        const int r0 = (tid >> a.lanes_log2) * R;
+        const int64_t step = tile0 + r0 < tile_end ? tile0 + r0 : tile_end - 1;
+        row0 = BWD ? a.rows - 1 - step : step;
+        more = tile_end - 1 - step < R - 1 ? int(tile_end - 1 - step) : R - 1;
+        // (backward: the last tile reaches row 0, which has no row before it)
+        whole = tile0 + rows <= tile_end && (!BWD || tile_end < a.rows);
+    }
+    // the lane's first element of a tensor
+    template <class T>
+    __device__ __forceinline__ typename InTraits<T>::S *at(const RecurTensor &t) const
+    {
+        return static_cast<typename InTraits<T>::S *>(const_cast<void *>(t.p)) + seg * t.bs + row0 * t.ts + c0;
+    }
+};
+
+// Rows are a stride apart, so a step adds a scalar to an address.
+template <bool BWD>
+__device__ __forceinline__ int64_t way(int64_t r, int64_t ts) { return (BWD ? -r : r) * ts; }
+
+// A lane's inputs as they come from memory.
+template <class X, class G, bool BLEND, int V, int R, bool BWD>
+struct Inputs {
+    using PX = Pack<X, V>;
+    using PG = Pack<G, V>;
+    static constexpr bool HAS_X = !BWD || BLEND;
+    typename PG::Raw gate[R];
+    typename PX::Raw x[HAS_X ? R : 1], d[BWD ? R : 1], h[BWD ? R : 1];
+
+    template <bool CLAMP>
+    __device__ __forceinline__ void load_rows(const RecurArgs &a, const Place<V, R, BWD> &p)
+    {
+        const auto *gate_p = p.template at<G>(a.gate);
+        const auto *x_p = p.template at<X>(a.x), *d_p = p.template at<X>(a.dout), *h_p = p.template at<X>(a.h);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = CLAMP && r > p.more ? p.more : r;
+            gate[r] = PG::load(gate_p + way<BWD>(i, a.gate.ts));
+            if constexpr (HAS_X)
+                x[r] = PX::load(x_p + way<BWD>(i, a.x.ts));
+            if constexpr (BWD) {
+                d[r] = PX::load(d_p + way<BWD>(i, a.dout.ts));
+                h[r] = PX::load(h_p + way<BWD>(CLAMP && i + 1 > p.row0 ? p.row0 : i + 1, a.h.ts));
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const RecurArgs &a, const Place<V, R, BWD> &p)
+    {
+        if (p.whole)
+            load_rows<false>(a, p);
+        else
+            load_rows<true>(a, p);
+    }
+};
+
+template <class X, class G, int KIND, bool BLEND, int V, int R, bool BWD>
+__global__ __launch_bounds__(kB, kRecurWaves)
+void k_recur(RecurArgs a)
 {
     using PX = Pack<X, V>;
     using PG = Pack<G, V>;
-    using XS = typename PX::S;
-    using GS = typename PG::S;
-    __shared__ uint32_t s_id;
+    constexpr bool FINE = sizeof(typename PG::S) == 4;
     __shared__ __attribute__((aligned(16))) uint8_t s_flag[kB * R];
     __shared__ int32_t s_seq[kB * R];
     __shared__ float s_A[kWaves][kStrip], s_H[kWaves][kStrip], s_in[kStrip];
-    __shared__ int s_reset[kWaves];
+    __shared__ int s_reset[kWaves], s_next, s_back;
+    __shared__ float2 s_maps[kAhead][kStrip];
 
-    const int tid = int(threadIdx.x), lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int LC = 1 << a.lanes_log2;
-    uint32_t id = blockIdx.x;
-    if (a.linked) {
-        if (tid == 0)
-            s_id = __hip_atomic_fetch_add(a.ws, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        id = __builtin_amdgcn_readfirstlane(s_id);
-        if (id >= gridDim.x)                   // never: the counter starts at zero
-            return;
-    }
-    const uint32_t cols = uint32_t(a.strips) * uint32_t(a.segs);
-    const int64_t tile = id / cols;
-    const uint32_t col = id % cols;
-    const int64_t seg = col / uint32_t(a.strips);
-    const int64_t cl = int64_t(col % uint32_t(a.strips)) * (LC * V) + (tid & (LC - 1)) * V;
-    // a lane that would pass the last channel takes the last V ones and drops those that are not its own
-    const int64_t c0 = cl + V <= a.channels ? cl : a.channels - V;
-    const int drop = cl - c0 < V ? int(cl - c0) : V;
-    const int64_t tile0 = tile * a.tile_rows, tile_end = tile0 + a.tile_rows < a.rows ? tile0 + a.tile_rows : a.rows;
-    const int r0 = (tid >> a.lanes_log2) * R;
+    const int LC = 1 << a.lanes_log2, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const uint32_t cols = uint32_t(a.strips) * uint32_t(a.segs), col = blockIdx.x % cols;
+    const int64_t tile = blockIdx.x / cols;
+    constexpr int kWords = (R + 3) / 4;
+    Inputs<X, G, BLEND, V, R, BWD> in;
+    uint32_t flags[kWords];
+    float ga[BWD ? 1 : R][V], gb[BWD ? 1 : R][V], A[V], H[V];
+    bool plain, before_reset;
+    float tile_A = 1.0f, tile_H = 0.0f;       // the tile's own map, in the first wave
+    bool tile_known = true;
+    const auto flag = [&](int r) { return flags[r / 4] >> (r % 4 * 8) & 0xffu; };
 
-    // rows of this lane's steps, kept inside the tile
-    auto row_of = [&](int r) {
-        int64_t s = tile0 + r0 + r;
-        s = s < tile_end ? s : tile_end - 1;
-        return BWD ? a.rows - 1 - s : s;
-    };
-    typename PG::Raw gate[R];
-    typename PX::Raw x[R], d[BWD ? R : 1], h[BWD ? R : 1];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t row = row_of(r);
-        gate[r] = PG::load(row_at<G>(a.gate, seg, row, c0));
-        if constexpr (BWD) {
-            d[r] = PX::load(row_at<X>(a.dout, seg, row, c0));
-            h[r] = PX::load(row_at<X>(a.h, seg, row > 0 ? row - 1 : 0, c0));
-            if (a.blend)
-                x[r] = PX::load(row_at<X>(a.x, seg, row, c0));
-            else
-                x[r] = typename PX::Raw{};
-        } else {
-            x[r] = PX::load(row_at<X>(a.x, seg, row, c0));
-        }
-    }
+    // The tile's map, and the state that enters it.  (More than one turn only where a tile before it has not been
+    // started: this block then computes that one's map, and its own again.)
+    bool force = a.force_help;
+#pragma unroll 1
+    for (int64_t target = tile;;) {
+    // (what follows from the thread's number is not kept from turn to turn: there is hardly ever a second)
+    int tid = int(threadIdx.x);
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, r0 = (tid >> a.lanes_log2) * R;
+    const Place<V, R, BWD> at(a, target, col, tid);
+    in.load(a, at);
     issue_barrier();
     for (int i = tid; i < (kB >> a.lanes_log2) * R; i += kB) {
-        const int64_t s = tile0 + i;
+        const int64_t s = at.tile0 + i;
         uint32_t f = 0;
         int32_t b = -1;
-        if (s < tile_end)
-            b = sequence_of<BWD>(a, seg, BWD ? a.rows - 1 - s : s, &f);
+        if (s < at.tile_end)
+            b = sequence_of<BWD>(a, at.seg, BWD ? a.rows - 1 - s : s, &f);
         s_flag[i] = uint8_t(f);
         s_seq[i] = b;
     }
     __syncthreads();
-    uint8_t flag[R];
-    __builtin_memcpy(flag, __builtin_assume_aligned(s_flag + r0, R), R);
+    // steps in the middle of sequences are all alike; others are looked at one by one
+    bool inside = true;
+    if constexpr (R < 4) {
+        flags[0] = s_flag[r0];
+        inside = flags[0] == kIn;
+    } else {
+        static_assert(R % 4 == 0, "whole words");
+        __builtin_memcpy(flags, __builtin_assume_aligned(s_flag + r0, R % 8 == 0 ? 8 : 4), R);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            inside = inside && flags[i] == kIn * 0x01010101u;
+    }
+    plain = __ballot(!inside) == 0;
 
-    float A[V], H[V], start[V];
+    // The lane's map, from state 0.  A forward lane keeps, for each step, what the state is multiplied with and
+    // what is added; a sequence's first state goes into its first step's (and need not be read again, when the
+    // last one may have taken its place).  A backward lane keeps its inputs as they came and computes the gates
+    // twice: four inputs a step, of 16 bits, take fewer registers than what they come to.
     bool reset = false;
-    int last_reset = -1;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         A[k] = 1.0f;
         H[k] = 0.0f;
-        start[k] = 0.0f;
     }
-    auto reset_value = [&](int r, float (&s)[V]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float g[V], v[V], ak[V], wk[V];
+        PG::get(in.gate[r], g);
         if constexpr (BWD)
-            last_gradient(a, s_seq[r0 + r], c0, s);
+            PX::get(in.d[r], v);
         else
-            first_state(a, s_seq[r0 + r], c0, s);
-    };
-    // the lane's map, from state 0; `start`: the state of its last reset, not read again where the
-    // sequence's last state may take its place
-    auto fold = [&](auto kind) {
-        constexpr int KIND = decltype(kind)::value;
+            PX::get(in.x[r], v);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = flag[r] & kIn;
-            float g[V], v[V];
-            PG::get(gate[r], g);
-            if constexpr (BWD)
-                PX::get(d[r], v);
-            else
-                PX::get(x[r], v);
-            if (flag[r] & kReset) {
+        for (int k = 0; k < V; ++k) {
+            gate_of<KIND, FINE, BLEND && !BWD>(g[k], ak[k], wk[k]);
+            if constexpr (BLEND && !BWD)
+                v[k] *= wk[k];
+        }
+        if (!plain && flag(r) != kIn) {
+            if (flag(r) & kReset) {
                 reset = true;
-                last_reset = r;
-                reset_value(r, start);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    H[k] = start[k];
-            }
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float ak, wk;
-                gate_of<KIND, !BWD>(g[k], ak, wk);
+                    float start[V];
                 if constexpr (BWD)
-                    H[k] = in ? ak * (v[k] + H[k]) : H[k];
+                    last_gradient(a, s_seq[r0 + r], at.c0, start);
                 else
-                    H[k] = in ? __builtin_fmaf(ak, H[k], a.blend ? wk * v[k] : v[k]) : H[k];
-                A[k] = in ? A[k] * ak : A[k];
+                    first_state(a, s_seq[r0 + r], at.c0, start);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    if constexpr (BWD) {
+                        H[k] = start[k];
+                    } else {
+                        v[k] = __builtin_fmaf(ak[k], start[k], v[k]);
+                        ak[k] = 0.0f;
+                        H[k] = 0.0f;
+                    }
+                }
+            } else if (!(flag(r) & kIn)) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    ak[k] = 1.0f;          // a token of no sequence passes the state on
+                    v[k] = 0.0f;
+                }
             }
         }
-    };
-    if (a.kind == RECUR_SIGMOID)
-        fold(std::integral_constant<int, RECUR_SIGMOID>{});
-    else if (a.kind == RECUR_LOG)
-        fold(std::integral_constant<int, RECUR_LOG>{});
-    else
-        fold(std::integral_constant<int, RECUR_VALUE>{});
-
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if constexpr (BWD) {
+                H[k] = ak[k] * (v[k] + H[k]);
+            } else {
+                H[k] = __builtin_fmaf(ak[k], H[k], v[k]);
+                ga[r][k] = ak[k];
+                gb[r][k] = v[k];
+            }
+            A[k] *= ak[k];
+        }
+        issue_barrier();                   // a row at a time: registers bound the tokens on their way
+    }
     // maps of the groups up to this one in the wave, then of those before it
     for (int dist = LC; dist < 64; dist <<= 1) {
         const int from = lane >= dist ? lane - dist : lane;
@@ -437,7 +602,7 @@ __global__ __launch_bounds__(kB, 2) void k_recur(RecurArgs a)
         if (lane == 63)
             s_reset[wave] = reset;
     }
-    bool before_reset = bpermute32(reset, lane >= LC ? lane - LC : lane);
+    before_reset = bpermute32(reset, lane >= LC ? lane - LC : lane);
     before_reset = lane >= LC && before_reset;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -448,42 +613,82 @@ __global__ __launch_bounds__(kB, 2) void k_recur(RecurArgs a)
         H[k] = lane >= LC ? pH : 0.0f;
     }
     __syncthreads();
-    if (a.linked) {
-        if (wave == 0) {
-            const int c = lane < LC * V ? lane : LC * V - 1;
-            float tA = s_A[0][c], tH = s_H[0][c];
-            bool tr = s_reset[0];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) {
-                const bool r = s_reset[w];
-                tH = r ? s_H[w][c] : apply(s_A[w][c], tH, s_H[w][c]);
-                tA *= s_A[w][c];
-                tr = tr || r;
-            }
-            const RecurRecord rec(a, col, tile);
-            const bool known = tr || tile == 0, behind = tile + 1 < a.tiles;
-            if (behind) {
-                if (known) {
-                    store_partial(rec.after(c), tH);
-                } else {
-                    store_partial(rec.factor(c), tA);
-                    store_partial(rec.addend(c), tH);
-                }
-                publish(rec, known ? kStateKnown : kMapKnown);
-            }
-            float s = 0.0f;
-            if (tile > 0 && !(s_flag[0] & kReset)) {
-                s = look_back(a, col, tile, c);
-                if (behind && !known) {
-                    store_partial(rec.after(c), apply(tA, s, tH));
-                    publish(rec, kStateKnown);
-                }
-            }
-            if (lane < LC * V)
-                s_in[c] = s;
+    if (!a.linked)
+        break;
+    if (wave == 0) {
+        const int c = lane < LC * V ? lane : LC * V - 1;   // a lane a channel of the strip
+        float tA = 1.0f, tH = 0.0f, s = 0.0f;
+        bool known = target == 0;
+        for (int w = 0; w < kWaves; ++w) {
+            const bool r = s_reset[w];
+            tH = r ? s_H[w][c] : apply(s_A[w][c], tH, s_H[w][c]);
+            tA *= s_A[w][c];
+            known = known || r;
         }
-        __syncthreads();
+        const RecurRecord rec(a, col, target);
+        int64_t next = -1, back = 0;
+        if (target != tile) {
+            rec.offer(1, c, tA, kMapKnown);
+            rec.offer(0, c, tH, known ? kStateKnown : kMapKnown);
+            next = tile;
+        } else {
+            const bool behind = tile + 1 < a.tiles;
+            if (behind) {
+                rec.put(0, c, tH, known ? kStateKnown : kMapKnown);
+                if (!known)
+                    rec.put(1, c, tA, kMapKnown);
+            }
+            if (tile > 0 && !(s_flag[0] & kReset)) {
+                s = look_back(a, col, tile, c, force, &next, &back);
+                if (next < 0 && back == 0 && behind && !known)
+                    rec.put(0, c, apply(tA, s, tH), kStateKnown);
+            }
+        }
+        if (lane < LC * V)
+            s_in[c] = s;
+        if (lane == 0) {
+            s_next = int(next);
+            s_back = int(back);
+        }
+        tile_A = tA;
+        tile_H = tH;
+        tile_known = known;
     }
+    force = false;
+    __syncthreads();
+    const int next = __builtin_amdgcn_readfirstlane(s_next);
+    if (next < 0)
+        break;
+    target = next;
+    }
+    if (a.linked) {
+        const int lane = lane_id(), c = lane < LC * V ? lane : LC * V - 1;
+        int back = __builtin_amdgcn_readfirstlane(s_back);
+        if (back > 0) {
+            float s = 0.0f;
+            for (; back > 0; back -= kAhead) {
+                const int count = back < kAhead ? back : kAhead;
+                gather_maps(a, col, tile - back, count, wave, c, s_maps);
+                __syncthreads();
+                if (wave == 0)
+                    for (int i = 0; i < count; ++i) {
+                        const float2 m = s_maps[i][c];
+                        s = bitcast<uint32_t>(m.y) == kTaken ? m.x : apply(m.y, s, m.x);
+                    }
+                if (back > kAhead)
+                    __syncthreads();
+            }
+            if (wave == 0) {
+                if (tile + 1 < a.tiles && !tile_known)
+                    RecurRecord(a, col, tile).put(0, c, apply(tile_A, s, tile_H), kStateKnown);
+                if (lane < LC * V)
+                    s_in[c] = s;
+            }
+            __syncthreads();
+        }
+    }
+    const int tid = int(threadIdx.x), r0 = (tid >> a.lanes_log2) * R;
+    const Place<V, R, BWD> at(a, tile, col, tid);
     // the state that enters this lane's steps
     float s[V];
 #pragma unroll
@@ -494,68 +699,55 @@ __global__ __launch_bounds__(kB, 2) void k_recur(RecurArgs a)
             s[k] = s_reset[w] ? s_H[w][c] : apply(s_A[w][c], s[k], s_H[w][c]);
         s[k] = before_reset ? H[k] : apply(A[k], s[k], H[k]);
     }
-
-    auto finish = [&](auto kind) {
-        constexpr int KIND = decltype(kind)::value;
+    auto *const out_p = at.template at<X>(a.out);
+    auto *const dgate_p = at.template at<G>(a.dgate);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float g[V], v[V];
-            PG::get(gate[r], g);
-            if (flag[r] & kReset) {
-                if (r == last_reset) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        s[k] = start[k];
-                } else {
-                    reset_value(r, s);
-                }
-            }
-            const int64_t row = row_of(r);
+    for (int r = 0; r < R; ++r) {
+        const bool special = !plain && flag(r) != kIn, there = !special || (flag(r) & kIn) != 0;
+        if (special && (flag(r) & kReset)) {
             if constexpr (BWD) {
-                float dv[V], hv[V], dx[V], dg[V];
-                PX::get(d[r], dv);
-                PX::get(h[r], hv);
-                PX::get(x[r], v);
-                if (flag[r] & kEnd)
-                    first_state(a, s_seq[r0 + r], c0, hv);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float ak, wk;
-                    gate_of<KIND, true>(g[k], ak, wk);
-                    const float gr = dv[k] + s[k];
-                    dx[k] = a.blend ? wk * gr : gr;
-                    const float da = a.blend ? gr * (hv[k] - v[k]) : gr * hv[k];
-                    dg[k] = KIND == RECUR_SIGMOID ? da * (ak * wk) : KIND == RECUR_LOG ? da * ak : da;
-                    s[k] = (flag[r] & kIn) ? ak * gr : s[k];
-                }
-                if (flag[r] & kIn) {
-                    PX::store(const_cast<XS *>(row_at<X>(a.out, seg, row, c0)), dx, drop);
-                    PG::store(const_cast<GS *>(row_at<G>(a.dgate, seg, row, c0)), dg, drop);
-                }
+                last_gradient(a, s_seq[r0 + r], at.c0, s);
             } else {
-                PX::get(x[r], v);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float ak, wk;
-                    gate_of<KIND, true>(g[k], ak, wk);
-                    const float n = __builtin_fmaf(ak, s[k], a.blend ? wk * v[k] : v[k]);
-                    s[k] = (flag[r] & kIn) ? n : s[k];
-                }
-                if (flag[r] & kIn)
-                    PX::store(const_cast<XS *>(row_at<X>(a.out, seg, row, c0)), s, drop);
-            }
-            if ((flag[r] & kEnd) && a.state_out) {
-                float *p = a.state_out + int64_t(s_seq[r0 + r]) * a.channels + c0;
-                Pack<float, V>::store(p, s, drop);
+                for (int k = 0; k < V; ++k)
+                    s[k] = 0.0f;               // (nothing of what was before, were it a NaN)
             }
         }
-    };
-    if (a.kind == RECUR_SIGMOID)
-        finish(std::integral_constant<int, RECUR_SIGMOID>{});
-    else if (a.kind == RECUR_LOG)
-        finish(std::integral_constant<int, RECUR_LOG>{});
-    else
-        finish(std::integral_constant<int, RECUR_VALUE>{});
+        if constexpr (BWD) {
+            float g[V], v[V], dv[V], hv[V], dx[V], dg[V];
+            decode_anew(in.gate[r]);
+            decode_anew(in.d[r]);
+            PG::get(in.gate[r], g);
+            PX::get(in.d[r], dv);
+            PX::get(in.h[r], hv);
+            if constexpr (BLEND)
+                PX::get(in.x[r], v);
+            if (special && (flag(r) & kEnd))
+                first_state(a, s_seq[r0 + r], at.c0, hv);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float ak, wk;
+                gate_of<KIND, FINE, BLEND || KIND == RECUR_SIGMOID>(g[k], ak, wk);
+                const float gr = dv[k] + s[k], da = BLEND ? gr * (hv[k] - v[k]) : gr * hv[k];
+                dx[k] = BLEND ? wk * gr : gr;
+                dg[k] = KIND == RECUR_VALUE ? da : da * (KIND == RECUR_LOG ? ak : ak * wk);
+                s[k] = there ? ak * gr : s[k];
+            }
+            if (there) {
+                PX::store(out_p + way<BWD>(r, a.out.ts), dx, at.drop);
+                PG::store(dgate_p + way<BWD>(r, a.dgate.ts), dg, at.drop);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                s[k] = __builtin_fmaf(ga[r][k], s[k], gb[r][k]);
+            if (there)
+                PX::store(out_p + way<BWD>(r, a.out.ts), s, at.drop);
+        }
+        if (special && (flag(r) & kEnd) && a.state_out)
+            Pack<float, V>::store(a.state_out + int64_t(s_seq[r0 + r]) * a.channels + at.c0, s, at.drop);
+        issue_barrier();
+    }
     if (a.starts)
         empty_sequences<BWD>(a);
 }
@@ -563,8 +755,16 @@ __global__ __launch_bounds__(kB, 2) void k_recur(RecurArgs a)
 template <class X, class G, int V, int R, bool BWD>
 int launch_one(const RecurLaunch &L)
 {
-    launch_timed(k_recur<X, G, V, R, BWD>, dim3(uint32_t(L.plan.grid)), dim3(kB), 0, L.stream,
-                 L.ev_begin, L.ev_end, L.a);
+    const auto go = [&](auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        const auto kernel = L.a.blend ? k_recur<X, G, KIND, true, V, R, BWD> : k_recur<X, G, KIND, false, V, R, BWD>;
+        launch_timed(kernel, dim3(uint32_t(L.plan.grid)), dim3(kB), 0, L.stream, L.ev_begin, L.ev_end, L.a);
+    };
+    switch (L.a.kind) {
+    case RECUR_SIGMOID: go(std::integral_constant<int, RECUR_SIGMOID>{}); break;
+    case RECUR_LOG: go(std::integral_constant<int, RECUR_LOG>{}); break;
+    default: go(std::integral_constant<int, RECUR_VALUE>{}); break;
+    }
     return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
@@ -579,21 +779,17 @@ int launch_recur(const RecurLaunch &L)
         return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
     }
     if (p.linked) {
-        const int64_t recs = p.grid;
-        hipLaunchKernelGGL(k_recur_clear, dim3(uint32_t((recs + kB - 1) / kB)), dim3(kB), 0,
-                           static_cast<hipStream_t>(L.stream), L.a, recs);
+        const int64_t vectors = p.tiles * p.strips * L.a.segs * kRecurRecBytes / 16;
+        const int64_t blocks = (vectors + kB * 8 - 1) / (kB * 8), most = 2048;
+        hipLaunchKernelGGL(k_recur_clear, dim3(uint32_t(blocks < most ? blocks : most)), dim3(kB), 0,
+                           static_cast<hipStream_t>(L.stream), L.a, vectors);
         if (hipGetLastError() != hipSuccess)
             return ST_HIP;
     }
-    if (p.vec == 1)
-        return p.per_lane == 1 ? launch_one<X, G, 1, 1, BWD>(L) : launch_one<X, G, 1, 4, BWD>(L);
     constexpr int R = recur_rows(sizeof(typename InTraits<X>::S), sizeof(typename InTraits<G>::S), BWD);
-    static_assert(R == (BWD && std::is_same_v<G, float> ? 8 : 16), "the plan's tokens of a lane");
-    switch (p.per_lane) {
-    case 1: return launch_one<X, G, 4, 1, BWD>(L);
-    case 4: return launch_one<X, G, 4, 4, BWD>(L);
-    default: return launch_one<X, G, 4, R, BWD>(L);
-    }
+    if (p.vec == 1)
+        return launch_one<X, G, 1, 4, BWD>(L);
+    return p.per_lane == 1 ? launch_one<X, G, 4, 1, BWD>(L) : launch_one<X, G, 4, R, BWD>(L);
 }
 
 template <class X>
@@ -604,19 +800,6 @@ int launch_recur_x(const RecurLaunch &L)
     if constexpr (!std::is_same_v<X, float>)
         return L.backward ? launch_recur<X, X, true>(L) : launch_recur<X, X, false>(L);
     return ST_UNSUPPORTED;
-}
-
-inline int take_recur_timeouts(uint64_t *count)
-{
-    uint32_t n = 0;
-    const uint32_t zero = 0;
-    const size_t at = size_t(kArriveSlots) * 4;
-    if (hipMemcpyFromSymbol(&n, HIP_SYMBOL(g_timeouts), 4, at, hipMemcpyDeviceToHost) != hipSuccess)
-        return ST_HIP;
-    if (n && hipMemcpyToSymbol(HIP_SYMBOL(g_timeouts), &zero, 4, at, hipMemcpyHostToDevice) != hipSuccess)
-        return ST_HIP;
-    *count += n;
-    return ST_OK;
 }
 
 }  // namespace

@@ -28,10 +28,10 @@ int plan_recur(int x_dtype, int gate_dtype, int64_t rows, int64_t segs, int64_t 
     if (strips * segs > 0xffffff)
         return ST_UNSUPPORTED;                // blocks of 256 threads of a launch
     const int64_t groups = tune::kRecurBlock >> p->lanes_log2;
-    // as many tokens a lane as leave a few blocks for every CU
+    // one token a lane where more would leave half of the CUs without a block
     p->per_lane = p->vec == 1 ? 4 : recur_rows(dtype_size(x_dtype), dtype_size(gate_dtype), backward);
-    while (p->per_lane > 1 && (rows + groups * p->per_lane - 1) / (groups * p->per_lane) * strips * segs < 2 * int64_t(cus))
-        p->per_lane = p->per_lane > 4 ? 4 : 1;
+    if (p->vec > 1 && (rows + groups * p->per_lane - 1) / (groups * p->per_lane) * strips * segs < cus / 2)
+        p->per_lane = 1;
     int64_t tile = groups * p->per_lane;
     // whole sequences a tile, where at most a quarter of its lanes is left idle: no state passes between tiles then
     p->linked = period == 0 || (tile % period != 0 && 4 * period > tile);
@@ -46,7 +46,7 @@ int plan_recur(int x_dtype, int gate_dtype, int64_t rows, int64_t segs, int64_t 
     p->grid = p->tiles * strips * segs;
     if (p->linked) {
         p->launches = 2;
-        p->ws_bytes = round_up_256(size_t(kRecurHeaderBytes) + size_t(p->grid) * kRecurRecBytes);
+        p->ws_bytes = round_up_256(size_t(p->grid + kRecurBatch - 1) * kRecurRecBytes);
     }
     return ST_OK;
 }

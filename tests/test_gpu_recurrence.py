@@ -413,22 +413,27 @@ def test_streams_and_captures():
             assert torch.equal(o[0], w) and torch.equal(o[1], wg)
 
 
-def test_waits_that_give_up_are_counted():
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+def test_blocks_help_where_they_would_wait(types):
+    """Every block that looks back computes the map of the tile before its own, too: the same bits."""
     rk = _rk()
     g = gen(9)
-    gate, x = gates(g, (1, 9000, 64), "sigmoid", F32).to(DEV), torch.randn(1, 9000, 64, generator=g).to(DEV)
-    want = rk.linear_recurrence(gate, x, kind="sigmoid")[0].clone()
-    stream = torch.cuda.current_stream().cuda_stream
-    assert rk.rk_stream_timeouts(stream) == 0
-    rk.rk_debug_force_wait_timeout(3)
-    try:
-        rk.linear_recurrence(gate, x, kind="sigmoid")
-        torch.cuda.synchronize()
-    finally:
-        rk.rk_debug_force_wait_timeout(-1)
-    assert rk.rk_stream_timeouts(stream) > 0
-    assert rk.rk_stream_timeouts(stream) == 0
-    assert torch.equal(rk.linear_recurrence(gate, x, kind="sigmoid")[0], want)
+    for shape, starts in (((1, 9000, 64), None), ((2, 1500, 130), None), ((9000, 70), torch.tensor([0, 5, 3000, 3001, 8999, 9000], dtype=torch.int32, device=DEV))):
+        gate, x = gates(g, shape, "sigmoid", types[1]).to(DEV), torch.randn(shape, generator=g).to(types[0]).to(DEV)
+        n = shape[0] if starts is None else 5
+        state = torch.randn(n, shape[-1], generator=g).to(DEV)
+        call = lambda: rk.linear_recurrence(gate, x, state=state, kind="sigmoid", blend=True, starts=starts)  # noqa: E731
+        out, last = call()
+        back = lambda: rk.linear_recurrence_backward(gate, x, out, x, state=state, dstate_out=state, kind="sigmoid", blend=True, starts=starts)  # noqa: E731
+        want = (out, last, *back())
+        rk.rk_debug_force_wait_timeout(0)
+        try:
+            got = (*call(), *back())
+            torch.cuda.synchronize()
+        finally:
+            rk.rk_debug_force_wait_timeout(-1)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert rk.rk_stream_timeouts(torch.cuda.current_stream().cuda_stream) == 0
 
 
 def test_launch_failures_and_small_workspaces():
