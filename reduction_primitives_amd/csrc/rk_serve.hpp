@@ -72,7 +72,7 @@ constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
 // ---- beam selection
 constexpr int kBeamBlock = 256;
 constexpr int kBeamTile = 2048;           // vocabulary entries of a wave's tile
-constexpr int kBeamWavesPerCu = 8;        // waves of the first launch = CUs * this, or a wave a tile
+constexpr int kBeamWavesPerCu = 16;       // waves of the first launch = CUs * this, or a wave a tile
 constexpr int kBeamMost = 64;             // candidates kept of a request: a lane each
 constexpr int kBeamLines = 4096;          // beams of a request, 12 bytes of LDS each
 // ---- forked, compacted and copied blocks
@@ -288,6 +288,8 @@ struct BeamArgs {
     const uint8_t *ended;     // or NULL
     int64_t end_token;
     int64_t chunks, per_wave, items;
+    int lanes;                // second launch: lanes that share a line's chunks
+    Divider per_line;         // entries of a line's lists
     double *sums;             // of every item (a wave's part of a line)
     float *tops, *best_x;     // the largest entry; the count largest
     int32_t *best_at;

@@ -426,6 +426,10 @@ int rk_beam_select(int dtype, int token_dtype, const void *logits, int64_t strid
     L.a.chunks = p.chunks;
     L.a.per_wave = p.per_wave;
     L.a.items = p.items;
+    L.a.per_line = make_divider(uint32_t(p.chunks * count));
+    L.a.lanes = 1;
+    while (L.a.lanes < 64 && L.a.lanes < p.chunks && L.a.lanes * 2 * int64_t(beams) <= tune::kBeamBlock)
+        L.a.lanes *= 2;
     L.a.sums = static_cast<double *>(workspace);
     L.a.tops = reinterpret_cast<float *>(L.a.sums + p.items);
     L.a.best_x = L.a.tops + p.items;

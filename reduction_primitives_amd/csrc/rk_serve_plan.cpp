@@ -99,7 +99,8 @@ int plan_beams(int dtype, int64_t n, int64_t req, int64_t beams, int64_t count, 
     p->per_wave = each * tune::kBeamTile;
     p->items = lines * p->chunks;
     p->grid = (p->items + tune::kBeamBlock / 64 - 1) / (tune::kBeamBlock / 64);
-    if (p->grid > kMaxThreads / tune::kBeamBlock || req > kMaxThreads / tune::kBeamBlock)
+    if (p->grid > kMaxThreads / tune::kBeamBlock || req > kMaxThreads / tune::kBeamBlock ||
+        beams * p->chunks * count > 0x7fffffff - 4 * tune::kBeamBlock)
         return ST_UNSUPPORTED;
     p->ws_bytes = round_up_256(size_t(p->items) * (12 + 8 * size_t(count)));
     return ST_OK;

@@ -39,18 +39,24 @@ __device__ __forceinline__ int32_t ordered(float v)
 
 __device__ __forceinline__ float from_ordered(int32_t i) { return bitcast<float>(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// The largest b so that n lanes hold a value of at least b (n <= 64 lanes, no NaN).
+// The n-th largest of the lanes' values (no NaN), found bit by bit.  COARSE: values
+// whose low 16 bits do not matter (as integers of this order all 0 or all 1): a bound
+// that n lanes reach, at most a last place of 16 bits below it.
+template <bool COARSE>
 __device__ __forceinline__ int32_t nth_largest(int32_t v, int n)
 {
     const uint32_t u = uint32_t(v) ^ 0x80000000u;
     uint32_t b = 0;
 #pragma unroll
-    for (int bit = 31; bit >= 0; --bit) {
+    for (int bit = 31; bit >= (COARSE ? 16 : 0); --bit) {
         const uint32_t with = b | (1u << bit);
         b = __popcll(__ballot(u >= with)) >= n ? with : b;
     }
     return int32_t(b ^ 0x80000000u);
 }
+
+// The next smaller float (-0 is 0).
+__device__ __forceinline__ float below(int32_t v) { return from_ordered(v == 0 ? -2 : v - 1); }
 
 template <class T>
 __device__ __forceinline__ T lane_before(T v)
@@ -88,31 +94,39 @@ struct Tile {
     static constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
     float v[U][V];
 
-    __device__ __forceinline__ static int place(int u) { return (u * 64 + lane_id()) * V; }
-
-    __device__ __forceinline__ void load(const S *x, int left)
-    {
-        if (left >= kTile) {
-            u32x4 w[U];
+    // A whole tile as it comes from memory.
+    struct Raw {
+        u32x4 w[U];
+        __device__ __forceinline__ void load(const S *x)
+        {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 w[u] = Words<4>::load<true>(x + place(u));
-            issue_barrier();
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                InTraits<In>::decode(w[u], v[u]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    v[u][k] = place(u) + k < left ? InTraits<In>::template one<float>(x[place(u) + k]) : kNone;
         }
+    };
+
+    __device__ __forceinline__ static int place(int u) { return (u * 64 + lane_id()) * V; }
+
+    // (-0 is 0)
+    __device__ __forceinline__ void decode(const Raw &r)
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            InTraits<In>::decode(r.w[u], v[u]);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                v[u][k] += 0.0f;
+        }
+    }
+
+    // the line's end: `left` entries, fewer than a tile's
+    __device__ __forceinline__ void load_rest(const S *x, int left)
+    {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                v[u][k] += 0.0f;              // -0 is 0
+                v[u][k] = place(u) + k < left ? InTraits<In>::template one<float>(x[place(u) + k]) + 0.0f : kNone;
     }
 
     __device__ __forceinline__ float largest(int u) const
@@ -128,16 +142,20 @@ struct Tile {
     {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float m = largest(u);
-            for (uint64_t hit = __ballot(m > best.bar); hit;) {
-                const int l = __builtin_ctzll(hit);
+            // entries that pass the bar as it was, lane by lane: in the order of their tokens
+            uint64_t over[V], any = 0;
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float x = read_lane(v[u][k], l);
-                    if (x > best.bar)
-                        best.insert(x, base + (u * 64 + l) * V + k);
-                }
-                hit = l == 63 ? 0 : __ballot(m > best.bar) & (~uint64_t(0) << (l + 1));
+            for (int k = 0; k < V; ++k)
+                any |= over[k] = __ballot(v[u][k] > best.bar);
+            for (; any; any &= any - 1) {
+                const int l = __builtin_ctzll(any);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (over[k] >> l & 1) {
+                        const float x = read_lane(v[u][k], l);
+                        if (x > best.bar)
+                            best.insert(x, base + (u * 64 + l) * V + k);
+                    }
             }
         }
     }
@@ -150,7 +168,13 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
 {
     using S = typename InTraits<In>::S;
     using T = Tile<In>;
-    const int64_t item = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    // the waves' bars: of those that go through the same line, the highest holds for all
+    __shared__ float s_bar[kWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    if (threadIdx.x < kWaves)
+        s_bar[threadIdx.x] = kNone;
+    __syncthreads();
+    const int64_t item = int64_t(blockIdx.x) * kWaves + wave;
     if (item >= a.items)
         return;
     const int64_t line = item / a.chunks;
@@ -162,9 +186,18 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
     Best best(a.count);
     float m = kNone;
     double s = 0.0;
+    typename T::Raw raw;                       // the next tile is on its way while one is gone through
+    if (from + kTile <= to)
+        raw.load(x + from);
     for (int64_t base = from; base < to; base += kTile) {
         T t;
-        t.load(x + base, int(to - base < kTile ? to - base : kTile));
+        if (base + kTile <= to)
+            t.decode(raw);
+        else
+            t.load_rest(x + base, int(to - base));
+        if (base + 2 * kTile <= to)
+            raw.load(x + base + kTile);
+        issue_barrier();
         float top = t.largest(0);
 #pragma unroll
         for (int u = 1; u < T::U; ++u)
@@ -178,14 +211,20 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
                 part += __builtin_amdgcn_exp2f((t.v[u][k] - ref) * kLog2e);
         s = s * double(__builtin_amdgcn_exp2f((m - ref) * kLog2e)) + double(part);
         m = now;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            if (w >= wave - chunk && w < wave - chunk + a.chunks) {   // (`count` entries reach it: one that does not is out)
+                const float b = __hip_atomic_load(s_bar + w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                best.bar = b > kNone && w != wave ? __builtin_fmaxf(best.bar, below(ordered(b))) : best.bar;
+            }
         const uint64_t over = __ballot(top > best.bar);
         if (over) {
             // many lanes at once: of their largest entries the count-th best bars the rest
-            if (__popcll(over) > a.count) {
-                const int32_t k = nth_largest(ordered(top == top ? top : kNone), a.count);
-                best.bar = __builtin_fmaxf(best.bar, from_ordered(k == 0 ? -2 : k - 1));   // (-1: -0, which is 0)
-            }
+            if (__popcll(over) > a.count)
+                best.bar = __builtin_fmaxf(best.bar, below(nth_largest<sizeof(S) == 2>(ordered(top == top ? top : kNone), a.count)));
             t.select(best, int32_t(base));
+            if (lane_id() == 0)
+                __hip_atomic_store(s_bar + wave, best.bar, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
     }
     // (a NaN in a lane makes the maximum one)
@@ -210,11 +249,10 @@ struct Candidate {
     int32_t line, at;         // line of the request
     __device__ __forceinline__ bool before(const Candidate &o) const
     {
-        if (s != o.s)
-            return s > o.s;
-        if (line != o.line)
-            return line < o.line;
-        return x != o.x ? x > o.x : at < o.at;
+        // (no branches: all four are there already)
+        const bool by_at = (x > o.x) | ((x == o.x) & (at < o.at));
+        const bool by_line = (line < o.line) | ((line == o.line) & by_at);
+        return (s > o.s) | ((s == o.s) & by_line);
     }
 };
 
@@ -223,8 +261,9 @@ __device__ __forceinline__ Candidate read_candidate(const Candidate &c, int l)
     return Candidate{read_lane(c.s, l), read_lane(c.x, l), read_lane(c.line, l), read_lane(c.at, l)};
 }
 
+// The best candidates of a wave, the i-th in lane i.
 struct Merge {
-    Candidate c;              // the i-th best in lane i
+    Candidate c;
     double bar;
     int n;
 
@@ -244,13 +283,7 @@ struct Merge {
     // 64 candidates, those of -inf left out
     __device__ __forceinline__ void offer(const Candidate &v)
     {
-        uint64_t over = __ballot(v.s > kNone64 && v.s >= bar);
-        if (__popcll(over) > n) {
-            // rounded to float32 (monotone), the n-th best bars what is below it
-            const float f = from_ordered(nth_largest(ordered(float(v.s) + 0.0f), n));
-            over &= __ballot(float(v.s) >= f);
-        }
-        for (uint64_t hit = over; hit; hit &= hit - 1) {
+        for (uint64_t hit = __ballot(v.s > kNone64 && v.s >= bar); hit; hit &= hit - 1) {
             const int l = __builtin_ctzll(hit);
             if (read_lane(v.s, l) >= bar)
                 insert(read_candidate(v, l));
@@ -258,93 +291,204 @@ struct Merge {
     }
 };
 
+// What is kept of a request's lines for its second launch.
+struct Lines {
+    const BeamArgs &a;
+    int64_t line0;
+    const double *base;       // score - log sum; -inf: no candidate
+    const float *top;         // what is taken from the logits first
+
+    // Entry i of the request's lists (a line's that has none may hold anything).
+    struct Entry {
+        float x;
+        int32_t at;
+    };
+    __device__ __forceinline__ Entry entry(uint32_t i) const
+    {
+        const int64_t e = line0 * int64_t(a.per_line.d) + i;
+        return Entry{a.best_x[e], a.best_at[e]};
+    }
+    // the candidate it is (of s = -inf: none)
+    __device__ __forceinline__ Candidate candidate(uint32_t i, const Entry &e) const
+    {
+        const uint32_t j = divide(i, a.per_line);
+        Candidate v{kNone64, e.x, int32_t(j), e.at};
+        const float t = top[j];
+        if (t == kEnded) {
+            if (i == j * a.per_line.d) {
+                v.s = base[j];
+                v.x = 0.0f;
+                v.at = int32_t(a.end_token);
+            }
+        } else if (base[j] > kNone64 && e.x > kNone) {
+            v.s = (double(e.x) - double(t)) + base[j];
+        }
+        return v;
+    }
+    __device__ __forceinline__ Candidate candidate(uint32_t i) const { return candidate(i, entry(i)); }
+    static constexpr float kEnded = kNone;    // a top that no line with candidates has
+};
+
+// Sum or largest value over each group of `lanes` neighbouring lanes.
+template <class Op, class T>
+__device__ __forceinline__ T group_reduce(T v, int lanes)
+{
+    for (int d = 1; d < lanes; d *= 2) {
+        const int from = lane_id() ^ d;
+        v = Op::apply(v, move_words(v, [from](uint32_t w) { return bpermute32(w, from); }));
+    }
+    return v;
+}
+
+constexpr int kNear = 512;                     // candidates that are ranked against each other
+
 template <class Tok>
 __global__ __launch_bounds__(kB) void k_beam_merge(BeamArgs a)
 {
-    extern __shared__ double s_base[];        // of every line: score - log sum, -inf: no candidate
-    float *s_top = reinterpret_cast<float *>(s_base + a.beams);   // and what is taken from its logits first
-    __shared__ Candidate s_list[kWaves][64];
-    __shared__ int s_odd[kWaves];
+    extern __shared__ double s_base[];        // of every line, then their tops
+    float *s_top = reinterpret_cast<float *>(s_base + a.beams);
+    __shared__ Candidate s_near[kNear];
+    __shared__ int s_odd, s_count;
+    __shared__ float s_bar[kWaves];
     const int64_t req = blockIdx.x, line0 = req * a.beams;
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int tid = int(threadIdx.x), lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (tid == 0) {
+        s_odd = 0;
+        s_count = 0;
+    }
+    __syncthreads();
+    const Lines lines{a, line0, s_base, s_top};
+    const uint32_t all = a.per_line.d * uint32_t(a.beams);
+    // a thread's first entries, on their way while the lines' sums are
+    constexpr int kMine = 4;
+    Lines::Entry mine[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        mine[k] = lines.entry(uint32_t(tid + k * kB) < all ? tid + k * kB : 0);
     bool odd = false;                          // NaN or +inf where there is something to choose
-    for (int j = wave; j < a.beams; j += kWaves) {
-        const float score = a.scores[line0 + j];
-        const bool ended = a.ended && a.ended[line0 + j];
-        double base = kNone64;
-        float m = 0.0f;
-        odd |= !(score < std::numeric_limits<float>::infinity());
-        if (proposes(score, ended)) {
-            const int64_t i0 = (line0 + j) * a.chunks;
-            m = kNone;
-            for (int c = lane; c < a.chunks; c += 64)
+    const int group = a.lanes;                 // lanes that share a line's chunks
+    for (int j0 = 0; j0 < a.beams; j0 += kB / group) {
+        const int j = j0 + tid / group;
+        const bool there = j < a.beams;
+        const int64_t i0 = (line0 + (there ? j : 0)) * a.chunks, first = i0 + (tid % group < a.chunks ? tid % group : 0);
+        const float score = there ? a.scores[line0 + j] : kNone, top0 = a.tops[first];
+        const double sum0 = a.sums[first];
+        const bool ended = there && a.ended && a.ended[line0 + j], live = there && proposes(score, ended);
+        float m = live && tid % group < a.chunks ? top0 : kNone;
+        double s = 0.0;
+        if (live)
+            for (int64_t c = tid % group + group; c < a.chunks; c += group)
                 m = OpMax::apply(m, a.tops[i0 + c]);
-            m = wave_reduce<OpMax>(m);
-            odd |= !(m < std::numeric_limits<float>::infinity());
-            if (m > kNone && m < std::numeric_limits<float>::infinity()) {
-                double s = 0.0;
-                for (int c = lane; c < a.chunks; c += 64)
-                    s += a.sums[i0 + c] * exp(double(a.tops[i0 + c]) - double(m));
-                s = wave_reduce<OpSum>(s);
-                base = double(score) - log(s);
-            }
-        } else if (ended) {
-            base = double(score);
+        m = group_reduce<OpMax>(m, group);
+        const bool fine = live && m > kNone && m < std::numeric_limits<float>::infinity();
+        if (fine) {
+            if (tid % group < a.chunks)
+                s = sum0 * exp(double(top0) - double(m));
+            for (int64_t c = tid % group + group; c < a.chunks; c += group)
+                s += a.sums[i0 + c] * exp(double(a.tops[i0 + c]) - double(m));
         }
-        if (lane == 0) {
-            s_base[j] = base;
-            s_top[j] = m;
+        s = group_reduce<OpSum>(s, group);
+        odd |= there && !(score < std::numeric_limits<float>::infinity());
+        odd |= live && !(m < std::numeric_limits<float>::infinity());
+        if (there && tid % group == 0) {
+            s_base[j] = fine ? double(score) - log(s) : ended ? double(score) : kNone64;
+            s_top[j] = fine ? m : Lines::kEnded;
         }
     }
-    if (lane == 0)
-        s_odd[wave] = odd;
+    if (odd)
+        s_odd = 1;
     __syncthreads();
-    Merge best(a.count);
-    const int64_t per_line = int64_t(a.chunks) * a.count, all = per_line * a.beams;
-    for (int64_t i0 = int64_t(wave) * 64; i0 < all; i0 += kB) {
-        const int64_t i = i0 + lane;
-        Candidate v{kNone64, kNone, 0, 0};
-        if (i < all) {
-            const int j = int(i / per_line);
-            const int64_t k = i - int64_t(j) * per_line;
-            v.line = j;
-            if (a.ended && a.ended[line0 + j]) {
-                if (k == 0) {
-                    v.s = s_base[j];
-                    v.x = 0.0f;
-                    v.at = int32_t(a.end_token);
-                }
-            } else if (s_base[j] > kNone64) {
-                const int64_t e = line0 * per_line + i;
-                v.x = a.best_x[e];
-                v.at = a.best_at[e];
-                if (v.x > kNone)
-                    v.s = (double(v.x) - double(s_top[j])) + s_base[j];
-            }
+
+    // A bar below which nothing is kept: the count-th largest of the lanes' best, rounded to float32 (which keeps
+    // their order), of the wave where that is highest.
+    float low = kNone;
+    Candidate first[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        first[k] = lines.candidate(uint32_t(tid + k * kB) < all ? tid + k * kB : 0, mine[k]);
+        if (uint32_t(tid + k * kB) >= all)
+            first[k].s = kNone64;
+        low = __builtin_fmaxf(low, float(first[k].s) + 0.0f);
+    }
+    for (uint32_t i = tid + kMine * kB; i < all; i += kB)
+        low = __builtin_fmaxf(low, float(lines.candidate(i).s) + 0.0f);
+    const float bar = from_ordered(nth_largest<false>(ordered(low), a.count));
+    if (lane == 0)
+        s_bar[wave] = bar;
+    __syncthreads();
+    low = s_bar[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+        low = __builtin_fmaxf(low, s_bar[w]);
+    // What is left is ranked, all against all.
+    const auto keep = [&](const Candidate &v) {
+        if (v.s > kNone64 && float(v.s) >= low) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kNear)
+                s_near[at] = v;
         }
+    };
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        keep(first[k]);
+    for (uint32_t i = tid + kMine * kB; i < all; i += kB)
+        keep(lines.candidate(i));
+    __syncthreads();
+    const int near = s_count;
+    const bool bad = s_odd != 0;
+    const auto write = [&](int64_t o, const Candidate &c, bool some) {
+        a.best[o] = bad ? std::numeric_limits<float>::quiet_NaN() : some ? float(c.s) : kNone;
+        static_cast<Tok *>(a.tokens)[o] = some && !bad ? Tok(c.at) : Tok(-1);
+        a.parents[o] = some && !bad ? int32_t(line0 + c.line) : -1;
+    };
+    if (near <= kNear) {
+        // `share` lanes a candidate, each against every share-th; four reads on their way at once.  (One lane a
+        // candidate and one read after the other took 10 us of 19 at 64 requests of 8 lines.)
+        int share = 1;
+        while (share < 16 && near * share * 2 <= kB)
+            share *= 2;
+        for (int i0 = 0; i0 < near; i0 += kB / share) {
+            const int i = i0 + tid / share, mod = tid % share;
+            const Candidate v = s_near[i < near ? i : 0];
+            int rank = 0;
+            for (int k = mod; k < near; k += 4 * share) {
+                Candidate o[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    o[u] = s_near[k + u * share < near ? k + u * share : k];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    rank += int(o[u].before(v)) & int(k + u * share < near);
+            }
+            rank = group_reduce<OpSum>(rank, share);
+            if (mod == 0 && i < near && rank < a.count)
+                write(req * a.count + rank, v, true);
+        }
+        for (int i = near + tid; i < a.count; i += kB)
+            write(req * a.count + i, Candidate{}, false);
+        return;
+    }
+    // Too many alike: one after the other, a quarter of them a wave.
+    Merge best(a.count);
+    for (uint32_t i0 = uint32_t(wave) * 64; i0 < all; i0 += kB) {
+        Candidate v{kNone64, kNone, 0, 0};
+        if (i0 + lane < all)
+            v = lines.candidate(i0 + lane);
         best.offer(v);
     }
-    if (wave > 0)
-        s_list[wave][lane] = best.c;
+    __syncthreads();
+    s_near[wave * 64 + lane] = best.c;
     __syncthreads();
     if (wave != 0)
         return;
     for (int w = 1; w < kWaves; ++w) {
-        Candidate v = s_list[w][lane];
+        Candidate v = s_near[w * 64 + lane];
         if (lane >= a.count)
             v.s = kNone64;
         best.offer(v);
     }
-    bool bad = false;
-    for (int w = 0; w < kWaves; ++w)
-        bad |= s_odd[w] != 0;
-    if (lane < a.count) {
-        const bool some = !bad && best.c.s > kNone64;
-        const int64_t o = req * a.count + lane;
-        a.best[o] = bad ? std::numeric_limits<float>::quiet_NaN() : float(best.c.s);
-        static_cast<Tok *>(a.tokens)[o] = some ? Tok(best.c.at) : Tok(-1);
-        a.parents[o] = some ? int32_t(line0 + best.c.line) : -1;
-    }
+    if (lane < a.count)
+        write(req * a.count + lane, best.c, best.c.s > kNone64);
 }
 
 template <class In>
