@@ -77,7 +77,8 @@ constexpr int kBeamMost = 64;             // candidates kept of a request: a lan
 constexpr int kBeamLines = 4096;          // beams of a request, 12 bytes of LDS each
 // ---- forked, compacted and copied blocks
 constexpr int kPageBlock = 256;
-constexpr int kPageSeg = 1024;            // table entries a wave goes through at a time
+constexpr int kPageSeg = 1024;            // entries of a new row that a wave copies
+constexpr int kPageRows = 8;              // old rows that a wave goes through, 64 entries of each
 constexpr int kPageLdsRows = 4096;        // rows (old and new each) that every block plans for itself in LDS
 constexpr int kPageBlocksPerCu = 8;       // grid cap = CUs * this
 constexpr int kCompactChunk = 4096;       // ids whose flags a block packs
@@ -316,7 +317,7 @@ struct ForkArgs {
     Divider block;
     const int32_t *table;
     int64_t ts;
-    int max_blocks, segs;     // entries of a line, and waves that go through it
+    int max_blocks, segs;     // entries of a line, and of 64
     int32_t *ring;
     int64_t ring_size;
     const int64_t *state;
@@ -328,7 +329,7 @@ struct ForkArgs {
     // workspace
     int32_t *child;           // [rows]: the first child, none: INT32_MAX
     int32_t *gives, *takes;   // [rows], [rows_out]: blocks given back; then (many rows) those given and taken before
-    int32_t *parts;           // [rows][segs]: blocks given back by a segment
+    uint64_t *masks;          // [rows][segs]: the entries that give their blocks back
     uint32_t *owner;          // [n_blocks]: 0 where a row goes on naming the block, else the first entry naming it, + 1
     int64_t *totals;          // [4]: given back, wanted; head and tail of the ring before the call
 };

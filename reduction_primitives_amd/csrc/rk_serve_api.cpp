@@ -509,7 +509,7 @@ int rk_fork_blocks(const int32_t *parents, int64_t n_out, const int32_t *lens, i
     a.table = table;
     a.ts = table_stride;
     a.max_blocks = max_blocks;
-    a.segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
+    a.segs = (max_blocks + 63) / 64;
     a.ring = ring;
     a.ring_size = ring_size;
     a.state = state;
@@ -521,11 +521,11 @@ int rk_fork_blocks(const int32_t *parents, int64_t n_out, const int32_t *lens, i
     a.pairs = pairs;
     a.state_out = state_out;
     a.totals = static_cast<int64_t *>(workspace);
-    a.child = reinterpret_cast<int32_t *>(a.totals + 4);
+    a.masks = reinterpret_cast<uint64_t *>(a.totals + 4);
+    a.child = reinterpret_cast<int32_t *>(a.masks + n_rows * a.segs);
     a.gives = a.child + n_rows;
     a.takes = a.gives + n_rows;
-    a.parts = a.takes + n_out;
-    a.owner = reinterpret_cast<uint32_t *>(a.parts + n_rows * a.segs);
+    a.owner = reinterpret_cast<uint32_t *>(a.takes + n_out);
     L.in_lds = n_rows <= tune::kPageLdsRows && n_out <= tune::kPageLdsRows;
     L.grid = int64_t(host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus) * tune::kPageBlocksPerCu;
     L.stream = stream;

@@ -108,8 +108,7 @@ int plan_beams(int dtype, int64_t n, int64_t req, int64_t beams, int64_t count, 
 
 size_t fork_ws_bytes(int64_t rows, int64_t rows_out, int64_t max_blocks, int64_t n_blocks)
 {
-    const int64_t segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
-    return round_up_256(32 + 4 * size_t(2 * rows + rows_out + rows * segs + n_blocks));
+    return round_up_256(32 + 8 * size_t(rows * ((max_blocks + 63) / 64)) + 4 * size_t(2 * rows + rows_out + n_blocks));
 }
 
 size_t compact_ws_bytes(int64_t n_blocks)

@@ -6,17 +6,23 @@
 // free are the blocks that only rows without children name.  The first launch
 // copies the rows and marks the dead rows' entries, the second lets every dead
 // entry claim its block for the lowest entry's number while rows alive store 0
-// (no order matters: the least value stays), the third counts what each row
-// gives back, and in the fourth every block scans these counts, and the rows
-// that want a fresh block, for itself, as the block tables do.  Most entries of
-// a request's beams are shared at the same position: an entry that the nearest
-// row alive before it, or for a dead row the nearest dead one, names at the
-// same position is settled without touching the blocks' words.
+// (no order matters: the least value stays), the third keeps a bit for each entry
+// that gives its block back and counts them by row, and in the fourth every block
+// scans these counts, and the rows that want a fresh block, for itself, as the
+// block tables do.  Most entries of a request's beams are shared at the same
+// position: an entry that the nearest row alive before it, or for a dead row the
+// nearest dead one, names at the same position is settled without touching the
+// block's word.  A wave holds 64 positions of eight rows, so the table is read
+// once a launch.  256 rows of 4 k tokens: 5 + 6 + 4 + 5 us, latency; 2048 rows of
+// 64 k tokens: 23 + 34 + 15 + 17 us, bound by the words' single stores and loads
+// all over the pool (with a store that is no atomic one the second took 44 us,
+// with a byte for alive beside the word 30, but the first and third 11 more).
 //
-// compact_blocks.  A flag for each id in use, packed to 64-bit words with the
-// number of ids in use before each: the rank of any id is then two loads and a
+// compact_blocks.  A flag for each id in use, packed to words of 64 bits with the
+// number of ids in use before each: the rank of any id is then one load and a
 // population count, and the k-th used id beyond their number u and the k-th
 // free one below it are what their own ranks say, so no search is needed.
+// Entries that the row before names at the same position are looked up once.
 //
 // copy_blocks.  Pairs are read 256 at a time, those that name blocks kept in LDS
 // in their order and dealt to the `parts` thread blocks that read the same ones.
@@ -62,67 +68,108 @@ __device__ __forceinline__ Child child_of(const ForkArgs &a, int64_t r, First &&
     return c;
 }
 
-// The entries of one segment of a row, `of` the row's length: f(j, there), all
-// lanes at a time, j rising.
-template <class F>
-__device__ __forceinline__ void for_segment(int seg, int of, F &&f)
-{
-    const int from = seg * kSeg, to = from + kSeg < of ? from + kSeg : of;
-    for (int j = from; j < to; j += 64)
-        f(j + lane_id(), j + lane_id() < to);
-}
+__device__ __forceinline__ int low_lane(uint64_t lanes) { return __builtin_ctzll(lanes); }
+__device__ __forceinline__ uint64_t lanes_before(int l) { return (uint64_t(1) << l) - 1; }
 
-// Rows near a row whose entries at the same position settle its own: the
-// nearest row alive before it, and the nearest dead one.
-struct Near {
-    static constexpr int kReach = 16;
-    int64_t alive = -1, dead = -1;
-    int alive_held = 0, dead_held = 0;
+constexpr int kRows = tune::kPageRows;
 
-    template <class First>
-    __device__ __forceinline__ Near(const ForkArgs &a, int64_t row, First &&first)
+// The 64 entries at the same positions of kRows rows in a row, all on their way at
+// once: id[r] is entry col of row row0 + r, -1 where it names no block of the pool.
+// (Wider tiles are longer code that runs once: 256 entries took 14 us where these
+// take 5, at 256 rows.)
+struct Tile {
+    int64_t row0;
+    int seg, n, col;                           // n: rows that there are
+    int32_t id[kRows];
+
+    __device__ __forceinline__ Tile(int64_t item, int64_t rows, int segs)
+        : row0(int64_t(uint32_t(item) / uint32_t(segs)) * kRows), seg(int(uint32_t(item) % uint32_t(segs))),
+          n(int(rows - row0 < kRows ? rows - row0 : kRows)), col(seg * 64 + lane_id()) {}
+    template <class Args>
+    __device__ __forceinline__ int32_t read(const Args &a, int64_t row, int held) const
     {
-        for (int64_t p = row - 1; p >= 0 && p >= row - kReach && (alive < 0 || dead < 0); --p) {
-            const bool live = first(p) != kNoChild;
-            if (live && alive < 0) {
-                alive = p;
-                alive_held = clamp_held(a.held[p], a.max_blocks);
-            } else if (!live && dead < 0) {
-                dead = p;
-                dead_held = clamp_held(a.held[p], a.max_blocks);
-            }
-        }
+        return col < held ? a.table[row * a.ts + col] : -1;
     }
-    __device__ __forceinline__ bool alive_names(const ForkArgs &a, int j, int32_t id) const
+    template <class Args>
+    static __device__ __forceinline__ int32_t in_pool(const Args &a, int32_t v)
     {
-        return j < alive_held && a.table[alive * a.ts + j] == id;
+        asm volatile("" : "+v"(v));            // (the loads stay before the first of these, together)
+        return v >= 0 && v < a.n_blocks ? v : -1;
     }
-    __device__ __forceinline__ bool dead_names(const ForkArgs &a, int j, int32_t id) const
+    // held: of row row0 + r in lane lane0 + r
+    template <class Args>
+    __device__ __forceinline__ void load(const Args &a, int held, int lane0)
     {
-        return j < dead_held && a.table[dead * a.ts + j] == id;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            id[r] = read(a, r < n ? row0 + r : 0, r < n ? read_lane(held, lane0 + r) : 0);
+    }
+    template <class Args>
+    __device__ __forceinline__ void settle(const Args &a)
+    {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            id[r] = in_pool(a, id[r]);
     }
 };
 
-__device__ __forceinline__ bool in_pool(const ForkArgs &a, int32_t id) { return id >= 0 && id < a.n_blocks; }
+// A tile of the old rows, and what the nearest rows before it name at the same
+// positions: an entry that a row alive before its own names there too, or for a dead
+// row a dead one, is settled without touching the block's word.  Every launch goes
+// through the same tiles, so that it takes the same entries for settled.
+struct Old : Tile {
+    static constexpr int kLane0 = 64 - kRows;  // lanes before: rows before the tile
+    uint64_t live, dead;                       // of the rows, as lanes
+    int held;
+    int32_t by_live, by_dead;
 
-__device__ __forceinline__ uint32_t entry_number(const ForkArgs &a, int64_t row, int j)
-{
-    return uint32_t(row * a.max_blocks + j) + 1;
-}
+    template <class First>
+    __device__ __forceinline__ Old(const ForkArgs &a, int64_t item, First &&first) : Tile(item, a.rows, a.segs)
+    {
+        const int64_t p = row0 - kLane0 + lane_id();
+        const bool there = p >= 0 && p < a.rows;
+        const int32_t child = there ? first(p) : 0;
+        held = there ? clamp_held(a.held[p], a.max_blocks) : 0;
+        live = __ballot(there && child != kNoChild);
+        dead = __ballot(there && child == kNoChild);
+    }
+    __device__ __forceinline__ bool any_dead() const { return (dead >> kLane0) != 0; }
+    __device__ __forceinline__ void load(const ForkArgs &a)
+    {
+        Tile::load(a, held, kLane0);
+        const uint64_t l = live & lanes_before(kLane0), d = dead & lanes_before(kLane0);
+        const int at_l = l ? 63 - __builtin_clzll(l) : 0, at_d = d ? 63 - __builtin_clzll(d) : 0;
+        by_live = read(a, l ? row0 - kLane0 + at_l : 0, l ? read_lane(held, at_l) : 0);
+        by_dead = read(a, d ? row0 - kLane0 + at_d : 0, d ? read_lane(held, at_d) : 0);
+        settle(a);
+        by_live = in_pool(a, by_live);
+        by_dead = in_pool(a, by_dead);
+    }
+    // alive(id): entries of rows alive that are not settled; dying(r, id, may): all of dead rows, may: not settled
+    template <class Alive, class Dying>
+    __device__ __forceinline__ void walk(Alive &&alive, Dying &&dying)
+    {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t v = id[r];
+            const bool fresh = v >= 0 && v != by_live;
+            if (live >> (kLane0 + r) & 1) {
+                if (fresh)
+                    alive(v);
+                by_live = v >= 0 ? v : by_live;
+            } else {
+                dying(r, v, fresh && v != by_dead);
+                by_dead = v >= 0 ? v : by_dead;
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t number(const ForkArgs &a, int r) const
+    {
+        return uint32_t((row0 + r) * a.max_blocks + col) + 1;
+    }
+};
 
-// Whether a dead row's entry may give its block back: nothing near settles it.
-__device__ __forceinline__ bool may_give(const ForkArgs &a, const Near &n, int j, int32_t id)
-{
-    return in_pool(a, id) && !n.alive_names(a, j, id) && !n.dead_names(a, j, id);
-}
-
-__device__ __forceinline__ bool gives(const ForkArgs &a, const Near &n, int64_t row, int j, bool there, int32_t *id)
-{
-    if (!there)
-        return false;
-    *id = a.table[row * a.ts + j];
-    return may_give(a, n, j, *id) && a.owner[*id] == entry_number(a, row, j);
-}
+__device__ __forceinline__ int64_t tiles_of(int64_t rows, int segs) { return (rows + kRows - 1) / kRows * segs; }
 
 __global__ __launch_bounds__(kB) void k_fork_clear(ForkArgs a)
 {
@@ -148,10 +195,16 @@ __global__ __launch_bounds__(kB) void k_fork_rows(ForkArgs a)
         for (int r = int(threadIdx.x); r < a.rows; r += kB)
             s_child[r] = kNoChild;
         __syncthreads();
-        for (int r = int(threadIdx.x); r < a.rows_out; r += kB) {
-            const int64_t p = a.parents[r];
-            if (p >= 0 && p < a.rows)
-                atomicMin(s_child + p, r);
+        constexpr int kAhead = 8;
+        for (int r0 = int(threadIdx.x); r0 < a.rows_out; r0 += kAhead * kB) {
+            int32_t p[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                p[k] = a.parents[r0 + k * kB < a.rows_out ? r0 + k * kB : r0];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (r0 + k * kB < a.rows_out && p[k] >= 0 && p[k] < a.rows)
+                    atomicMin(s_child + p[k], r0 + k * kB);
         }
         __syncthreads();
     }
@@ -165,27 +218,41 @@ __global__ __launch_bounds__(kB) void k_fork_rows(ForkArgs a)
         a.totals[2] = a.state[0];
         a.totals[3] = a.state[1];
     }
-    const int64_t items = a.rows_out * a.segs, more = a.rows * a.segs;
-    for (int64_t i = wave_number(); i < items + more; i += wave_count()) {
-        if (i < items) {
-            const int64_t r = i / a.segs;
-            const Child c = child_of(a, r, first);
-            const int32_t *from = a.table + (c.parent < 0 ? 0 : c.parent) * a.ts;
-            int32_t *to = a.table_out + r * a.tos;
-            for_segment(int(i - r * a.segs), c.keep, [&](int j, bool there) {
-                if (there)
-                    to[j] = from[j];
-            });
-        } else {
-            const int64_t row = (i - items) / a.segs;
-            if (first(row) != kNoChild)
+    const int segs = a.max_blocks > kSeg ? (a.max_blocks + kSeg - 1) / kSeg : 1;
+    const int64_t tiles = tiles_of(a.rows, a.segs), items = tiles + a.rows_out * segs;
+    for (int64_t i = wave_number(); i < items; i += wave_count()) {
+        if (i < tiles) {
+            Old t(a, i, first);
+            if (!t.any_dead())
                 continue;
-            const Near n(a, row, first);
-            for_segment(int(i - items - row * a.segs), clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-                const int32_t id = there ? a.table[row * a.ts + j] : -1;
-                if (may_give(a, n, j, id))
+            t.load(a);
+            t.walk([](int32_t) {}, [&](int, int32_t id, bool may) {
+                if (may)
                     a.owner[id] = 0xffffffffu;
             });
+            continue;
+        }
+        const int64_t r = uint32_t(i - tiles) / uint32_t(segs);
+        const int seg = int(uint32_t(i - tiles) % uint32_t(segs)), from = seg * kSeg;
+        const Child c = child_of(a, r, first);
+        const int32_t *src = a.table + (c.parent < 0 ? 0 : c.parent) * a.ts;
+        int32_t *dst = a.table_out + r * a.tos;
+        const int to = c.keep < from + kSeg ? c.keep : from + kSeg;
+        constexpr int kAhead = 8;
+        for (int j0 = from + lane_id(); j0 < to; j0 += kAhead * 64) {
+            int32_t v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                v[k] = src[j0 + k * 64 < to ? j0 + k * 64 : j0];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (j0 + k * 64 < to)
+                    dst[j0 + k * 64] = v[k];
+        }
+        if (seg == 0 && lane_id() == 0) {
+            a.held_out[r] = c.keep;            // (its block of its own comes with the last launch)
+            a.lens_out[r] = c.len;
+            a.takes[r] = c.wants;
         }
     }
 }
@@ -193,40 +260,48 @@ __global__ __launch_bounds__(kB) void k_fork_rows(ForkArgs a)
 __global__ __launch_bounds__(kB) void k_fork_claim(ForkArgs a)
 {
     const auto first = [&](int64_t p) { return a.child[p]; };
-    for (int64_t i = wave_number(); i < a.rows * a.segs; i += wave_count()) {
-        const int64_t row = i / a.segs;
-        const int seg = int(i - row * a.segs), held = clamp_held(a.held[row], a.max_blocks);
-        const Near n(a, row, first);
-        const bool alive = first(row) != kNoChild;
-        for_segment(seg, held, [&](int j, bool there) {
-            const int32_t id = there ? a.table[row * a.ts + j] : -1;
-            if (!in_pool(a, id) || n.alive_names(a, j, id))
-                return;
-            if (alive)
-                __hip_atomic_store(a.owner + id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            else if (!n.dead_names(a, j, id))
-                __hip_atomic_fetch_min(a.owner + id, entry_number(a, row, j), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        });
+    const int64_t tiles = tiles_of(a.rows, a.segs);
+    for (int64_t i = wave_number(); i < tiles; i += wave_count()) {
+        Old t(a, i, first);
+        t.load(a);
+        t.walk([&](int32_t id) { __hip_atomic_store(a.owner + id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); },
+               [&](int r, int32_t id, bool may) {
+                   if (may)
+                       __hip_atomic_fetch_min(a.owner + id, t.number(a, r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+               });
     }
 }
 
+// What is given back: a bit for each entry, and their number.
 __global__ __launch_bounds__(kB) void k_fork_count(ForkArgs a)
 {
     const auto first = [&](int64_t p) { return a.child[p]; };
-    for (int64_t i = wave_number(); i < a.rows * a.segs; i += wave_count()) {
-        const int64_t row = i / a.segs;
-        if (first(row) != kNoChild)
-            continue;
-        const Near n(a, row, first);
-        int32_t sum = 0;
-        for_segment(int(i - row * a.segs), clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-            int32_t id;
-            sum += __popcll(__ballot(gives(a, n, row, j, there, &id)));
-        });
-        if (lane_id() == 0) {
-            a.parts[i] = sum;
-            if (sum)
-                __hip_atomic_fetch_add(a.gives + row, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int64_t tiles = tiles_of(a.rows, a.segs);
+    const int lane = lane_id();
+    for (int64_t i = wave_number(); i < tiles; i += wave_count()) {
+        Old t(a, i, first);
+        uint64_t mine = 0;                     // of row row0 + lane
+        if (t.any_dead()) {
+            t.load(a);
+            uint32_t owner[kRows];             // of what is not settled, all on their way at once
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                owner[r] = 0;
+            t.walk([](int32_t) {}, [&](int r, int32_t id, bool may) {
+                if (may)
+                    owner[r] = a.owner[id];
+            });
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                asm volatile("" : "+v"(owner[r]));
+                const uint64_t m = __ballot(owner[r] == t.number(a, r));
+                mine = lane == r ? m : mine;
+            }
+        }
+        if (lane < t.n) {
+            a.masks[(t.row0 + lane) * a.segs + t.seg] = mine;
+            if (mine)
+                __hip_atomic_fetch_add(a.gives + t.row0 + lane, __popcll(mine), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     }
 }
@@ -250,14 +325,28 @@ __device__ __forceinline__ int32_t scan_counts(int64_t n, Count &&count, To *to,
     return total;
 }
 
+// Counts read into LDS, several at once.
+__device__ __forceinline__ void counts_to(int32_t *to, const int32_t *from, int n)
+{
+    constexpr int kAhead = 8;
+    for (int i0 = int(threadIdx.x); i0 < n; i0 += kAhead * kB) {
+        int32_t v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            v[k] = from[i0 + k * kB < n ? i0 + k * kB : i0];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i0 + k * kB < n)
+                to[i0 + k * kB] = v[k];
+    }
+}
+
 // Many rows: one block's sums for all.
 __global__ __launch_bounds__(tune::kScanBlock) void k_fork_plan(ForkArgs a)
 {
     __shared__ int32_t part[tune::kScanBlock / 64];
-    const auto first = [&](int64_t p) { return a.child[p]; };
     const int32_t given = scan_counts<tune::kScanBlock>(a.rows, [&](int64_t r) { return a.gives[r]; }, a.gives, part);
-    const int32_t wanted = scan_counts<tune::kScanBlock>(a.rows_out, [&](int64_t r) { return int32_t(child_of(a, r, first).wants); },
-                                                         a.takes, part);
+    const int32_t wanted = scan_counts<tune::kScanBlock>(a.rows_out, [&](int64_t r) { return a.takes[r]; }, a.takes, part);
     if (threadIdx.x == 0) {
         a.totals[0] = given;
         a.totals[1] = wanted;
@@ -270,12 +359,14 @@ __global__ __launch_bounds__(kB) void k_fork_move(ForkArgs a)
 {
     extern __shared__ int32_t s_sums[];
     __shared__ int32_t part[kB / 64];
-    const auto first = [&](int64_t p) { return a.child[p]; };
     int64_t given, wanted;
     int32_t *s_gives = s_sums, *s_takes = s_sums + a.rows;
     if constexpr (LDS) {
-        given = scan_counts<kB>(a.rows, [&](int64_t r) { return a.gives[r]; }, s_gives, part);
-        wanted = scan_counts<kB>(a.rows_out, [&](int64_t r) { return int32_t(child_of(a, r, first).wants); }, s_takes, part);
+        counts_to(s_gives, a.gives, int(a.rows));
+        counts_to(s_takes, a.takes, int(a.rows_out));
+        __syncthreads();
+        given = scan_counts<kB>(a.rows, [&](int64_t r) { return s_gives[r]; }, s_gives, part);
+        wanted = scan_counts<kB>(a.rows_out, [&](int64_t r) { return s_takes[r]; }, s_takes, part);
     } else {
         given = a.totals[0];
         wanted = a.totals[1];
@@ -285,28 +376,44 @@ __global__ __launch_bounds__(kB) void k_fork_move(ForkArgs a)
     const int64_t head = a.totals[2], tail = a.totals[3];
     const Ring ring(head, tail, a.ring_size, given, wanted);
 
+    // 64 words of a row a wave, those that give something four at a time
+    const int words = (a.segs + 63) / 64;
     if (given > 0)
-        for (int64_t i = wave_number(); i < a.rows * a.segs; i += wave_count()) {
-            const int64_t row = i / a.segs;
-            const int seg = int(i - row * a.segs);
-            if (first(row) != kNoChild || seg * kSeg >= clamp_held(a.held[row], a.max_blocks) || a.parts[i] == 0)
+        for (int64_t i = wave_number(); i < a.rows * words; i += wave_count()) {
+            const int64_t row = uint32_t(i) / uint32_t(words), base = row * a.segs;
+            const int seg0 = int(uint32_t(i) % uint32_t(words)) * 64;
+            const uint64_t m = seg0 + lane_id() < a.segs ? a.masks[base + seg0 + lane_id()] : 0;
+            uint64_t some = __ballot(m != 0);
+            if (!some)
                 continue;
-            const Near n(a, row, first);
-            int64_t g = gives_before(row);
-            for (int s = 0; s < seg; ++s)
-                g += a.parts[row * a.segs + s];
-            for_segment(seg, clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-                int32_t id = -1;
-                const bool out = gives(a, n, row, j, there, &id);
-                const uint64_t m = __ballot(out);
-                const int64_t at = g + __popcll(m & ((uint64_t(1) << lane_id()) - 1));
-                if (out && at < ring.given)
-                    a.ring[wrap(ring.head + ring.there + at, a.ring_size)] = id;   // (head + there + given <= head + size)
-                g += __popcll(m);
-            });
+            int32_t before = 0;
+            for (int s = lane_id(); s < seg0; s += 64)
+                before += __popcll(a.masks[base + s]);
+            const int32_t count = __popcll(m);
+            const int64_t g0 = gives_before(row) + (seg0 ? wave_reduce<OpSum>(before) : 0);
+            const int32_t g = wave_prefix<Plus>(count) - count;
+            while (some) {
+                constexpr int kAhead = 4;
+                int l[kAhead];
+                int32_t id[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    l[k] = some ? low_lane(some) : -1;
+                    some &= some - 1;
+                    const int j = (seg0 + (l[k] < 0 ? l[0] : l[k])) * 64 + lane_id();
+                    id[k] = a.table[row * a.ts + (j < a.max_blocks ? j : 0)];
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const uint64_t mk = l[k] < 0 ? 0 : read_lane(m, l[k] < 0 ? 0 : l[k]);
+                    const int64_t at = g0 + read_lane(g, l[k] < 0 ? 0 : l[k]) + __popcll(mk & lanes_before(lane_id()));
+                    if ((mk >> lane_id() & 1) && at < ring.given)
+                        a.ring[wrap(ring.head + ring.there + at, a.ring_size)] = id[k];   // (head + there + given <= head + size)
+                }
+            }
         }
 
-    // the id of give number g, found by a whole wave (g the same in all lanes)
+    // the id of give number g
     const auto given_id = [&](int64_t g) {
         int64_t row = 0, hi = a.rows;          // the last row with at most g given before it
         while (hi - row > 1) {
@@ -316,53 +423,26 @@ __global__ __launch_bounds__(kB) void k_fork_move(ForkArgs a)
             else
                 hi = mid;
         }
-        int64_t k = g - gives_before(row);
-        int seg = 0;
-        while (seg + 1 < a.segs && k >= a.parts[row * a.segs + seg]) {
-            k -= a.parts[row * a.segs + seg];
-            ++seg;
-        }
-        const Near n(a, row, first);
-        int32_t found = -1;
-        for_segment(seg, clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-            int32_t id = -1;
-            const bool out = gives(a, n, row, j, there, &id);
-            const uint64_t m = __ballot(out);
-            const bool it = out && k == __popcll(m & ((uint64_t(1) << lane_id()) - 1));
-            const uint64_t at = __ballot(it);
-            if (at)
-                found = read_lane(id, __builtin_ctzll(at));
+        int64_t k = g - gives_before(row), i = row * a.segs;
+        uint64_t m = a.masks[i];
+        for (; k >= __popcll(m); m = a.masks[++i])
             k -= __popcll(m);
-        });
-        return found;
+        for (; k > 0; --k)
+            m &= m - 1;
+        return a.table[row * a.ts + (i - row * a.segs) * 64 + low_lane(m)];
     };
-    for (int64_t r0 = wave_number() * 64; r0 < a.rows_out; r0 += wave_count() * 64) {
-        const int64_t r = r0 + lane_id();
-        Child c{-1, 0, 0, 0, false, false};
-        int32_t fresh = -1;
-        int64_t t = 0;
-        bool got = false;
-        if (r < a.rows_out) {
-            c = child_of(a, r, first);
-            t = takes_before(r);
-            got = c.wants && t < ring.taken;
-            if (got && t < ring.there)
-                fresh = a.ring[wrap(ring.head + t, a.ring_size)];
+    for (int64_t r = int64_t(blockIdx.x) * kB + threadIdx.x; r < a.rows_out; r += int64_t(gridDim.x) * kB) {
+        const int64_t t = takes_before(r), next = r + 1 < a.rows_out ? takes_before(r + 1) : wanted;
+        int32_t from = -1, fresh = -1;
+        if (next > t && t < ring.taken) {
+            const int keep = a.held_out[r];
+            from = a.table[a.parents[r] * a.ts + keep];
+            fresh = t < ring.there ? a.ring[wrap(ring.head + t, a.ring_size)] : given_id(t - ring.there);
+            a.table_out[r * a.tos + keep] = fresh;
+            a.held_out[r] = keep + 1;
         }
-        for (uint64_t rest = __ballot(got && t >= ring.there); rest; rest &= rest - 1) {
-            const int l = __builtin_ctzll(rest);
-            const int32_t id = given_id(read_lane(t, l) - ring.there);
-            if (lane_id() == l)
-                fresh = id;
-        }
-        if (r < a.rows_out) {
-            a.held_out[r] = c.keep + got;
-            a.lens_out[r] = c.len;
-            a.pairs[2 * r] = got ? a.table[c.parent * a.ts + c.keep] : -1;
-            a.pairs[2 * r + 1] = got ? fresh : -1;
-            if (got)
-                a.table_out[r * a.tos + c.keep] = fresh;
-        }
+        a.pairs[2 * r] = from;
+        a.pairs[2 * r + 1] = fresh;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.state_out[0] = head + ring.taken;
@@ -370,6 +450,15 @@ __global__ __launch_bounds__(kB) void k_fork_move(ForkArgs a)
         a.state_out[2] = wanted - ring.taken;
         a.state_out[3] = given - ring.given;
     }
+}
+
+// What the compaction still goes through row by row.
+template <class F>
+__device__ __forceinline__ void for_segment(int seg, int of, F &&f)
+{
+    const int from = seg * kSeg, to = from + kSeg < of ? from + kSeg : of;
+    for (int j = from; j < to; j += 64)
+        f(j + lane_id(), j + lane_id() < to);
 }
 
 // -------------------------------------------------------------------- compact
@@ -556,9 +645,9 @@ int launch_fork(const ForkLaunch &L)
         if (!launched())
             return ST_HIP;
     }
-    const int64_t old = a.rows * a.segs, items = old + a.rows_out * a.segs;
-    const dim3 grid(uint32_t(blocks_for(items, L.grid))), grid_old(uint32_t(blocks_for(old, L.grid)));
-    const int64_t moving = old > (a.rows_out + 63) / 64 ? old : (a.rows_out + 63) / 64;
+    const int64_t tiles = (a.rows + kRows - 1) / kRows * a.segs, items = tiles + a.rows_out * (a.max_blocks > kSeg ? (a.max_blocks + kSeg - 1) / kSeg : 1);
+    const dim3 grid(uint32_t(blocks_for(items, L.grid))), grid_old(uint32_t(blocks_for(tiles, L.grid)));
+    const int64_t old = a.rows * ((a.segs + 63) / 64), moving = old > (a.rows_out + 63) / 64 ? old : (a.rows_out + 63) / 64;
     const dim3 grid_move(uint32_t(blocks_for(moving, L.grid)));
     if (L.in_lds)
         launch_timed(k_fork_rows<true>, grid, block, size_t(a.rows) * 4, L.stream, L.ev_begin, L.ev_end, a);
