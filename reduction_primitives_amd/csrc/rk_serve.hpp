@@ -82,6 +82,7 @@ constexpr int kPageRows = 8;              // old rows that a wave goes through, 
 constexpr int kPageLdsRows = 4096;        // rows (old and new each) that every block plans for itself in LDS
 constexpr int kPageBlocksPerCu = 8;       // grid cap = CUs * this
 constexpr int kCompactChunk = 4096;       // ids whose flags a block packs
+constexpr int kCompactSums = 4096;        // chunks that every block sums up for itself
 constexpr int kCopyCaches = 64;           // caches of a launch
 constexpr int kCopyBlocksPerCu = 16;      // blocks of a launch = CUs * this, or one a pair of a chunk
 constexpr int kCopyChunk = 16384;         // bytes of a cache's block that a thread block copies at a time
@@ -343,10 +344,16 @@ struct ForkLaunch {
 int launch_fork(const ForkLaunch &L);
 size_t fork_ws_bytes(int64_t rows, int64_t rows_out, int64_t max_blocks, int64_t n_blocks);
 
+// 64 ids: those in use, and the number in use before them, of their chunk and of all.
+struct alignas(16) CompactWord {
+    uint64_t used;
+    int32_t before, rank;
+};
+
 struct CompactArgs {
     const int32_t *held, *table;
     int64_t rows, ts;
-    int max_blocks, segs;
+    int max_blocks, segs;     // entries of a line, and of 64
     int64_t n_blocks;
     int32_t *table_out;
     int64_t tos;
@@ -355,9 +362,9 @@ struct CompactArgs {
     int64_t *state_out;
     // workspace
     uint8_t *used;            // [chunks * kCompactChunk]
-    uint64_t *bits;           // [chunks * kCompactChunk / 64]
-    uint16_t *before;         // of each word: blocks in use of its chunk before it
-    int32_t *chunk;           // [chunks + 1]: blocks in use in a chunk; then before it (at last: all)
+    CompactWord *words;       // [chunks * kCompactChunk / 64]
+    int32_t *chunk;           // [chunks + 1]: blocks in use in a chunk; many chunks: then before it (at last: all)
+    int64_t *totals;          // [2]: blocks in use, those of them below their number
     int64_t chunks;
 };
 

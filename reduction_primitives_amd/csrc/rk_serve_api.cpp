@@ -581,7 +581,7 @@ int rk_compact_blocks(const int32_t *held, int64_t n_rows, const int32_t *table,
     a.rows = n_rows;
     a.ts = table_stride;
     a.max_blocks = max_blocks;
-    a.segs = (max_blocks + tune::kPageSeg - 1) / tune::kPageSeg;
+    a.segs = (max_blocks + 63) / 64;
     a.n_blocks = n_blocks;
     a.table_out = table_out;
     a.tos = table_out_stride;
@@ -591,9 +591,9 @@ int rk_compact_blocks(const int32_t *held, int64_t n_rows, const int32_t *table,
     a.state_out = state_out;
     a.chunks = (n_blocks + tune::kCompactChunk - 1) / tune::kCompactChunk;
     a.used = static_cast<uint8_t *>(workspace);
-    a.bits = reinterpret_cast<uint64_t *>(a.used + a.chunks * tune::kCompactChunk);
-    a.chunk = reinterpret_cast<int32_t *>(a.bits + a.chunks * (tune::kCompactChunk / 64));
-    a.before = reinterpret_cast<uint16_t *>(a.chunk + a.chunks + 1);
+    a.words = reinterpret_cast<CompactWord *>(a.used + a.chunks * tune::kCompactChunk);
+    a.totals = reinterpret_cast<int64_t *>(a.words + a.chunks * (tune::kCompactChunk / 64));
+    a.chunk = reinterpret_cast<int32_t *>(a.totals + 2);
     L.grid = int64_t(host::device_cus() > 0 ? host::device_cus() : tune::kDefaultCus) * tune::kPageBlocksPerCu;
     L.stream = stream;
     host::launch_events(&L.ev_begin, &L.ev_end);

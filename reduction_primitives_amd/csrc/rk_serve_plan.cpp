@@ -114,7 +114,7 @@ size_t fork_ws_bytes(int64_t rows, int64_t rows_out, int64_t max_blocks, int64_t
 size_t compact_ws_bytes(int64_t n_blocks)
 {
     const size_t chunks = size_t((n_blocks + tune::kCompactChunk - 1) / tune::kCompactChunk);
-    return round_up_256(chunks * (tune::kCompactChunk + tune::kCompactChunk / 64 * 10) + (chunks + 1) * 4);
+    return round_up_256(16 + chunks * (tune::kCompactChunk + tune::kCompactChunk / 64 * sizeof(CompactWord)) + (chunks + 1) * 4);
 }
 
 Divider make_divider(uint32_t d)

@@ -22,7 +22,11 @@
 // number of ids in use before each: the rank of any id is then one load and a
 // population count, and the k-th used id beyond their number u and the k-th
 // free one below it are what their own ranks say, so no search is needed.
-// Entries that the row before names at the same position are looked up once.
+// Entries that the row before names at the same position are marked and looked up
+// once.  256 rows of 4 k tokens: 2 + 4 + 3 + 6 + 5 us in five launches, latency;
+// 4096 rows of 16 k tokens in a pool of 4 times what is used: 4 + 16 + 4 + 12 + 18
+// us, bound by single bytes and words all over the pool (each row by itself, with
+// three loads a rank: 5 + 24 + 7 + 10 + 32 and a launch for the sums).
 //
 // copy_blocks.  Pairs are read 256 at a time, those that name blocks kept in LDS
 // in their order and dealt to the `parts` thread blocks that read the same ones.
@@ -452,15 +456,6 @@ __global__ __launch_bounds__(kB) void k_fork_move(ForkArgs a)
     }
 }
 
-// What the compaction still goes through row by row.
-template <class F>
-__device__ __forceinline__ void for_segment(int seg, int of, F &&f)
-{
-    const int from = seg * kSeg, to = from + kSeg < of ? from + kSeg : of;
-    for (int j = from; j < to; j += 64)
-        f(j + lane_id(), j + lane_id() < to);
-}
-
 // -------------------------------------------------------------------- compact
 
 __global__ __launch_bounds__(kB) void k_compact_clear(CompactArgs a)
@@ -472,42 +467,55 @@ __global__ __launch_bounds__(kB) void k_compact_clear(CompactArgs a)
 
 __global__ __launch_bounds__(kB) void k_compact_mark(CompactArgs a)
 {
-    for (int64_t i = wave_number(); i < a.rows * a.segs; i += wave_count()) {
-        const int64_t row = i / a.segs;
-        for_segment(int(i - row * a.segs), clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-            const int32_t id = there ? a.table[row * a.ts + j] : -1;
-            if (id >= 0 && id < a.n_blocks)
-                a.used[id] = 1;
-        });
+    const int64_t tiles = tiles_of(a.rows, a.segs);
+    for (int64_t i = wave_number(); i < tiles; i += wave_count()) {
+        Tile t(i, a.rows, a.segs);
+        const int64_t p = t.row0 - 1 + lane_id();
+        const int held = p >= 0 && p < a.rows ? clamp_held(a.held[p], a.max_blocks) : 0;
+        t.load(a, held, 1);
+        int32_t by = t.read(a, t.row0 > 0 ? t.row0 - 1 : 0, read_lane(held, 0));   // (that row's wave marks it)
+        t.settle(a);
+        by = Tile::in_pool(a, by);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t v = t.id[r];
+            if (v >= 0 && v != by)
+                a.used[v] = 1;
+            by = v >= 0 ? v : by;
+        }
     }
 }
 
 // Flags to words, a chunk of kCompactChunk ids a block.
 __global__ __launch_bounds__(kB) void k_compact_pack(CompactArgs a)
 {
-    constexpr int kWords = tune::kCompactChunk / 64, kEach = kWords / (kB / 64);
+    constexpr int kWords = tune::kCompactChunk / 64, kMine = kWords / (kB / 64);
+    static_assert(kWords == 64 && kMine == 16, "a wave packs the words whose numbers its lanes 0 .. 15 hold");
     __shared__ int32_t counts[kWords];
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)), lane = lane_id();
     const int64_t base = int64_t(blockIdx.x) * tune::kCompactChunk, word = int64_t(blockIdx.x) * kWords;
-#pragma unroll 4
-    for (int i = 0; i < kEach; ++i) {
-        const int w = wave * kEach + i;
-        const uint64_t m = __ballot(a.used[base + w * 64 + lane_id()] != 0);
-        if (lane_id() == 0) {
-            a.bits[word + w] = m;
-            counts[w] = __popcll(m);
-        }
+    uint8_t flag[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        flag[i] = a.used[base + (wave * kMine + i) * 64 + lane];
+    uint64_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const uint64_t m = __ballot(flag[i] != 0);
+        mine = lane == i ? m : mine;
     }
+    if (lane < kMine)
+        counts[wave * kMine + lane] = __popcll(mine);
     __syncthreads();
-    static_assert(kWords == 64, "one wave scans a chunk's words");
-    if (wave == 0) {
-        const int32_t incl = wave_prefix<Plus>(counts[lane_id()]);
-        a.before[word + lane_id()] = uint16_t(incl - counts[lane_id()]);
-        if (lane_id() == 63)
-            a.chunk[blockIdx.x] = incl;
-    }
+    const int32_t count = counts[lane], incl = wave_prefix<Plus>(count), before = incl - count;
+    const int32_t at = int32_t(bpermute32(uint32_t(before), wave * kMine + (lane & (kMine - 1))));
+    if (lane < kMine)
+        a.words[word + wave * kMine + lane] = CompactWord{mine, at, 0};
+    if (wave == 0 && lane == 63)
+        a.chunk[blockIdx.x] = incl;
 }
 
+// Many chunks: one block's sums for all.
 __global__ __launch_bounds__(tune::kScanBlock) void k_compact_scan(CompactArgs a)
 {
     __shared__ int32_t part[tune::kScanBlock / 64];
@@ -516,39 +524,81 @@ __global__ __launch_bounds__(tune::kScanBlock) void k_compact_scan(CompactArgs a
         a.chunk[a.chunks] = all;
 }
 
-// Blocks in use below an id (0 <= id < chunks * kCompactChunk).
-__device__ __forceinline__ int64_t rank_of(const CompactArgs &a, int64_t id, uint64_t *word)
+// Sums over chunks [0, end) and [0, all), in every thread.
+__device__ __forceinline__ int2 sum_chunks(const CompactArgs &a, int64_t end, int64_t all, int2 *part)
 {
-    *word = a.bits[id >> 6];
-    return int64_t(a.chunk[id / tune::kCompactChunk]) + a.before[id >> 6] + __popcll(*word & ((uint64_t(1) << (id & 63)) - 1));
+    int2 v = make_int2(0, 0);
+    for (int64_t c = threadIdx.x; c < all; c += kB) {
+        const int32_t n = a.chunk[c];
+        v.x += c < end ? n : 0;
+        v.y += n;
+    }
+    v = make_int2(wave_reduce<OpSum>(v.x), wave_reduce<OpSum>(v.y));
+    __syncthreads();
+    if (lane_id() == 0)
+        part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < kB / 64; ++w)
+        v = make_int2(v.x + part[w].x, v.y + part[w].y);
+    return v;
 }
 
-__device__ __forceinline__ int64_t used_below(const CompactArgs &a, int64_t id)
-{
-    uint64_t w;
-    return id < a.n_blocks ? rank_of(a, id, &w) : a.chunk[a.chunks];
-}
-
-// The moves, and the ring of what is free after them.
+// The moves, and the ring of what is free after them; each word's rank.  A chunk a block.
+template <bool SCANNED>
 __global__ __launch_bounds__(kB) void k_compact_pairs(CompactArgs a)
 {
-    const int64_t u = a.chunk[a.chunks], kept = used_below(a, u), moves = u - kept;
-    for (int64_t id = int64_t(blockIdx.x) * kB + threadIdx.x; id < a.n_blocks; id += int64_t(gridDim.x) * kB) {
-        uint64_t w;
-        const int64_t r = rank_of(a, id, &w);
-        const bool used = (w >> (id & 63)) & 1;
-        if (used && id >= u)
-            a.pairs[2 * (r - kept)] = int32_t(id);
-        else if (!used && id < u)
-            a.pairs[2 * (id - r) + 1] = int32_t(id);
-        if (id >= u)
-            a.ring[id - u] = int32_t(id);
+    __shared__ int2 part[kB / 64];
+    constexpr int kWords = tune::kCompactChunk / 64;
+    const int64_t own = blockIdx.x;
+    int64_t base, u, kept = 0;                 // used before the chunk; in all; below u
+    if constexpr (SCANNED) {
+        base = a.chunk[own];
+        u = a.chunk[a.chunks];
+    } else {
+        const int2 v = sum_chunks(a, own, a.chunks, part);
+        base = v.x;
+        u = v.y;
+    }
+    if (u < a.n_blocks) {
+        const int64_t c = u / tune::kCompactChunk;
+        kept = SCANNED ? a.chunk[c] : sum_chunks(a, c, c, part).x;
+        const CompactWord w = a.words[u >> 6];
+        kept += w.before + __popcll(w.used & lanes_before(int(u & 63)));
+    } else {
+        kept = u;
+    }
+    const int64_t moves = u - kept;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)), lane = lane_id();
+    const int64_t word0 = own * kWords + wave * (kWords / (kB / 64));
+    constexpr int kMine = kWords / (kB / 64);
+    if (own < a.chunks) {
+        const CompactWord mine = a.words[word0 + (lane & (kMine - 1))];
+        const int32_t rank = int32_t(base) + mine.before;
+        if (lane < kMine)
+            a.words[word0 + lane].rank = rank;
+#pragma unroll 4
+        for (int i = 0; i < kMine; ++i) {
+            const uint64_t m = read_lane(mine.used, i);
+            const int64_t r = read_lane(rank, i) + __popcll(m & lanes_before(lane)), id = (word0 + i) * 64 + lane;
+            const bool used = m >> lane & 1;
+            if (id < a.n_blocks) {
+                if (used && id >= u)
+                    a.pairs[2 * (r - kept)] = int32_t(id);
+                else if (!used && id < u)
+                    a.pairs[2 * (id - r) + 1] = int32_t(id);
+                if (id >= u)
+                    a.ring[id - u] = int32_t(id);
+            }
+        }
     }
     for (int64_t k = moves + int64_t(blockIdx.x) * kB + threadIdx.x; k < a.max_pairs; k += int64_t(gridDim.x) * kB) {
         a.pairs[2 * k] = -1;
         a.pairs[2 * k + 1] = -1;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.totals[0] = u;
+        a.totals[1] = kept;
         a.state_out[0] = 0;
         a.state_out[1] = a.n_blocks - u;
         a.state_out[2] = moves;
@@ -556,21 +606,51 @@ __global__ __launch_bounds__(kB) void k_compact_pairs(CompactArgs a)
     }
 }
 
+// (The row before a tile is not looked at: it may have its new ids already.)
 __global__ __launch_bounds__(kB) void k_compact_tables(CompactArgs a)
 {
-    const int64_t u = a.chunk[a.chunks], kept = used_below(a, u);
-    for (int64_t i = wave_number(); i < a.rows * a.segs; i += wave_count()) {
-        const int64_t row = i / a.segs;
-        for_segment(int(i - row * a.segs), clamp_held(a.held[row], a.max_blocks), [&](int j, bool there) {
-            if (!there)
-                return;
-            int32_t id = a.table[row * a.ts + j];
-            if (id >= u && id < a.n_blocks) {
-                uint64_t w;
-                id = a.pairs[2 * (rank_of(a, id, &w) - kept) + 1];
+    const int64_t u = a.totals[0], kept = a.totals[1], tiles = tiles_of(a.rows, a.segs);
+    for (int64_t i = wave_number(); i < tiles; i += wave_count()) {
+        Tile t(i, a.rows, a.segs);
+        const int64_t p = t.row0 + lane_id();
+        const int held = p < a.rows && lane_id() < kRows ? clamp_held(a.held[p], a.max_blocks) : 0;
+        t.load(a, held, 0);
+        // three rounds of loads, each for all rows at once: entries, their words, their places
+        uint64_t used[kRows];
+        int32_t rank[kRows], to[kRows], by = -1;
+        bool look[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            asm volatile("" : "+v"(t.id[r]));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t v = t.id[r];
+            look[r] = v >= u && v < a.n_blocks && v != by;   // (u >= 0; entries that are not there are -1)
+            by = v >= u && v < a.n_blocks ? v : by;
+            used[r] = 0;
+            rank[r] = 0;
+            if (look[r]) {
+                used[r] = a.words[v >> 6].used;
+                rank[r] = a.words[v >> 6].rank;
             }
-            a.table_out[row * a.tos + j] = id;
-        });
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            asm volatile("" : "+v"(used[r]), "+v"(rank[r]));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            to[r] = 0;
+            if (look[r])
+                to[r] = a.pairs[2 * (int64_t(rank[r]) + __popcll(used[r] & lanes_before(t.id[r] & 63)) - kept) + 1];
+        }
+        int32_t last = 0;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int32_t v = t.id[r];
+            last = look[r] ? to[r] : last;
+            if (t.col < read_lane(held, r))
+                a.table_out[(t.row0 + r) * a.tos + t.col] = v >= u && v < a.n_blocks ? last : v;
+        }
     }
 }
 
@@ -668,14 +748,18 @@ int launch_compact(const CompactLaunch &L)
 {
     const CompactArgs &a = L.a;
     hipStream_t st = static_cast<hipStream_t>(L.stream);
-    const dim3 block(kB), rows(uint32_t(blocks_for(a.rows * a.segs, L.grid)));
-    const dim3 ids(uint32_t(blocks_for((a.n_blocks + 63) / 64, L.grid)));
-    launch_timed(k_compact_clear, ids, block, 0, L.stream, L.ev_begin, L.ev_end, a);
+    const dim3 block(kB), rows(uint32_t(blocks_for((a.rows + kRows - 1) / kRows * a.segs, L.grid)));
+    const dim3 chunks(uint32_t(a.chunks > 0 ? a.chunks : 1));
+    launch_timed(k_compact_clear, chunks, block, 0, L.stream, L.ev_begin, L.ev_end, a);
     hipLaunchKernelGGL(k_compact_mark, rows, block, 0, st, a);
     if (a.chunks > 0)
-        hipLaunchKernelGGL(k_compact_pack, dim3(uint32_t(a.chunks)), block, 0, st, a);
-    hipLaunchKernelGGL(k_compact_scan, dim3(1), dim3(tune::kScanBlock), 0, st, a);
-    hipLaunchKernelGGL(k_compact_pairs, ids, block, 0, st, a);
+        hipLaunchKernelGGL(k_compact_pack, chunks, block, 0, st, a);
+    if (a.chunks > tune::kCompactSums) {
+        hipLaunchKernelGGL(k_compact_scan, dim3(1), dim3(tune::kScanBlock), 0, st, a);
+        hipLaunchKernelGGL(k_compact_pairs<true>, chunks, block, 0, st, a);
+    } else {
+        hipLaunchKernelGGL(k_compact_pairs<false>, chunks, block, 0, st, a);
+    }
     hipLaunchKernelGGL(k_compact_tables, rows, block, 0, st, a);
     return launched() ? ST_OK : ST_HIP;
 }

@@ -363,6 +363,21 @@ def test_compact_pools(pool, share):
             assert np.array_equal(g.cpu().numpy(), w), name
 
 
+def test_compact_pool_of_many_chunks():
+    """More than 4096 chunks of 4096 ids: their counts are summed by a launch of its own."""
+    rk = _rk()
+    rng = np.random.default_rng(8)
+    pool = 4096 * 4097 + 13
+    ids = np.unique(np.concatenate([rng.integers(0, pool, 6000), [0, 4095, 4096, pool - 1, pool - 14, pool // 2]]))
+    table = np.concatenate([rng.permutation(ids), rng.permutation(ids)]).reshape(2, -1)
+    d = lambda v: torch.from_numpy(np.asarray(v)).to(torch.int32).to(DEV)  # noqa: E731
+    dr, ring = d(np.full(pool, -3)), np.full(pool, -3)
+    got, pairs, state = rk.compact_blocks(i32([len(ids)] * 2), d(table), dr, pool)
+    want = ref.compact_blocks([len(ids)] * 2, table, ring, pool, pool // 2)
+    for name, g, w in zip(("table", "pairs", "state", "ring"), (got, pairs, state, dr), want):
+        assert np.array_equal(g.cpu().numpy(), w), name
+
+
 def test_compact_of_nothing():
     rk = _rk()
     z = torch.zeros(0, dtype=torch.int32, device=DEV)
