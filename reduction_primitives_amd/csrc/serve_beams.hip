@@ -8,15 +8,18 @@
 // largest logits, and one pass over the logits finds both them and the sum.
 //
 // First launch: a wave takes consecutive tiles of a line, every lane keeping its
-// own running maximum and sum.  The wave's best so far are a list across its
-// lanes, sorted, and an entry is looked at again only if it passes the list's
-// last one: after the first tile, one comparison of a lane's largest entry for 32.
-// There the bar is the count-th largest of the lanes' maxima, found bit by bit
-// with ballots.  Entries are inserted in the order of their tokens, so of equal
-// ones the first stays first.
+// own running maximum and sum.  What passes the wave's bar goes to a list in LDS, in
+// any order, and when that holds more than 64 the count-th largest is found bit by
+// bit with ballots, the rest dropped, and the bar raised to it; a tile none of whose
+// lanes' largest entries passes costs one comparison.  In the first tile the bar is
+// the count-th largest of the lanes' maxima, later also what other waves of the block
+// have for the same line.  (A sorted list across the lanes, each entry put in its
+// place: 50 instructions an entry, more than the exponentials, and 41 us where this
+// takes XX, at 512 lines of 131072 bf16.)  Equal entries without end, as in a line of
+// one value, are put into such a list all the same, one after the other.
 //
-// Second launch: a block a request folds its lines' sums and merges their lists
-// the same way, in float64.
+// Second launch: a block a request folds its lines' sums, finds a bar the same way,
+// and ranks what is left, all against all, in float64.
 #define RK_UNIT unit_serve_beams
 #include "rk_serve_device.hpp"
 
@@ -39,24 +42,43 @@ __device__ __forceinline__ int32_t ordered(float v)
 
 __device__ __forceinline__ float from_ordered(int32_t i) { return bitcast<float>(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// The n-th largest of the lanes' values (no NaN), found bit by bit.  COARSE: values
-// whose low 16 bits do not matter (as integers of this order all 0 or all 1): a bound
-// that n lanes reach, at most a last place of 16 bits below it.
-template <bool COARSE>
-__device__ __forceinline__ int32_t nth_largest(int32_t v, int n)
+// The n-th largest of the values of the lanes, two a lane (no NaN), found bit by bit,
+// as an unsigned integer of the same order, for values whose LOW lowest bits do not
+// matter (all 0 or all 1).  n values are at least it.
+template <int LOW>
+__device__ __forceinline__ uint32_t nth_of(uint32_t u, uint32_t w, int n)
 {
-    const uint32_t u = uint32_t(v) ^ 0x80000000u;
     uint32_t b = 0;
 #pragma unroll
-    for (int bit = 31; bit >= (COARSE ? 16 : 0); --bit) {
+    for (int bit = 31; bit >= LOW; --bit) {
+        const uint32_t with = b | (1u << bit);
+        b = __popcll(__ballot(u >= with)) + __popcll(__ballot(w >= with)) >= n ? with : b;
+    }
+    return b;
+}
+
+__device__ __forceinline__ uint32_t rising(float v) { return uint32_t(ordered(v)) ^ 0x80000000u; }
+
+// One value a lane.
+template <int LOW>
+__device__ __forceinline__ float nth_largest(float v, int n)
+{
+    const uint32_t u = rising(v);
+    uint32_t b = 0;
+#pragma unroll
+    for (int bit = 31; bit >= LOW; --bit) {
         const uint32_t with = b | (1u << bit);
         b = __popcll(__ballot(u >= with)) >= n ? with : b;
     }
-    return int32_t(b ^ 0x80000000u);
+    return from_ordered(int32_t((b >> 31 ? b : b | ((1u << LOW) - 1)) ^ 0x80000000u));
 }
 
-// The next smaller float (-0 is 0).
-__device__ __forceinline__ float below(int32_t v) { return from_ordered(v == 0 ? -2 : v - 1); }
+// The next smaller float (of 0 and -0 what is below both).
+__device__ __forceinline__ float below(float v)
+{
+    const int32_t i = ordered(v);
+    return from_ordered(i == 0 ? -2 : i - 1);
+}
 
 template <class T>
 __device__ __forceinline__ T lane_before(T v)
@@ -66,7 +88,7 @@ __device__ __forceinline__ T lane_before(T v)
     });
 }
 
-// A wave's best entries, the i-th in lane i.
+// A wave's best entries in order, the i-th in lane i.
 struct Best {
     float x;
     int32_t at;
@@ -75,10 +97,10 @@ struct Best {
 
     __device__ explicit Best(int count) : x(kNone), at(-1), bar(kNone), n(count) {}
 
-    // (wave-uniform v and i, in the order of i)
+    // (wave-uniform v and i)
     __device__ __forceinline__ void insert(float v, int32_t i)
     {
-        const int p = __popcll(__ballot(x >= v)), lane = lane_id();
+        const int p = __popcll(__ballot(x > v || (x == v && at < i))), lane = lane_id();
         const float px = lane_before(x);
         const int32_t pa = lane_before(at);
         x = lane < p ? x : lane == p ? v : px;
@@ -92,6 +114,7 @@ template <class In>
 struct Tile {
     using S = typename InTraits<In>::S;
     static constexpr int V = InTraits<In>::vec, U = kTile / (64 * V);
+    static constexpr int LOW = std::is_same_v<In, bf16_in> ? 16 : std::is_same_v<In, f16_in> ? 13 : 0;   // bits that are all alike
     float v[U][V];
 
     // A whole tile as it comes from memory.
@@ -107,16 +130,11 @@ struct Tile {
 
     __device__ __forceinline__ static int place(int u) { return (u * 64 + lane_id()) * V; }
 
-    // (-0 is 0)
     __device__ __forceinline__ void decode(const Raw &r)
     {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u)
             InTraits<In>::decode(r.w[u], v[u]);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                v[u][k] += 0.0f;
-        }
     }
 
     // the line's end: `left` entries, fewer than a tile's
@@ -126,7 +144,7 @@ struct Tile {
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                v[u][k] = place(u) + k < left ? InTraits<In>::template one<float>(x[place(u) + k]) + 0.0f : kNone;
+                v[u][k] = place(u) + k < left ? InTraits<In>::template one<float>(x[place(u) + k]) : kNone;
     }
 
     __device__ __forceinline__ float largest(int u) const
@@ -138,26 +156,142 @@ struct Tile {
         return m;
     }
 
+    // f(u, k, which lanes' entries pass)
+    template <class F>
+    __device__ __forceinline__ void passing(const float (&tops)[U], float bar, F &&f) const
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (__ballot(tops[u] > bar))
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const uint64_t m = __ballot(v[u][k] > bar);
+                    if (m)
+                        f(u, k, m);
+                }
+    }
+
+    // one after the other, in the order of their tokens
     __device__ __forceinline__ void select(Best &best, int32_t base) const
     {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // entries that pass the bar as it was, lane by lane: in the order of their tokens
-            uint64_t over[V], any = 0;
+            float m = largest(u);
+            for (uint64_t hit = __ballot(m > best.bar); hit;) {
+                const int l = __builtin_ctzll(hit);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                any |= over[k] = __ballot(v[u][k] > best.bar);
-            for (; any; any &= any - 1) {
-                const int l = __builtin_ctzll(any);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (over[k] >> l & 1) {
-                        const float x = read_lane(v[u][k], l);
-                        if (x > best.bar)
-                            best.insert(x, base + (u * 64 + l) * V + k);
-                    }
+                for (int k = 0; k < V; ++k) {
+                    const float x = read_lane(v[u][k], l);
+                    if (x > best.bar)
+                        best.insert(x, base + (u * 64 + l) * V + k);
+                }
+                hit = l == 63 ? 0 : __ballot(m > best.bar) & (~uint64_t(0) << (l + 1));
             }
         }
+    }
+};
+
+constexpr int kList = 128;
+
+// A wave's entries that may be among its line's best, in LDS.
+template <class In>
+struct List {
+    using T = Tile<In>;
+    float *x;
+    int32_t *at;
+    int n, count;
+    float bar;                // at least `count` entries of the line are larger or, of lower tokens, as large
+
+    __device__ __forceinline__ static void in_order()
+    {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    __device__ __forceinline__ void take(const T &t, const float (&tops)[T::U], int32_t base)
+    {
+        const int before = n, lane = lane_id();
+        t.passing(tops, bar, [&](int u, int k, uint64_t m) {
+            const int p = n + int(__builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0)));
+            if ((m >> lane & 1) && p < kList) {
+                x[p] = t.v[u][k];
+                at[p] = base + (u * 64 + lane) * T::V + k;
+            }
+            n += __popcll(m);
+        });
+        in_order();
+        if (n > kList) {
+            n = before;
+            in_turn(t, base);
+        } else if (n > 64) {
+            drop();
+        }
+    }
+
+    // The `count` best, of equal ones those of the lowest tokens.
+    __device__ __forceinline__ void drop()
+    {
+        if (n <= count)
+            return;
+        const int lane = lane_id();
+        const bool some[2] = {lane < n, lane + 64 < n};
+        float v[2];
+        int32_t i[2];
+        uint32_t u[2];
+        uint64_t keep[2], equal[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v[h] = x[lane + 64 * h];
+            i[h] = at[lane + 64 * h];
+            u[h] = some[h] ? rising(v[h] + 0.0f) : 0;      // (0 is no number's)
+        }
+        const uint32_t b = nth_of<T::LOW>(u[0], u[1], count);
+        int over = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            keep[h] = __ballot(some[h] && u[h] >> T::LOW >= b >> T::LOW);
+            equal[h] = __ballot(some[h] && u[h] >> T::LOW == b >> T::LOW);
+            over += __popcll(keep[h]);
+        }
+        for (; over > count; --over) {
+            const int32_t a0 = equal[0] >> lane & 1 ? i[0] : -1, a1 = equal[1] >> lane & 1 ? i[1] : -1;
+            const int32_t last = wave_reduce<OpMax>(a0 > a1 ? a0 : a1);
+            const uint64_t out[2] = {__ballot(a0 == last), __ballot(a1 == last)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                equal[h] &= ~out[h];
+                keep[h] &= ~out[h];
+            }
+        }
+        in_order();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (keep[h] >> lane & 1) {
+                const int p = (h ? __popcll(keep[0]) : 0) + __popcll(keep[h] & ((uint64_t(1) << lane) - 1));
+                x[p] = v[h];
+                at[p] = i[h];
+            }
+        n = count;
+        in_order();
+        bar = __builtin_fmaxf(bar, from_ordered(int32_t((b >> 31 ? b : b | ((1u << T::LOW) - 1)) ^ 0x80000000u)));
+    }
+
+    __device__ __forceinline__ void in_turn(const T &t, int32_t base)
+    {
+        Best best(count);
+        const int lane = lane_id();
+        for (int i = 0; i < n; ++i)
+            best.insert(x[i], at[i]);
+        best.bar = __builtin_fmaxf(best.bar, bar);
+        t.select(best, base);
+        in_order();
+        if (lane < count) {
+            x[lane] = best.x;
+            at[lane] = best.at;
+        }
+        n = __popcll(__ballot(lane < count && best.x > kNone));
+        bar = best.bar;
+        in_order();
     }
 };
 
@@ -169,7 +303,8 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
     using S = typename InTraits<In>::S;
     using T = Tile<In>;
     // the waves' bars: of those that go through the same line, the highest holds for all
-    __shared__ float s_bar[kWaves];
+    __shared__ float s_bar[kWaves], s_x[kWaves][kList];
+    __shared__ int32_t s_at[kWaves][kList];
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     if (threadIdx.x < kWaves)
         s_bar[threadIdx.x] = kNone;
@@ -177,13 +312,13 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
     const int64_t item = int64_t(blockIdx.x) * kWaves + wave;
     if (item >= a.items)
         return;
-    const int64_t line = item / a.chunks;
+    const int64_t line = uint32_t(item) / uint32_t(a.chunks);
     const int chunk = int(item - line * a.chunks);
     if (!proposes(a.scores[line], a.ended && a.ended[line]))
         return;                                // (nothing of this line is read by the second launch)
     const S *x = static_cast<const S *>(a.x) + line * a.stride;
     const int64_t from = int64_t(chunk) * a.per_wave, to = from + a.per_wave < a.n ? from + a.per_wave : a.n;
-    Best best(a.count);
+    List<In> best{s_x[wave], s_at[wave], 0, a.count, kNone};
     float m = kNone;
     double s = 0.0;
     typename T::Raw raw;                       // the next tile is on its way while one is gone through
@@ -198,10 +333,11 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
         if (base + 2 * kTile <= to)
             raw.load(x + base + kTile);
         issue_barrier();
-        float top = t.largest(0);
+        float tops[T::U], top = tops[0] = t.largest(0);
 #pragma unroll
         for (int u = 1; u < T::U; ++u)
-            top = OpMax::apply(top, t.largest(u));
+            top = OpMax::apply(top, tops[u] = t.largest(u));
+        top += 0.0f;                           // (-0 is 0, where they are ordered as integers)
         const float now = OpMax::apply(m, top), ref = now > kNone ? now : 0.0f;
         float part = 0.0f;
 #pragma unroll
@@ -215,14 +351,14 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
         for (int w = 0; w < kWaves; ++w)
             if (w >= wave - chunk && w < wave - chunk + a.chunks) {   // (`count` entries reach it: one that does not is out)
                 const float b = __hip_atomic_load(s_bar + w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                best.bar = b > kNone && w != wave ? __builtin_fmaxf(best.bar, below(ordered(b))) : best.bar;
+                best.bar = b > kNone && w != wave ? __builtin_fmaxf(best.bar, below(b)) : best.bar;
             }
         const uint64_t over = __ballot(top > best.bar);
         if (over) {
             // many lanes at once: of their largest entries the count-th best bars the rest
             if (__popcll(over) > a.count)
-                best.bar = __builtin_fmaxf(best.bar, below(nth_largest<sizeof(S) == 2>(ordered(top == top ? top : kNone), a.count)));
-            t.select(best, int32_t(base));
+                best.bar = __builtin_fmaxf(best.bar, below(nth_largest<T::LOW>(top == top ? top : kNone, a.count)));
+            best.take(t, tops, int32_t(base));
             if (lane_id() == 0)
                 __hip_atomic_store(s_bar + wave, best.bar, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
@@ -236,9 +372,10 @@ __global__ __launch_bounds__(kB) void k_beam_lines(BeamArgs a)
         a.tops[item] = all;
         a.sums[item] = sum;
     }
+    best.drop();
     if (lane < a.count) {
-        a.best_x[item * a.count + lane] = best.x;
-        a.best_at[item * a.count + lane] = best.at;
+        a.best_x[item * a.count + lane] = lane < best.n ? best.x[lane] : kNone;
+        a.best_at[item * a.count + lane] = best.at[lane];
     }
 }
 
@@ -412,7 +549,7 @@ __global__ __launch_bounds__(kB) void k_beam_merge(BeamArgs a)
     }
     for (uint32_t i = tid + kMine * kB; i < all; i += kB)
         low = __builtin_fmaxf(low, float(lines.candidate(i).s) + 0.0f);
-    const float bar = from_ordered(nth_largest<false>(ordered(low), a.count));
+    const float bar = nth_largest<0>(low, a.count);
     if (lane == 0)
         s_bar[wave] = bar;
     __syncthreads();
