@@ -82,6 +82,7 @@ constexpr int kPageRows = 8;              // old rows that a wave goes through, 
 constexpr int kPageLdsRows = 4096;        // rows (old and new each) that every block plans for itself in LDS
 constexpr int kPageBlocksPerCu = 8;       // grid cap = CUs * this
 constexpr int kCompactChunk = 4096;       // ids whose flags a block packs
+constexpr int kCompactOwn = 65536;        // ids of a pool whose flags every block packs for itself
 constexpr int kCompactSums = 4096;        // chunks that every block sums up for itself
 constexpr int kCopyCaches = 64;           // caches of a launch
 constexpr int kCopyBlocksPerCu = 16;      // blocks of a launch = CUs * this, or one a pair of a chunk

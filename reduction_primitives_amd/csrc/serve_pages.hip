@@ -23,7 +23,8 @@
 // population count, and the k-th used id beyond their number u and the k-th
 // free one below it are what their own ranks say, so no search is needed.
 // Entries that the row before names at the same position are marked and looked up
-// once.  256 rows of 4 k tokens: 2 + 4 + 3 + 6 + 5 us in five launches, latency;
+// once.  Up to 65536 ids every block packs and ranks for itself: 256 rows of 4 k
+// tokens take 2 + 3 + 8 us in three launches, latency (2 + 3 + 3 + 6 + 5 in five);
 // 4096 rows of 16 k tokens in a pool of 4 times what is used: 4 + 16 + 4 + 12 + 18
 // us, bound by single bytes and words all over the pool (each row by itself, with
 // three loads a rank: 5 + 24 + 7 + 10 + 32 and a launch for the sums).
@@ -654,6 +655,117 @@ __global__ __launch_bounds__(kB) void k_compact_tables(CompactArgs a)
     }
 }
 
+// Small pools, all of it after the marks in one launch: every block packs the flags and
+// ranks the words for itself, and finds the k-th free id by bisection.
+__global__ __launch_bounds__(kB) void k_compact_own(CompactArgs a)
+{
+    constexpr int kWords = tune::kCompactOwn / 64, kMine = kWords / kB;
+    __shared__ __attribute__((aligned(16))) uint64_t s_used[kWords];
+    __shared__ int32_t s_rank[kWords], s_part[kB / 64];
+    const int tid = int(threadIdx.x), lane = lane_id(), words = int(a.chunks) * (tune::kCompactChunk / 64);
+    {
+        constexpr int kAhead = tune::kCompactOwn / 16 / kB;
+        u32x4 f[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = tid + k * kB;
+            f[k] = reinterpret_cast<const u32x4 *>(a.used)[i < words * 4 ? i : 0];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            uint32_t m = 0;                    // four bytes of 0 or 1 to the bits 24 .. 27 of the product
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                m |= (f[k][j] * 0x01020408u >> 24 & 0xf) << (4 * j);
+            const int i = tid + k * kB;
+            reinterpret_cast<uint16_t *>(s_used)[i] = uint16_t(i < words * 4 ? m : 0);
+        }
+    }
+    __syncthreads();
+    int32_t sum = 0, u;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        sum += __popcll(s_used[tid * kMine + k]);
+    int32_t run = block_prefix<kB>(sum, s_part, &u);
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        s_rank[tid * kMine + k] = run;
+        run += __popcll(s_used[tid * kMine + k]);
+    }
+    __syncthreads();
+    const auto rank = [&](int id) { return s_rank[id >> 6] + int(__popcll(s_used[id >> 6] & lanes_before(id & 63))); };
+    const int n = int(a.n_blocks), kept = u < n ? rank(u) : u, moves = u - kept;
+    // the k-th free ids, N at a time
+    const auto places = [&](auto &k) {
+        constexpr int N = sizeof(k) / sizeof(k[0]);
+        int w[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            w[r] = 0;
+#pragma unroll
+        for (int d = kWords / 2; d > 0; d /= 2)
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+                w[r] += (w[r] + d) * 64 - s_rank[w[r] + d] <= k[r] ? d : 0;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            uint64_t m = ~s_used[w[r]];
+            int left = k[r] - (w[r] * 64 - s_rank[w[r]]), at = 0;
+#pragma unroll
+            for (int d = 32; d > 0; d /= 2) {
+                const int c = __popcll(m & ((uint64_t(1) << d) - 1));
+                const bool up = left >= c;
+                left -= up ? c : 0;
+                at += up ? d : 0;
+                m = up ? m >> d : m;
+            }
+            k[r] = w[r] * 64 + at;
+        }
+    };
+    for (int id = int(blockIdx.x) * kB + tid; id < n; id += int(gridDim.x) * kB) {
+        if (id < u)
+            continue;
+        a.ring[id - u] = id;
+        if (s_used[id >> 6] >> (id & 63) & 1) {
+            int k[1] = {rank(id) - kept};
+            const int64_t pair = 2 * int64_t(k[0]);
+            places(k);
+            a.pairs[pair] = id;
+            a.pairs[pair + 1] = k[0];
+        }
+    }
+    for (int64_t k = moves + int64_t(blockIdx.x) * kB + tid; k < a.max_pairs; k += int64_t(gridDim.x) * kB) {
+        a.pairs[2 * k] = -1;
+        a.pairs[2 * k + 1] = -1;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        a.state_out[0] = 0;
+        a.state_out[1] = n - u;
+        a.state_out[2] = moves;
+        a.state_out[3] = 0;
+    }
+    const int64_t tiles = tiles_of(a.rows, a.segs);
+    for (int64_t i = wave_number(); i < tiles; i += wave_count()) {
+        Tile t(i, a.rows, a.segs);
+        const int64_t p = t.row0 + lane;
+        const int held = p < a.rows && lane < kRows ? clamp_held(a.held[p], a.max_blocks) : 0;
+        t.load(a, held, 0);
+        int to[kRows];
+        bool moved[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            asm volatile("" : "+v"(t.id[r]));
+            moved[r] = t.id[r] >= u && t.id[r] < n;
+            to[r] = moved[r] ? rank(t.id[r]) - kept : 0;
+        }
+        places(to);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (t.col < read_lane(held, r))
+                a.table_out[(t.row0 + r) * a.tos + t.col] = moved[r] ? to[r] : t.id[r];
+    }
+}
+
 // ----------------------------------------------------------------------- copy
 
 typedef u32x4 AnyVec __attribute__((aligned(1)));
@@ -752,6 +864,11 @@ int launch_compact(const CompactLaunch &L)
     const dim3 chunks(uint32_t(a.chunks > 0 ? a.chunks : 1));
     launch_timed(k_compact_clear, chunks, block, 0, L.stream, L.ev_begin, L.ev_end, a);
     hipLaunchKernelGGL(k_compact_mark, rows, block, 0, st, a);
+    if (a.n_blocks <= tune::kCompactOwn) {     // (two blocks a CU at most: each reads all flags)
+        const int64_t by_id = (a.n_blocks + 63) / 64, by_tile = (a.rows + kRows - 1) / kRows * a.segs;
+        hipLaunchKernelGGL(k_compact_own, dim3(uint32_t(blocks_for(by_id > by_tile ? by_id : by_tile, L.grid / 4))), block, 0, st, a);
+        return launched() ? ST_OK : ST_HIP;
+    }
     if (a.chunks > 0)
         hipLaunchKernelGGL(k_compact_pack, chunks, block, 0, st, a);
     if (a.chunks > tune::kCompactSums) {

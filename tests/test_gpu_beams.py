@@ -346,7 +346,7 @@ def test_compact(groups, beams, longest, spare, in_place):
     assert again[2][2] == 0 and (again[1] == -1).all()
 
 
-@pytest.mark.parametrize("pool", [1, 2, 63, 64, 65, 4095, 4096, 4097, 70000])
+@pytest.mark.parametrize("pool", [1, 2, 63, 64, 65, 4095, 4096, 4097, 65535, 65536, 65537, 70000])
 @pytest.mark.parametrize("share", [0.0, 0.3, 0.5, 1.0])
 def test_compact_pools(pool, share):
     rk = _rk()
