@@ -416,9 +416,18 @@ struct Place {
     }
 };
 
-// Rows are a stride apart, so a step adds a scalar to an address.
-template <bool BWD>
-__device__ __forceinline__ int64_t way(int64_t r, int64_t ts) { return (BWD ? -r : r) * ts; }
+// A lane's place in a tensor, a row further with each step.  (The stride is opaque:
+// its multiples, held for every row and tensor, are more scalars than there are, and
+// those that do not fit went to and from vector registers, 200 instructions a tile.)
+template <class T, bool BWD>
+struct Rows {
+    using S = typename InTraits<T>::S;
+    S *p;
+    int64_t by;
+    __device__ __forceinline__ Rows(S *first, int64_t ts) : p(first), by(BWD ? -ts : ts) { asm volatile("" : "+s"(by)); }
+    __device__ __forceinline__ void next() { p += by; }
+    __device__ __forceinline__ void next_if(bool more) { p += more ? by : 0; }
+};
 
 // A lane's inputs as they come from memory.
 template <class X, class G, bool BLEND, int V, int R, bool BWD>
@@ -432,17 +441,28 @@ struct Inputs {
     template <bool CLAMP>
     __device__ __forceinline__ void load_rows(const RecurArgs &a, const Place<V, R, BWD> &p)
     {
-        const auto *gate_p = p.template at<G>(a.gate);
-        const auto *x_p = p.template at<X>(a.x), *d_p = p.template at<X>(a.dout), *h_p = p.template at<X>(a.h);
+        Rows<G, BWD> gate_p(p.template at<G>(a.gate), a.gate.ts);
+        Rows<X, BWD> x_p(p.template at<X>(a.x), a.x.ts), d_p(p.template at<X>(a.dout), a.dout.ts), h_p(p.template at<X>(a.h), a.h.ts);
+        if constexpr (BWD)
+            h_p.next_if(!CLAMP || p.row0 > 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t i = CLAMP && r > p.more ? p.more : r;
-            gate[r] = PG::load(gate_p + way<BWD>(i, a.gate.ts));
+            gate[r] = PG::load(gate_p.p);
             if constexpr (HAS_X)
-                x[r] = PX::load(x_p + way<BWD>(i, a.x.ts));
+                x[r] = PX::load(x_p.p);
             if constexpr (BWD) {
-                d[r] = PX::load(d_p + way<BWD>(i, a.dout.ts));
-                h[r] = PX::load(h_p + way<BWD>(CLAMP && i + 1 > p.row0 ? p.row0 : i + 1, a.h.ts));
+                d[r] = PX::load(d_p.p);
+                h[r] = PX::load(h_p.p);
+            }
+            if (r + 1 < R) {
+                const bool more = !CLAMP || r < p.more;
+                gate_p.next_if(more);
+                if constexpr (HAS_X)
+                    x_p.next_if(more);
+                if constexpr (BWD) {
+                    d_p.next_if(more);
+                    h_p.next_if(!CLAMP || (more && r + 2 <= p.row0));
+                }
             }
         }
     }
@@ -455,9 +475,19 @@ struct Inputs {
     }
 };
 
+// The kernel's arguments, read again: held from one end of it to the other they are more
+// scalars than there are, and go to vector registers and back.
+__device__ __forceinline__ const RecurArgs &args_again()
+{
+    using At = const __attribute__((address_space(4))) RecurArgs *;
+    At p = (At)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const RecurArgs *)p;
+}
+
 template <class X, class G, int KIND, bool BLEND, int V, int R, bool BWD>
 __global__ __launch_bounds__(kB, kRecurWaves)
-void k_recur(RecurArgs a)
+void k_recur(RecurArgs given)
 {
     using PX = Pack<X, V>;
     using PG = Pack<G, V>;
@@ -468,8 +498,8 @@ void k_recur(RecurArgs a)
     __shared__ int s_reset[kWaves], s_next, s_back;
     __shared__ float2 s_maps[kAhead][kStrip];
 
-    const int LC = 1 << a.lanes_log2, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const uint32_t cols = uint32_t(a.strips) * uint32_t(a.segs), col = blockIdx.x % cols;
+    const int LC = 1 << given.lanes_log2, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const uint32_t cols = uint32_t(given.strips) * uint32_t(given.segs), col = blockIdx.x % cols;
     const int64_t tile = blockIdx.x / cols;
     constexpr int kWords = (R + 3) / 4;
     Inputs<X, G, BLEND, V, R, BWD> in;
@@ -482,12 +512,13 @@ void k_recur(RecurArgs a)
 
     // The tile's map, and the state that enters it.  (More than one turn only where a tile before it has not been
     // started: this block then computes that one's map, and its own again.)
-    bool force = a.force_help;
+    bool force = given.force_help;
 #pragma unroll 1
     for (int64_t target = tile;;) {
     // (what follows from the thread's number is not kept from turn to turn: there is hardly ever a second)
     int tid = int(threadIdx.x);
     asm volatile("" : "+v"(tid));
+    const RecurArgs &a = args_again();
     const int lane = tid & 63, r0 = (tid >> a.lanes_log2) * R;
     const Place<V, R, BWD> at(a, target, col, tid);
     in.load(a, at);
@@ -616,6 +647,7 @@ void k_recur(RecurArgs a)
     if (!a.linked)
         break;
     if (wave == 0) {
+        const RecurArgs &a = args_again();
         const int c = lane < LC * V ? lane : LC * V - 1;   // a lane a channel of the strip
         float tA = 1.0f, tH = 0.0f, s = 0.0f;
         bool known = target == 0;
@@ -661,6 +693,7 @@ void k_recur(RecurArgs a)
         break;
     target = next;
     }
+    const RecurArgs &a = args_again();
     if (a.linked) {
         const int lane = lane_id(), c = lane < LC * V ? lane : LC * V - 1;
         int back = __builtin_amdgcn_readfirstlane(s_back);
@@ -699,8 +732,8 @@ void k_recur(RecurArgs a)
             s[k] = s_reset[w] ? s_H[w][c] : apply(s_A[w][c], s[k], s_H[w][c]);
         s[k] = before_reset ? H[k] : apply(A[k], s[k], H[k]);
     }
-    auto *const out_p = at.template at<X>(a.out);
-    auto *const dgate_p = at.template at<G>(a.dgate);
+    Rows<X, BWD> out_p(at.template at<X>(a.out), a.out.ts);
+    Rows<G, BWD> dgate_p(at.template at<G>(a.dgate), a.dgate.ts);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool special = !plain && flag(r) != kIn, there = !special || (flag(r) & kIn) != 0;
@@ -734,16 +767,18 @@ void k_recur(RecurArgs a)
                 s[k] = there ? ak * gr : s[k];
             }
             if (there) {
-                PX::store(out_p + way<BWD>(r, a.out.ts), dx, at.drop);
-                PG::store(dgate_p + way<BWD>(r, a.dgate.ts), dg, at.drop);
+                PX::store(out_p.p, dx, at.drop);
+                PG::store(dgate_p.p, dg, at.drop);
             }
+            dgate_p.next();
         } else {
 #pragma unroll
             for (int k = 0; k < V; ++k)
                 s[k] = __builtin_fmaf(ga[r][k], s[k], gb[r][k]);
             if (there)
-                PX::store(out_p + way<BWD>(r, a.out.ts), s, at.drop);
+                PX::store(out_p.p, s, at.drop);
         }
+        out_p.next();
         if (special && (flag(r) & kEnd) && a.state_out)
             Pack<float, V>::store(a.state_out + int64_t(s_seq[r0 + r]) * a.channels + at.c0, s, at.drop);
         issue_barrier();
@@ -780,7 +815,7 @@ int launch_recur(const RecurLaunch &L)
     }
     if (p.linked) {
         const int64_t vectors = p.tiles * p.strips * L.a.segs * kRecurRecBytes / 16;
-        const int64_t blocks = (vectors + kB * 8 - 1) / (kB * 8), most = 2048;
+        const int64_t blocks = (vectors + kB * 2 - 1) / (kB * 2), most = 4096;
         hipLaunchKernelGGL(k_recur_clear, dim3(uint32_t(blocks < most ? blocks : most)), dim3(kB), 0,
                            static_cast<hipStream_t>(L.stream), L.a, vectors);
         if (hipGetLastError() != hipSuccess)
