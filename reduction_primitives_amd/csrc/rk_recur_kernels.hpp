@@ -28,13 +28,14 @@
 //
 // States, products of gates and sums are float32; outputs are rounded once.
 //
-// Measured: 512 x 128 tokens x 2048 bf16, where no tile waits, 166 us forward (805 MB, 4.8
-// TB/s) and 512 x 64 backward 173 us (as many bytes); 16 x 4096 207, 1 x 65536 250
-// (3.2 TB/s), 16 x 2048 backward 202.  What the tiles wait for each other is what
-// is left: four blocks a CU hide a load's latency but not that as well.  (Blocks
-// that go from tile to tile with the next one's inputs loaded ahead took 337 us for
-// 1 x 65536: three blocks a CU then, and loads that come back in order behind the
-// look-back's.)
+// Measured, bf16 unless said: 512 x 128 tokens x 2048, where no tile waits, 167 us forward
+// (805 MB, 4.8 TB/s) and 512 x 64 backward 172 (as many bytes); 16 x 4096 203, 1 x 65536
+// 246 (3.3 TB/s), 8 x 4096 backward 195, 20011 x 1001 float32 backward 137.  What the
+// tiles wait for each other is what is left, and 5 us of clearing the records: four
+// blocks a CU hide a load's latency but not that as well, and a fifth has no registers
+// (40 spilled).  (Blocks that go from tile to tile with the next one's inputs loaded
+// ahead took 337 us for 1 x 65536: three blocks a CU then, and loads that come back in
+// order behind the look-back's.)
 #pragma once
 
 #include "rk_recur.hpp"
