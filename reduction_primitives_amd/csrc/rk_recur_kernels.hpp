@@ -675,6 +675,10 @@ void k_recur(RecurArgs given)
                 s = look_back(a, col, tile, c, force, &next, &back);
                 if (next < 0 && back == 0 && behind && !known)
                     rec.put(0, c, apply(tA, s, tH), kStateKnown);
+            } else {
+                // (outputs may take the inputs' place: a block that computes this tile's map too must not read
+                // them and find no record; a look-back's loads have come back behind the record's store)
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             }
         }
         if (lane < LC * V)
