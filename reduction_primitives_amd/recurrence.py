@@ -51,12 +51,17 @@ def linear_recurrence(gate, x, state=None, kind="value", blend=False, starts=Non
     Where gradients are recorded and gate, x or state requires one, the outputs
     have them (of the first order, computed on the stream that was current;
     sources, out, state_out and stream are then refused, and tokens of no
-    sequence get zeros)."""
+    sequence get zeros).  Not while the stream is captured: a captured backward
+    pass that meets an eager graph of the same leaves ends the process inside
+    torch; linear_recurrence_backward can be captured."""
     code = _kind("linear_recurrence", kind)
     if torch.is_grad_enabled() and (gate.requires_grad or x.requires_grad or (state is not None and state.requires_grad)):
         if sources is not None or out is not None or state_out is not None or stream is not None:
             raise ValueError("linear_recurrence: sources, out, state_out and stream have no gradient: detach the inputs, "
                              "or call under no_grad")
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("linear_recurrence: records no gradients while the stream is captured: call it and "
+                             "linear_recurrence_backward under no_grad")
         return _Recurrence.apply(gate, x, state, kind, blend, starts, workspace)
     handle = _handle("linear_recurrence", "gate", gate, stream)
     if out is None:

@@ -76,7 +76,7 @@ def test_beam_sizes(n, dt, beams, count):
         assert np.array_equal(t, wt) and np.array_equal(p, wp)
 
 
-@pytest.mark.parametrize("req,beams,n,count", [(40, 8, 9001, 16), (300, 4, 700, 8), (1, 16, 140001, 33), (2500, 2, 100, 4), (1, 300, 50, 64)])
+@pytest.mark.parametrize("req,beams,n,count", [(40, 8, 9001, 16), (300, 4, 700, 8), (1, 16, 140001, 33), (2500, 2, 100, 4), (1, 300, 50, 64), (2, 4096, 70, 64)])
 def test_beam_counts(req, beams, n, count):
     g = gen(req)
     x = torch.randn(req * beams, n, generator=g) * 2

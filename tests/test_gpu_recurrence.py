@@ -436,6 +436,33 @@ def test_blocks_help_where_they_would_wait(types):
         assert rk.rk_stream_timeouts(torch.cuda.current_stream().cuda_stream) == 0
 
 
+def test_no_gradients_are_recorded_in_a_capture():
+    """An eager graph of the same leaves is alive; the captured backward call gives what autograd gives."""
+    rk = _rk()
+    g = gen(5)
+    gate, x = gates(g, (3, 200, 64), "sigmoid", F32).to(DEV), torch.randn(3, 200, 64, generator=g).to(DEV)
+    leaves = [gate.clone().requires_grad_(), x.clone().requires_grad_()]
+    eager, _ = rk.linear_recurrence(*leaves, kind="sigmoid", blend=True)
+    n = rk.rk_linear_recurrence_workspace_size(rk.RK_F32, rk.RK_F32, 3, 200, 64, 0)
+    out, last, ws = torch.empty_like(x), torch.empty(3, 64, device=DEV), torch.empty(max(n, 8), dtype=torch.uint8, device=DEV)
+    dg, dx, ds = torch.empty_like(x), torch.empty_like(x), torch.empty(3, 64, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            rk.linear_recurrence(*leaves, kind="sigmoid", blend=True)
+        with torch.no_grad():
+            rk.linear_recurrence(*leaves, kind="sigmoid", blend=True, out=out, state_out=last, workspace=ws)
+            rk.linear_recurrence_backward(*leaves, out, x, kind="sigmoid", blend=True, dgate=dg, dx=dx, dstate=ds, workspace=ws)
+    want = torch.autograd.grad(eager, leaves, x)
+    for _ in range(3):
+        for t in (out, dg, dx):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(dg, want[0]) and torch.equal(dx, want[1])
+
+
 def test_launch_failures_and_small_workspaces():
     rk = _rk()
     x = torch.randn(1, 9000, 64, generator=gen(1)).to(DEV)
