@@ -81,6 +81,7 @@ struct RecurPlan {
     int64_t tiles = 0;
     int tile_rows = 0;
     bool linked = false;
+    bool step = false;        // one token a sequence, forward: a lane a row's four channels, no tiles
     int64_t grid = 0;
     int launches = 0;
     size_t ws_bytes = 0;

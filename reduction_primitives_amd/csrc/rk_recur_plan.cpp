@@ -21,6 +21,22 @@ int plan_recur(int x_dtype, int gate_dtype, int64_t rows, int64_t segs, int64_t 
     if (rows == 0)
         return ST_OK;
     cus = cus > 0 ? cus : tune::kDefaultCus;
+    if (period == 1 && !backward) {
+        const int64_t lanes = (channels + tune::kRecurVec - 1) / tune::kRecurVec;
+        p->step = true;
+        p->vec = tune::kRecurVec;
+        p->per_lane = 1;
+        while ((1 << p->lanes_log2) < lanes && (1 << p->lanes_log2) < tune::kRecurBlock)
+            ++p->lanes_log2;
+        const int64_t strips = ((lanes - 1) >> p->lanes_log2) + 1;
+        p->tile_rows = tune::kRecurBlock >> p->lanes_log2;
+        p->tiles = (rows + p->tile_rows - 1) / p->tile_rows;
+        if (p->tiles * strips > 0xffffff || segs != 1)
+            return ST_UNSUPPORTED;
+        p->strips = int(strips);
+        p->grid = p->tiles * strips;
+        return ST_OK;
+    }
     p->vec = channels < tune::kRecurVec ? 1 : tune::kRecurVec;
     while ((p->vec << p->lanes_log2) < channels && (p->vec << p->lanes_log2) < tune::kRecurStrip)
         ++p->lanes_log2;

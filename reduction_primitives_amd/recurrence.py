@@ -8,10 +8,12 @@ Buffers that are not given are allocated with torch on the call's stream.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _native as N
-from .serving import _calls, _code, _empty, _handle, _workspace
+from .serving import _calls, _code, _empty, _handle
 
 KINDS = {"value": N.RK_GATE_VALUE, "log": N.RK_GATE_LOG, "sigmoid": N.RK_GATE_SIGMOID}
 
@@ -26,10 +28,19 @@ def _scratch(name, gate, x, starts, stream):
     """A workspace for tokens like x's (None where none is needed, or where the call refuses them)."""
     if x.dim() != (3 if starts is None else 2):
         return None
+    if starts is None and x.shape[1] <= 1:     # (none is needed: the size would take as long as the call)
+        return None
     n_seq = x.shape[0] if starts is None else max(starts.numel() - 1, 0)
-    return _workspace(N.rk_linear_recurrence_workspace_size,
-                      (_code(name, "x", x.dtype), _code(name, "gate", gate.dtype), n_seq, x.shape[-2], x.shape[-1],
-                       int(starts is not None)), x, stream)
+    n = _size(x.get_device(), _code(name, "x", x.dtype), _code(name, "gate", gate.dtype), n_seq, x.shape[-2], x.shape[-1],
+              int(starts is not None))
+    return _empty(n, torch.uint8, x, stream) if n else None
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(device, *args):
+    """rk_linear_recurrence_workspace_size on a device (through ctypes it takes longer than a short sequence's call)."""
+    with torch.cuda.device(device):
+        return N.rk_linear_recurrence_workspace_size(*args)
 
 
 def _sequences(gate, starts):
