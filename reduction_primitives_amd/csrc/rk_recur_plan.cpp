@@ -21,21 +21,24 @@ int plan_recur(int x_dtype, int gate_dtype, int64_t rows, int64_t segs, int64_t 
     if (rows == 0)
         return ST_OK;
     cus = cus > 0 ? cus : tune::kDefaultCus;
-    if (period == 1 && !backward) {
+    if (period == 1 && !backward && segs == 1) {
         const int64_t lanes = (channels + tune::kRecurVec - 1) / tune::kRecurVec;
-        p->step = true;
-        p->vec = tune::kRecurVec;
-        p->per_lane = 1;
-        while ((1 << p->lanes_log2) < lanes && (1 << p->lanes_log2) < tune::kRecurBlock)
-            ++p->lanes_log2;
-        const int64_t strips = ((lanes - 1) >> p->lanes_log2) + 1;
-        p->tile_rows = tune::kRecurBlock >> p->lanes_log2;
-        p->tiles = (rows + p->tile_rows - 1) / p->tile_rows;
-        if (p->tiles * strips > 0xffffff || segs != 1)
-            return ST_UNSUPPORTED;
-        p->strips = int(strips);
-        p->grid = p->tiles * strips;
-        return ST_OK;
+        int log2 = 0;
+        while ((1 << log2) < lanes && (1 << log2) < tune::kRecurBlock)
+            ++log2;
+        const int64_t strips = ((lanes - 1) >> log2) + 1, rows_a_block = tune::kRecurBlock >> log2,
+                      blocks = (rows + rows_a_block - 1) / rows_a_block;
+        if (blocks <= 0xffffff / strips) {    // (more rows go through tiles of several)
+            p->step = true;
+            p->vec = tune::kRecurVec;
+            p->per_lane = 1;
+            p->lanes_log2 = log2;
+            p->strips = int(strips);
+            p->tile_rows = int(rows_a_block);
+            p->tiles = blocks;
+            p->grid = blocks * strips;
+            return ST_OK;
+        }
     }
     p->vec = channels < tune::kRecurVec ? 1 : tune::kRecurVec;
     while ((p->vec << p->lanes_log2) < channels && (p->vec << p->lanes_log2) < tune::kRecurStrip)

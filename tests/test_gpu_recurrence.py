@@ -518,3 +518,37 @@ def test_tokens_past_2_31_elements():
     # The tiles lie otherwise, so each side has a rounding of its own: half a step of bfloat16 (2^-8 of it), and in
     # float32, with a = 1/2, at most 2 * 16 * 2^-24 of sum |x| / 2^k <= 2 max |x| < 12.
     assert ((a - b).abs() <= 2 * 2.0 ** -8 * (b.abs() + (a - b).abs()) + 2 * 32 * 2.0 ** -24 * 12).all()
+
+
+@pytest.mark.parametrize("channels", [1, 3, 4, 5, 1023, 1024, 1025, 2050])
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F16, F32)])
+def test_single_tokens(channels, types):
+    """In place of the inputs, whose last channels no whole vector holds, and beside them; every kind."""
+    rk = _rk()
+    g = gen(channels)
+    for kind, blend in (("sigmoid", True), ("log", False), ("log", True), ("value", False)):
+        gate, x = gates(g, (37, 1, channels), kind, types[1]), torch.randn(37, 1, channels, generator=g).to(types[0])
+        state = torch.randn(37, channels, generator=g)
+        check(gate, x, kind, blend, state=state, backward=False)
+        want, want_last, err, err_last = ref.forward(np64(gate), np64(x), kind, blend, state=np64(state))
+        there, s = x.to(DEV), state.to(DEV)
+        out, last = rk.linear_recurrence(gate.to(DEV), there, state=s, kind=kind, blend=blend, out=there, state_out=s)
+        assert out is there and last is s
+        near(out, want, err)
+        near(last, want_last, err_last)
+
+
+def test_more_single_tokens_than_a_launch_has_blocks():
+    """17 million rows of 1024 channels go through tiles; float16 of one bit, so that a row of each is enough to look at."""
+    rk = _rk()
+    rows, channels = 0xffffff + 9, 1024
+    x = torch.ones(1, 1, channels, dtype=F16, device=DEV).expand(rows, 1, channels)
+    gate = torch.full((1, 1, channels), 0.5, dtype=F16, device=DEV).expand(rows, 1, channels)
+    out = torch.empty(rows, 1, channels, dtype=F16, device=DEV)
+    last = torch.empty(rows, channels, device=DEV)
+    sources = torch.arange(rows, dtype=torch.int32, device=DEV) % 2
+    rk.linear_recurrence(gate, x, state=torch.tensor([[2.0], [4.0]], device=DEV).expand(2, channels).contiguous(), sources=sources, out=out,
+                         state_out=last)
+    for at in (0, 1, 2, 0xfffffe, 0xffffff, 0x1000000, rows - 1):
+        assert (out[at] == 2 + at % 2).all() and (last[at] == 2 + at % 2).all()
+    assert int((out[:, 0, 5] == 2).sum()) == (rows + 1) // 2 and int((last[:, 1023] == 3).sum()) == rows // 2
