@@ -259,13 +259,15 @@ struct RecordBatch {
             A[k] = r.get(2 * k + 1, c);
         }
     }
-    // whether every lane has all words of the i first records
-    __device__ __forceinline__ bool there(int i) const
+    // whether every lane has all words of the records `from` to i - 1, and of number `state` the state (a tile's words
+    // of different channels lie in different lines, and the state of one may be seen while another's is on its way)
+    __device__ __forceinline__ bool there(int i, int from = 0, int state = -1) const
     {
         bool t = true;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            t = t && (k >= i || tag_of(H[k]) == kStateKnown || (tag_of(H[k]) == kMapKnown && tag_of(A[k]) == kMapKnown));
+            t = t && (k >= i || k < from || tag_of(H[k]) == kStateKnown ||
+                      (k != state && tag_of(H[k]) == kMapKnown && tag_of(A[k]) == kMapKnown));
         return __ballot(!t) == 0;
     }
     // the state behind them (where a tile's state has taken its addend's place, the same state)
@@ -313,7 +315,7 @@ __device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int6
                 *back = i;
                 return 0.0f;
             }
-            if (b.there(near))
+            if (b.there(near, near - int(i), near - int(i)))
                 return b.go_on(0.0f, near);    // (what comes before the known state falls to it)
         } else if (!nothing) {
             first -= 64;                       // maps only: the tiles before them
@@ -325,11 +327,12 @@ __device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int6
 }
 
 // The maps of `count` <= kAhead records from tile `from` on, a few from every
-// wave, to LDS: addend and factor, the factor kTaken for a state.
+// wave, to LDS: addend and factor, the factor kTaken for a state.  first: the first
+// one's state.
 constexpr int kAhead = 2 * kRecurBatch * kWaves;
 constexpr uint32_t kTaken = 0x7fc0dead;        // (a NaN that a product of gates is not without its addend being one)
 
-__device__ __forceinline__ void gather_maps(const RecurArgs &a, int64_t col, int64_t from, int count, int wave, int c,
+__device__ __forceinline__ void gather_maps(const RecurArgs &a, int64_t col, int64_t from, int count, bool first, int wave, int c,
                                             float2 (*maps)[kStrip])
 {
     constexpr int N = RecordBatch::N;
@@ -337,7 +340,7 @@ __device__ __forceinline__ void gather_maps(const RecurArgs &a, int64_t col, int
     for (int i = wave * N; i < count; i += kWaves * N) {
         const int n = count - i < N ? count - i : N;
         RecordBatch b;
-        while (b.load(RecurRecord(a, col, from + i), c), !b.there(n))
+        while (b.load(RecurRecord(a, col, from + i), c), !b.there(n, 0, first && i == 0 ? 0 : -1))
             __builtin_amdgcn_s_sleep(1);       // (words of channels beside the first are on their way)
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -704,9 +707,10 @@ void k_recur(RecurArgs given)
         int back = __builtin_amdgcn_readfirstlane(s_back);
         if (back > 0) {
             float s = 0.0f;
-            for (; back > 0; back -= kAhead) {
+            bool first = true;
+            for (; back > 0; back -= kAhead, first = false) {
                 const int count = back < kAhead ? back : kAhead;
-                gather_maps(a, col, tile - back, count, wave, c, s_maps);
+                gather_maps(a, col, tile - back, count, first, wave, c, s_maps);
                 __syncthreads();
                 if (wave == 0)
                     for (int i = 0; i < count; ++i) {
