@@ -579,7 +579,7 @@ void k_recur(RecurArgs given)
         if (!plain && flag(r) != kIn) {
             if (flag(r) & kReset) {
                 reset = true;
-                    float start[V];
+                float start[V];
                 if constexpr (BWD)
                     last_gradient(a, s_seq[r0 + r], at.c0, start);
                 else
