@@ -574,7 +574,9 @@ size_t rk_linear_recurrence_workspace_size(int x_dtype, int gate_dtype, int64_t 
  *   out         may be x or gate itself, or other columns of the same rows; no
  *               other overlap
  *   state_out   n_seq lines of channels float32: the last state, or the first one
- *               of a sequence without tokens.  May be state, without sources.
+ *               of a sequence without tokens.  May be state, without sources
+ *               (first states that are still to be read are then kept in the
+ *               workspace).
  * States, gates and their products are float32 and h is rounded once.  Nothing
  * passes from one sequence to another.  (Runs of up to 2048 tokens are folded
  * into one factor: a product of that many gates that leaves float32's range

@@ -96,6 +96,8 @@ struct RecurLaunch {
     RecurArgs a;
     int gate_dtype;
     bool backward;
+    const float *state;       // first states that are copied to `kept` before the tiles are begun, or NULL
+    float *kept;
     void *stream, *ev_begin, *ev_end;
 };
 int launch_recur_f32(const RecurLaunch &L);

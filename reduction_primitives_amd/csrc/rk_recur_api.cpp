@@ -11,6 +11,10 @@
 #include "rk_host.hpp"
 #include "rk_recur.hpp"
 
+namespace rk {
+size_t round_up_256(size_t b);
+}
+
 using namespace rk;
 using namespace rk::checks;
 
@@ -97,6 +101,13 @@ struct Request {
     void *stream;
 };
 
+bool states_fit(int64_t n, int64_t channels) { return channels == 0 || n <= (int64_t(1) << 44) / channels; }
+
+// Room for the first states, behind the records.  Where the last ones take their
+// place and states pass from tile to tile, the tiles read a copy: one that is
+// computed late, or once more by a block that helps, would find a last state there.
+size_t kept_states(int64_t n_seq, int64_t channels) { return round_up_256(size_t(n_seq) * size_t(channels) * 4); }
+
 size_t workspace_size(int x_dtype, int gate_dtype, int64_t n_seq, int64_t tokens, int64_t channels, bool packed)
 {
     if (n_seq < 0 || tokens < 0 || n_seq > 0x7fffffff || tokens > 0x7fffffff)
@@ -113,7 +124,7 @@ size_t workspace_size(int x_dtype, int gate_dtype, int64_t n_seq, int64_t tokens
             p.ws_bytes > most)
             most = p.ws_bytes;
     }
-    return most;
+    return most && states_fit(n_seq, channels) ? most + kept_states(n_seq, channels) : 0;
 }
 
 int recur(const char *name, const Request &q, bool backward)
@@ -140,7 +151,7 @@ int recur(const char *name, const Request &q, bool backward)
     if (q.n_seq == 0 || q.channels == 0)
         return RK_OK;
     const int64_t states = q.sources ? q.n_states : q.n_seq;
-    if (states > (int64_t(1) << 44) / q.channels || q.n_seq > (int64_t(1) << 44) / q.channels)
+    if (!states_fit(states, q.channels) || !states_fit(q.n_seq, q.channels))
         return RK_ERR_INVALID_ARGUMENT;
     for (const auto &t : in)
         if (t.t && !e.empty() && (!t.t->data || !aligned(t.t->data, t.size)))
@@ -163,15 +174,16 @@ int recur(const char *name, const Request &q, bool backward)
                               q.starts ? 0 : e.tokens, q.channels, backward, host::device_cus(), &p);
     if (rc)
         return rc;
-    if (p.ws_bytes > 0 && (!q.workspace || !aligned(q.workspace, 8) || q.workspace_bytes < p.ws_bytes))
+    const bool in_place = !backward && !q.sources && q.state == q.state_out, keep = in_place && q.state && p.linked;
+    const size_t ws = p.ws_bytes + (keep ? kept_states(q.n_seq, q.channels) : 0);
+    if (ws > 0 && (!q.workspace || !aligned(q.workspace, 8) || q.workspace_bytes < ws))
         return RK_ERR_INVALID_ARGUMENT;
 
     // what is written: the rows may take the place of an input's or stand beside them; the forward pass's
     // last states may be its first ones
-    const Span sw = span(q.workspace, int64_t(p.ws_bytes)), so = span(q.state_out, q.n_seq * q.channels * 4),
+    const Span sw = span(q.workspace, int64_t(ws)), so = span(q.state_out, q.n_seq * q.channels * 4),
                ss = span(q.state, states * q.channels * 4), sd = span(q.dlast, q.n_seq * q.channels * 4),
                sc = span(q.sources, q.n_seq * 4), st = span(q.starts, (q.n_seq + 1) * 4);
-    const bool in_place = !backward && !q.sources && q.state == q.state_out;
     if ((overlap(so, ss) && !in_place) || overlap(so, sd) || overlap(so, sc) || overlap(so, st) || overlap(so, sw))
         return RK_ERR_INVALID_ARGUMENT;
     for (const Span &s : {ss, sd, sc, st})
@@ -198,7 +210,7 @@ int recur(const char *name, const Request &q, bool backward)
     if (host::debug_enabled())
         std::fprintf(stderr, "%s: sequences=%lld tokens=%lld channels=%lld tiles=%lld strips=%d tokens a lane=%d ws=%zu\n", name,
                      (long long)q.n_seq, (long long)q.tokens, (long long)q.channels, (long long)p.tiles, p.strips, p.per_lane,
-                     p.ws_bytes);
+                     ws);
     RecurLaunch L;
     std::memset(static_cast<void *>(&L), 0, sizeof L);
     L.plan = p;
@@ -209,6 +221,11 @@ int recur(const char *name, const Request &q, bool backward)
     L.a.out = flat(q.out, e);
     L.a.dgate = flat(q.dgate, e);
     L.a.state = q.state;
+    if (keep) {
+        L.state = q.state;
+        L.kept = reinterpret_cast<float *>(static_cast<char *>(q.workspace) + p.ws_bytes);
+        L.a.state = L.kept;
+    }
     L.a.dlast = q.dlast;
     L.a.state_out = q.state_out;
     L.a.sources = q.sources;

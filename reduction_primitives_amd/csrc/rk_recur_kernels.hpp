@@ -380,11 +380,13 @@ __global__ __launch_bounds__(kB) void k_recur_empty(RecurArgs a)
     empty_sequences<BWD>(a);
 }
 
-// Zero the records.
-__global__ __launch_bounds__(kB) void k_recur_clear(RecurArgs a, int64_t vectors)
+// Zero the records, and copy n first states to where the tiles read them.
+__global__ __launch_bounds__(kB) void k_recur_clear(RecurArgs a, int64_t vectors, const float *state, float *kept, int64_t n)
 {
     for (int64_t i = int64_t(blockIdx.x) * kB + threadIdx.x; i < vectors; i += int64_t(gridDim.x) * kB)
         reinterpret_cast<u32x4 *>(a.ws)[i] = u32x4{0, 0, 0, 0};
+    for (int64_t i = int64_t(blockIdx.x) * kB + threadIdx.x; i < n; i += int64_t(gridDim.x) * kB)
+        kept[i] = state[i];
 }
 
 // Where a lane stands in a tile.
@@ -553,8 +555,9 @@ void k_recur(RecurArgs given)
     plain = __ballot(!inside) == 0;
 
     // The lane's map, from state 0.  A forward lane keeps, for each step, what the state is multiplied with and
-    // what is added; a sequence's first state goes into its first step's (and need not be read again, when the
-    // last one may have taken its place).  A backward lane keeps its inputs as they came and computes the gates
+    // what is added; a sequence's first state goes into its first step's.  (Tiles that pass states on may be computed
+    // late, or again: where the last states take the first ones' place they read a copy, made before any of them
+    // was begun; other tiles' sequences are all their own, and read before the block's barriers.)  A backward lane keeps its inputs as they came and computes the gates
     // twice: four inputs a step, of 16 bits, take fewer registers than what they come to.
     bool reset = false;
 #pragma unroll
@@ -886,9 +889,10 @@ int launch_recur(const RecurLaunch &L)
             return launch_step<X, G>(L);
     if (p.linked) {
         const int64_t vectors = p.tiles * p.strips * L.a.segs * kRecurRecBytes / 16;
-        const int64_t blocks = (vectors + kB * 2 - 1) / (kB * 2), most = 4096;
+        const int64_t states = L.kept ? L.a.n_seq * L.a.channels : 0, items = vectors > states ? vectors : states;
+        const int64_t blocks = (items + kB * 2 - 1) / (kB * 2), most = 4096;
         hipLaunchKernelGGL(k_recur_clear, dim3(uint32_t(blocks < most ? blocks : most)), dim3(kB), 0,
-                           static_cast<hipStream_t>(L.stream), L.a, vectors);
+                           static_cast<hipStream_t>(L.stream), L.a, vectors, L.state, L.kept, states);
         if (hipGetLastError() != hipSuccess)
             return ST_HIP;
     }

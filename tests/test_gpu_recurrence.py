@@ -436,6 +436,40 @@ def test_blocks_help_where_they_would_wait(types):
         assert rk.rk_stream_timeouts(torch.cuda.current_stream().cuda_stream) == 0
 
 
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("channels", [6, 64, 130])
+@pytest.mark.parametrize("cuts", [None, [0, 5, 3000, 3001, 8999, 9000], [0, 200, 200, 520, 4000, 4000, 4001, 9000], [100, 700, 8500],
+                                  list(range(0, 9001, 300))])
+def test_blocks_help_in_place(types, channels, cuts):
+    """The same with the last states in the first ones' place, and what is written in an input's place: a tile's inputs
+    and first states are read again, by its own block and by another one, and are what they were."""
+    rk = _rk()
+    g = gen(channels)
+    shape, n = ((2, 4500, channels), 2) if cuts is None else ((9000, channels), len(cuts) - 1)
+    starts = None if cuts is None else torch.tensor(cuts, dtype=torch.int32, device=DEV)
+    gate, x = gates(g, shape, "sigmoid", types[1]).to(DEV), torch.randn(shape, generator=g).to(types[0]).to(DEV)
+    dout, state = torch.randn(shape, generator=g).to(types[0]).to(DEV), torch.randn(n, channels, generator=g).to(DEV)
+    how = dict(kind="sigmoid", blend=True, starts=starts)
+    want, want_last = rk.linear_recurrence(gate, x, state=state, out=x.clone(), **how)
+    wants = rk.linear_recurrence_backward(gate, x, want, dout, state=state, dstate_out=state, dgate=gate.clone(), dx=dout.clone(), **how)
+    for force in (-1, 0, 0, 0):
+        rk.rk_debug_force_wait_timeout(force)
+        try:
+            s, s2, o, other = state.clone(), state.clone(), x.clone(), gate.clone()
+            out, last = rk.linear_recurrence(gate, o, state=s, out=o, state_out=s, **how)
+            assert out is o and last is s
+            rk.linear_recurrence(other, x, state=s2, out=other, state_out=s2, **how)
+            dg, dx = gate.clone(), dout.clone()
+            got = rk.linear_recurrence_backward(dg, x, want, dx, state=state, dstate_out=state, dgate=dg, dx=dx, **how)
+            torch.cuda.synchronize()
+        finally:
+            rk.rk_debug_force_wait_timeout(-1)
+        assert torch.equal(s, want_last) and torch.equal(s2, want_last)
+        rows = slice(None) if cuts is None else slice(cuts[0], cuts[-1])
+        for a, b in ((out, want), (other, want), *zip(got, wants)):
+            assert torch.equal(a[rows] if a.shape == x.shape else a, b[rows] if b.shape == x.shape else b)
+
+
 def test_no_gradients_are_recorded_in_a_capture():
     """An eager graph of the same leaves is alive; the captured backward call gives what autograd gives."""
     rk = _rk()

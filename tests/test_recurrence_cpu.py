@@ -97,6 +97,19 @@ def test_workspace_sizes():
     assert size(0, 0, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 0) == 0
 
 
+def test_first_states_are_kept_where_the_last_ones_take_their_place():
+    """A tile may be computed late, or once more by a block that helps, and reads its sequences' first states again then:
+    the workspace has room for them beside the records, and a call that needs it asks for it."""
+    size = _rk().rk_linear_recurrence_workspace_size
+    records = (3 * 157 + 3) * 1024                # 157 tiles of 128 tokens of each sequence
+    assert size(1, 1, 3, 20000, 50, 0) >= records + 3 * 50 * 4
+    assert size(1, 1, 1000, 20000, 50, 1) >= (157 + 3) * 1024 + 1000 * 50 * 4
+    inside = dict(last=BASE["state"], ws_bytes=records)
+    assert forward(**{**long(), **inside}) == 1
+    assert forward(**{**long(), **inside, "ws_bytes": records + 3 * 50 * 4 - 1}) == 1
+    assert size(0, 0, 1 << 30, 20000, 1 << 20, 1) == 0       # (more states than a call takes)
+
+
 def test_calls_of_nothing():
     assert forward(n_seq=0) == 0 and forward(ch=0) == 0 and backward(n_seq=0) == 0
     assert backward(tokens=0, dstate=None) == 0
