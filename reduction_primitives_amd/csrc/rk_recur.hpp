@@ -23,6 +23,12 @@ constexpr int64_t kRecurApart = 512, kRecurApartMost = 4096;
 // Polls of a look-back (a microsecond each) before its block does the work of one
 // that has not been started.
 constexpr uint32_t kRecurPatience = 4096;
+// And of a block that has done so: where blocks have been held back there may be
+// hundreds of such tiles in a column, one behind the other, and 4096 polls each
+// seconds in all.  (A block that is under way ends after some 15 us: 16384 of them
+// take 247, 1024 at a time.)
+constexpr uint32_t kRecurPatienceAgain = 64;
+static_assert(kRecurPatienceAgain <= kRecurPatience, "polls begin at the difference");
 }  // namespace tune
 
 // Most tokens of a lane: what leaves the registers for kRecurWaves waves.  The bytes

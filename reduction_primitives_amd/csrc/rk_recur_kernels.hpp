@@ -289,16 +289,18 @@ struct RecordBatch {
 // tiles between have started.  They start in the order of their numbers as far as
 // the device goes by these, which nothing depends on: where a map is missing after
 // a.patience polls, *missing is its tile, whose map the waiting block computes
-// itself (else -1).  force: ask for that in any case (a test's).  *back: 0, or how
-// far the state is where that is more than a batch, which is the whole block's to
-// gather.
-__device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int64_t tile, int c, bool force,
+// itself (else -1); one that has done so before (helped) waits for the next one no
+// longer than a tile under way takes.  a.force_help: every block asks for it once (a
+// test's).  *back: 0, or how far the state is where that is more than a batch, which
+// is the whole block's to gather.
+__device__ __forceinline__ float look_back(const RecurArgs &a, int64_t col, int64_t tile, int c, bool helped,
                                            int64_t *missing, int64_t *back)
 {
     constexpr int N = RecordBatch::N;
     const int near = tile < N ? int(tile) : N;
     RecordBatch b;
-    uint32_t polls = 0;
+    const bool force = a.force_help && !helped;
+    uint32_t polls = helped ? a.patience - tune::kRecurPatienceAgain : 0;
     *missing = -1;
     *back = 0;
     for (int64_t first = tile - 1;;) {         // 64 tiles from `first` down: what channel 0 knows of them
@@ -519,7 +521,7 @@ void k_recur(RecurArgs given)
 
     // The tile's map, and the state that enters it.  (More than one turn only where a tile before it has not been
     // started: this block then computes that one's map, and its own again.)
-    bool force = given.force_help;
+    bool helped = false;
 #pragma unroll 1
     for (int64_t target = tile;;) {
     // (what follows from the thread's number is not kept from turn to turn: there is hardly ever a second)
@@ -679,7 +681,7 @@ void k_recur(RecurArgs given)
                     rec.put(1, c, tA, kMapKnown);
             }
             if (tile > 0 && !(s_flag[0] & kReset)) {
-                s = look_back(a, col, tile, c, force, &next, &back);
+                s = look_back(a, col, tile, c, helped, &next, &back);
                 if (next < 0 && back == 0 && behind && !known)
                     rec.put(0, c, apply(tA, s, tH), kStateKnown);
             } else {
@@ -698,7 +700,7 @@ void k_recur(RecurArgs given)
         tile_H = tH;
         tile_known = known;
     }
-    force = false;
+    helped = true;
     __syncthreads();
     const int next = __builtin_amdgcn_readfirstlane(s_next);
     if (next < 0)
