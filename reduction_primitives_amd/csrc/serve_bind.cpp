@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -185,10 +186,21 @@ void *handle(PyObject *o)
 
 PyObject *status(int rc) { return PyLong_FromLong(rc); }
 
+// No call has a forward derivative: what carries a tangent is refused rather than
+// left without.  (no_grad does not turn these off, an autograd function's forward
+// does.)
+void no_tangent(const char *name, const char *what, PyObject *o)
+{
+    if (THPVariable_Check(o) && c10::AutogradState::get_tls_state().get_fw_grad_mode() &&
+        THPVariable_Unpack(o)._fw_grad(0).defined())
+        refuse("%s: %s carries a tangent and the call has no forward derivative: unpack it", name, what);
+}
+
 // Calls without a backward pass: where gradients are recorded, what requires
 // them is refused rather than left without.
 void no_gradient(const char *name, const char *what, PyObject *o)
 {
+    no_tangent(name, what, o);
     if (THPVariable_Check(o) && c10::GradMode::is_enabled() && THPVariable_Unpack(o).requires_grad())
         refuse("%s: %s requires grad and the call has no gradient: detach it, or call under no_grad", name, what);
 }
@@ -349,6 +361,9 @@ struct Recurrence {
 // linear_recurrence(stream, gate, x, state, kind, blend, starts, sources, out, state_out, workspace)
 PyObject *linear_recurrence(PyObject *const *a)
 {
+    no_tangent("linear_recurrence", "gate", a[1]);
+    no_tangent("linear_recurrence", "x", a[2]);
+    no_tangent("linear_recurrence", "state", a[3]);
     Call c("linear_recurrence", "gate", a[1]);
     const Recurrence r(c, a[1], a[2], a[4], a[5], a[6]);
     const Tokens out = tokens_of(c, "out", a[8], r.gate.t, r.x_dtype, r.packed);
@@ -368,6 +383,9 @@ PyObject *linear_recurrence(PyObject *const *a)
 // linear_recurrence_backward(stream, gate, x, out, dout, state, dstate_out, kind, blend, starts, dgate, dx, dstate, workspace)
 PyObject *linear_recurrence_backward(PyObject *const *a)
 {
+    static constexpr const char *inputs[] = {"gate", "x", "out", "dout", "state", "dstate_out"};
+    for (int i = 0; i < 6; ++i)
+        no_tangent("linear_recurrence_backward", inputs[i], a[i + 1]);
     Call c("linear_recurrence_backward", "gate", a[1]);
     const Recurrence r(c, a[1], a[2], a[7], a[8], a[9]);
     const Tokens out = tokens_of(c, "out", a[3], r.gate.t, r.x_dtype, r.packed),
@@ -485,6 +503,7 @@ PyObject *copy_blocks(PyObject *const *a)
     std::vector<rk_block_cache> caches;
     caches.reserve(size_t(count));
     for (Py_ssize_t i = 0; i < count; ++i) {
+        no_tangent("copy_blocks", "caches", PySequence_Fast_GET_ITEM(a[1], i));
         const at::Tensor &t = c.here("caches", PySequence_Fast_GET_ITEM(a[1], i));
         if (t.dim() < 1)
             refuse("%s: %s takes tensors of blocks", c.name, "caches");

@@ -62,7 +62,8 @@ def linear_recurrence(gate, x, state=None, kind="value", blend=False, starts=Non
     Where gradients are recorded and gate, x or state requires one, the outputs
     have them (of the first order, computed on the stream that was current;
     sources, out, state_out and stream are then refused, and tokens of no
-    sequence get zeros).  Not while the stream is captured: a captured backward
+    sequence get zeros).  There are no forward derivatives: tensors that carry
+    a tangent are refused.  Not while the stream is captured: a captured backward
     pass that meets an eager graph of the same leaves ends the process inside
     torch; linear_recurrence_backward can be captured."""
     code = _kind("linear_recurrence", kind)

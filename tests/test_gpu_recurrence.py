@@ -363,6 +363,27 @@ def test_autograd_of_parts():
         torch.autograd.grad(first.sum(), both)
 
 
+def test_tangents_are_refused():
+    """Forward derivatives: refused, with and without gradients recorded, and where copy_blocks would leave them behind."""
+    from torch.autograd import forward_ad
+    rk = _rk()
+    x, state = torch.rand(2, 30, 8, generator=gen(2)).to(DEV), torch.zeros(2, 8, device=DEV)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for call in (lambda: rk.linear_recurrence(dual, x), lambda: rk.linear_recurrence(x, dual),
+                     lambda: rk.linear_recurrence(x, x, state=forward_ad.make_dual(state, state.clone())),
+                     lambda: rk.linear_recurrence_backward(x, x, x, dual),
+                     lambda: rk.copy_blocks([x, dual], torch.tensor([[0, 1]], dtype=torch.int32, device=DEV))):
+            with pytest.raises(ValueError, match="carries a tangent"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="carries a tangent"):
+                call()
+        with pytest.raises(RuntimeError):                        # torch's own word, of an autograd function
+            rk.linear_recurrence(dual, x.clone().requires_grad_())
+        out, _ = rk.linear_recurrence(forward_ad.unpack_dual(dual).primal, x)
+    assert torch.equal(out, rk.linear_recurrence(x, x)[0])
+
+
 def test_same_bits_every_time():
     rk = _rk()
     g = gen(1)

@@ -129,6 +129,32 @@ def test_tensor_refusals():
         rk.linear_recurrence(x.requires_grad_(), x, out=x)
 
 
+def test_tangents_are_not_dropped():
+    """No call has a forward derivative: its module says so before it looks at devices, under no_grad, too."""
+    from torch.autograd import forward_ad
+    rk = _rk()
+    calls = rk.linear_recurrence.__globals__["_calls"]
+    x, s = torch.zeros(2, 3, 4), torch.zeros(2, 4)
+    with forward_ad.dual_level():
+        def each(names, run):
+            """run(arguments, one of them with a tangent at a time)"""
+            base = {n: torch.zeros_like(s) if n in ("state", "dstate_out", "logits", "scores") else torch.zeros_like(x) for n in names}
+            for n in names:
+                dual = forward_ad.make_dual(base[n], torch.ones_like(base[n]))
+                for grad in (True, False):
+                    with torch.set_grad_enabled(grad), pytest.raises(ValueError, match=n + " carries a tangent"):
+                        run({**base, n: dual})
+            with pytest.raises(ValueError, match="not on a GPU"):       # (refused for that alone)
+                run(base)
+
+        each(["gate", "x", "state"], lambda a: calls.linear_recurrence(0, a["gate"], a["x"], a["state"], 0, 0, None, None, x, s, None))
+        each(["gate", "x", "out", "dout", "state", "dstate_out"],
+             lambda a: calls.linear_recurrence_backward(0, a["gate"], a["x"], a["out"], a["dout"], a["state"], a["dstate_out"], 0, 0, None,
+                                                        x, x, s, None))
+        each(["logits", "scores"], lambda a: calls.beam_select(0, a["logits"], a["scores"], 1, None, 0, s, s, s, None))
+        each(["x"], lambda a: calls.softmax(0, a["x"], None, x, None))
+
+
 @pytest.mark.parametrize("kind", ["value", "log", "sigmoid"])
 @pytest.mark.parametrize("blend", [False, True])
 def test_plain_gradient_is_the_slope(kind, blend):
