@@ -361,9 +361,12 @@ struct Recurrence {
 // linear_recurrence(stream, gate, x, state, kind, blend, starts, sources, out, state_out, workspace)
 PyObject *linear_recurrence(PyObject *const *a)
 {
-    no_tangent("linear_recurrence", "gate", a[1]);
-    no_tangent("linear_recurrence", "x", a[2]);
-    no_tangent("linear_recurrence", "state", a[3]);
+    // (gradients of the inputs are recorded around the call)
+    no_gradient("linear_recurrence", "gate", a[1]);
+    no_gradient("linear_recurrence", "x", a[2]);
+    no_gradient("linear_recurrence", "state", a[3]);
+    no_gradient("linear_recurrence", "out", a[8]);
+    no_gradient("linear_recurrence", "state_out", a[9]);
     Call c("linear_recurrence", "gate", a[1]);
     const Recurrence r(c, a[1], a[2], a[4], a[5], a[6]);
     const Tokens out = tokens_of(c, "out", a[8], r.gate.t, r.x_dtype, r.packed);
@@ -383,9 +386,12 @@ PyObject *linear_recurrence(PyObject *const *a)
 // linear_recurrence_backward(stream, gate, x, out, dout, state, dstate_out, kind, blend, starts, dgate, dx, dstate, workspace)
 PyObject *linear_recurrence_backward(PyObject *const *a)
 {
-    static constexpr const char *inputs[] = {"gate", "x", "out", "dout", "state", "dstate_out"};
+    static constexpr const char *inputs[] = {"gate", "x", "out", "dout", "state", "dstate_out"},
+                                *outputs[] = {"dgate", "dx", "dstate"};
     for (int i = 0; i < 6; ++i)
-        no_tangent("linear_recurrence_backward", inputs[i], a[i + 1]);
+        no_gradient("linear_recurrence_backward", inputs[i], a[i + 1]);
+    for (int i = 0; i < 3; ++i)
+        no_gradient("linear_recurrence_backward", outputs[i], a[i + 10]);
     Call c("linear_recurrence_backward", "gate", a[1]);
     const Recurrence r(c, a[1], a[2], a[7], a[8], a[9]);
     const Tokens out = tokens_of(c, "out", a[3], r.gate.t, r.x_dtype, r.packed),
@@ -405,6 +411,7 @@ PyObject *beam_select(PyObject *const *a)
 {
     no_gradient("beam_select", "logits", a[1]);
     no_gradient("beam_select", "scores", a[2]);
+    no_gradient("beam_select", "best", a[6]);
     Call c("beam_select", "logits", a[1]);
     const at::Tensor &x = c.lines("logits", a[1]), &scores = c.here("scores", a[2]);
     const int code = c.prob_code("logits", x);
@@ -503,7 +510,7 @@ PyObject *copy_blocks(PyObject *const *a)
     std::vector<rk_block_cache> caches;
     caches.reserve(size_t(count));
     for (Py_ssize_t i = 0; i < count; ++i) {
-        no_tangent("copy_blocks", "caches", PySequence_Fast_GET_ITEM(a[1], i));
+        no_gradient("copy_blocks", "caches", PySequence_Fast_GET_ITEM(a[1], i));
         const at::Tensor &t = c.here("caches", PySequence_Fast_GET_ITEM(a[1], i));
         if (t.dim() < 1)
             refuse("%s: %s takes tensors of blocks", c.name, "caches");

@@ -94,7 +94,8 @@ def linear_recurrence_backward(gate, x, out, dout, state=None, dstate_out=None, 
     its outputs (rk_linear_recurrence_backward): out is what it returned, dout
     the gradient of that, dstate_out the last states' (None: zeros).  Returns
     (dgate, dx, dstate).  Where they are not given, tokens of no sequence get
-    zeros."""
+    zeros.  There is no second derivative: tensors that require grad are refused
+    where gradients are recorded."""
     code = _kind("linear_recurrence_backward", kind)
     handle = _handle("linear_recurrence_backward", "gate", gate, stream)
     if dgate is None:

@@ -254,7 +254,8 @@ def copy_blocks(caches, pairs, stream=None):
     """Copy blocks inside caches (rk_copy_blocks): block pairs[i, 1] becomes
     what block pairs[i, 0] is; pairs with an id outside a cache are left out.
     caches: a list of tensors whose first dim counts the blocks, each block
-    contiguous; pairs: int32.  Returns caches."""
+    contiguous; pairs: int32.  Returns caches.  Caches that require grad are
+    refused where gradients are recorded."""
     handle = _handle("copy_blocks", "pairs", pairs, stream)
     rc = _calls.copy_blocks(handle, caches, pairs)
     if rc:

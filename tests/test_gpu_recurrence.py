@@ -384,6 +384,20 @@ def test_tangents_are_refused():
     assert torch.equal(out, rk.linear_recurrence(x, x)[0])
 
 
+def test_gradients_are_not_dropped():
+    rk = _rk()
+    x = torch.rand(2, 30, 8, generator=gen(2)).to(DEV)
+    leaf, pairs = x.clone().requires_grad_(), torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    for call in (lambda: rk.linear_recurrence_backward(leaf, x, x, x), lambda: rk.linear_recurrence_backward(x, x, x, leaf),
+                 lambda: rk.linear_recurrence(x, x, out=leaf), lambda: rk.linear_recurrence_backward(x, x, x, x, dx=leaf),
+                 lambda: rk.copy_blocks([x.clone(), leaf], pairs)):
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
+        with torch.no_grad():
+            call()
+    assert torch.equal(leaf[0], leaf[1])
+
+
 def test_same_bits_every_time():
     rk = _rk()
     g = gen(1)

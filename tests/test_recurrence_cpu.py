@@ -155,6 +155,29 @@ def test_tangents_are_not_dropped():
         each(["x"], lambda a: calls.softmax(0, a["x"], None, x, None))
 
 
+def test_gradients_are_not_dropped():
+    """What requires grad, read or written, is refused where gradients are recorded and the call would leave it without."""
+    rk = _rk()
+    calls = rk.linear_recurrence.__globals__["_calls"]
+    x = torch.zeros(2, 3, 4)
+    inputs = ["gate", "x", "out", "dout", "state", "dstate_out", "dgate", "dx", "dstate"]
+    for n in inputs:
+        a = {i: torch.zeros(2, 4) if "state" in i else x.clone() for i in inputs}
+        a[n].requires_grad_()
+        back = lambda: calls.linear_recurrence_backward(  # noqa: E731
+            0, a["gate"], a["x"], a["out"], a["dout"], a["state"], a["dstate_out"], 0, 0, None, a["dgate"], a["dx"], a["dstate"], None)
+        forward = lambda: calls.linear_recurrence(0, a["gate"], a["x"], a["state"], 0, 0, None, None, a["out"], a["dstate"], None)  # noqa: E731
+        for call, name in ((back, n), (forward, {"dstate": "state_out"}.get(n, n) if n in ("gate", "x", "state", "out", "dstate") else None)):
+            if name:
+                with pytest.raises(ValueError, match=name + " requires grad"):
+                    call()
+                with torch.no_grad(), pytest.raises(ValueError, match="not on a GPU"):
+                    call()
+    s = torch.zeros(2, 4)
+    with pytest.raises(ValueError, match="best requires grad"):
+        calls.beam_select(0, s, s, 1, None, 0, s.clone().requires_grad_(), s, s, None)
+
+
 @pytest.mark.parametrize("kind", ["value", "log", "sigmoid"])
 @pytest.mark.parametrize("blend", [False, True])
 def test_plain_gradient_is_the_slope(kind, blend):
