@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <initializer_list>
 #include <vector>
 
 #include "rk.h"
@@ -186,6 +187,25 @@ void *handle(PyObject *o)
 
 PyObject *status(int rc) { return PyLong_FromLong(rc); }
 
+// What a call has written counts as changed in place, as with torch's own calls: a
+// graph that has saved it refuses to go backward, rather than taking the new values.
+void written(PyObject *o)
+{
+    if (!THPVariable_Check(o))
+        return;                                // (None)
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_inference())                     // (which have no counters)
+        t.unsafeGetTensorImpl()->bump_version();
+}
+
+PyObject *status(int rc, std::initializer_list<PyObject *> tensors)
+{
+    if (rc == RK_OK)
+        for (PyObject *o : tensors)
+            written(o);
+    return status(rc);
+}
+
 // No call has a forward derivative: what carries a tangent is refused rather than
 // left without.  (no_grad does not turn these off, an autograd function's forward
 // does.)
@@ -221,7 +241,7 @@ PyObject *softmax(PyObject *const *a)
     const int to = c.prob_code("out", out);
     const auto *tp = static_cast<const float *>(c.flat_or_null("temperature", a[2], lines, at::kFloat));
     return status(p_softmax(in, to, x.data_ptr(), n, lines, x.stride(0), tp, out.data_ptr(), out.stride(0), ws.at,
-                            ws.bytes, handle(a[0])));
+                            ws.bytes, handle(a[0])), {a[3]});
 }
 
 PyObject *draft_verify(PyObject *const *a)
@@ -254,7 +274,7 @@ PyObject *draft_verify(PyObject *const *a)
     auto *tp = c.flat("tokens", a[8], req * (int64_t(max_draft) + 1), ids);
     auto *ap = static_cast<int32_t *>(c.flat("accepted", a[9], req, at::kInt));
     return status(p_draft_verify(code, tok, p.data_ptr(), p.stride(0), q, qs, vocab, req, drafts, max_draft, sp, xp, up, rp,
-                                 tp, ap, ws.at, ws.bytes, handle(a[0])));
+                                 tp, ap, ws.at, ws.bytes, handle(a[0])), {a[8], a[9]});
 }
 
 PyObject *block_tables(PyObject *const *a)
@@ -277,7 +297,7 @@ PyObject *block_tables(PyObject *const *a)
     auto *sp = static_cast<int64_t *>(c.flat("state_out", a[8], 4, at::kLong));
     return status(p_block_tables(lp, req, block, hp, op, static_cast<int32_t *>(table.data_ptr()), table.stride(0), int(width),
                                  rp, places, static_cast<const int64_t *>(state.data_ptr()), sp, ws.at, ws.bytes,
-                                 handle(a[0])));
+                                 handle(a[0])), {a[4], a[5], a[7], a[8]});
 }
 
 PyObject *slot_map(PyObject *const *a)
@@ -299,7 +319,7 @@ PyObject *slot_map(PyObject *const *a)
     auto *qp = static_cast<int32_t *>(c.flat("requests", a[10], capacity, at::kInt));
     auto *tp = static_cast<int32_t *>(c.flat("starts", a[11], req + 1, at::kInt));
     return status(p_slot_map(lp, fp, req, block, static_cast<const int32_t *>(table.data_ptr()), table.stride(0), int(width), hp,
-                             integer(a[6]), code, capacity, sp, pp, qp, tp, handle(a[0])));
+                             integer(a[6]), code, capacity, sp, pp, qp, tp, handle(a[0])), {a[8], a[9], a[10], a[11]});
 }
 
 Tokens tokens_of(const Call &c, const char *what, PyObject *o, const at::Tensor *like, at::ScalarType dtype, bool packed)
@@ -380,7 +400,8 @@ PyObject *linear_recurrence(PyObject *const *a)
     float *last = r.states(c, "state_out", a[9], r.n_seq);
     const Buffer ws = c.workspace(a[10]);
     return status(p_recurrence(r.x_code, r.gate_code, r.kind, r.blend, &r.gate.rows, &r.x.rows, state, lines, sources,
-                               r.starts, r.n_seq, r.tokens, r.channels, &out.rows, last, ws.at, ws.bytes, handle(a[0])));
+                               r.starts, r.n_seq, r.tokens, r.channels, &out.rows, last, ws.at, ws.bytes, handle(a[0])),
+                  {a[8], a[9]});
 }
 
 // linear_recurrence_backward(stream, gate, x, out, dout, state, dstate_out, kind, blend, starts, dgate, dx, dstate, workspace)
@@ -403,7 +424,7 @@ PyObject *linear_recurrence_backward(PyObject *const *a)
     const Buffer ws = c.workspace(a[13]);
     return status(p_recurrence_backward(r.x_code, r.gate_code, r.kind, r.blend, &r.gate.rows, &r.x.rows, &out.rows, &dout.rows,
                                         state, dlast, r.starts, r.n_seq, r.tokens, r.channels, &dgate.rows, &dx.rows, dstate,
-                                        ws.at, ws.bytes, handle(a[0])));
+                                        ws.at, ws.bytes, handle(a[0])), {a[10], a[11], a[12]});
 }
 
 // beam_select(stream, logits, scores, count, ended, end_token, best, tokens, parents, workspace)
@@ -436,7 +457,7 @@ PyObject *beam_select(PyObject *const *a)
     auto *pp = static_cast<int32_t *>(c.flat("parents", a[8], req * count, at::kInt));
     const Buffer ws = c.workspace(a[9]);
     return status(p_beam_select(code, tok, x.data_ptr(), x.stride(0), x.size(1), req, int(beams), sp, ep, integer(a[5]), count,
-                                bp, tp, pp, ws.at, ws.bytes, handle(a[0])));
+                                bp, tp, pp, ws.at, ws.bytes, handle(a[0])), {a[6], a[7], a[8]});
 }
 
 int64_t *state_out_of(const Call &c, PyObject *o) { return static_cast<int64_t *>(c.flat("state_out", o, 4, at::kLong)); }
@@ -468,7 +489,7 @@ PyObject *fork_blocks(PyObject *const *a)
     return status(p_fork_blocks(par, out, lens, rows, small_integer(a[3]), held, static_cast<const int32_t *>(table.data_ptr()),
                                 table.stride(0), int(width), ring, places, static_cast<const int64_t *>(state.data_ptr()),
                                 integer(a[8]), static_cast<int32_t *>(to.data_ptr()), to.stride(0), ho, lo, pairs, so, ws.at,
-                                ws.bytes, handle(a[0])));
+                                ws.bytes, handle(a[0])), {a[6], a[9], a[10], a[11], a[12], a[13]});
 }
 
 // compact_blocks(stream, held, table, ring, n_blocks, table_out, pairs, state_out, workspace)
@@ -491,7 +512,7 @@ PyObject *compact_blocks(PyObject *const *a)
     const Buffer ws = c.workspace(a[8]);
     return status(p_compact_blocks(held, rows, static_cast<const int32_t *>(table.data_ptr()), table.stride(0), int(width),
                                    integer(a[4]), static_cast<int32_t *>(to.data_ptr()), to.stride(0), ring, places, pp, most, so,
-                                   ws.at, ws.bytes, handle(a[0])));
+                                   ws.at, ws.bytes, handle(a[0])), {a[3], a[5], a[6], a[7]});
 }
 
 // copy_blocks(stream, caches, pairs)
@@ -523,7 +544,10 @@ PyObject *copy_blocks(PyObject *const *a)
         const int64_t size = int64_t(t.element_size());
         caches.push_back(rk_block_cache{t.data_ptr(), t.stride(0) * size, whole * size, t.size(0)});
     }
-    return status(p_copy_blocks(caches.data(), int(count), pairs, n / 2, handle(a[0])));
+    const int rc = p_copy_blocks(caches.data(), int(count), pairs, n / 2, handle(a[0]));
+    for (Py_ssize_t i = 0; i < count && rc == RK_OK; ++i)
+        written(PySequence_Fast_GET_ITEM(a[1], i));
+    return status(rc);
 }
 
 // bind(softmax, draft_verify, ...): the library's functions, in the order above.

@@ -398,6 +398,66 @@ def test_gradients_are_not_dropped():
     assert torch.equal(leaf[0], leaf[1])
 
 
+def test_what_is_written_is_known_to_autograd():
+    """A tensor that a graph has saved and a call then overwrites: the graph's backward pass refuses, and what is only
+    read stays usable."""
+    rk = _rk()
+    g = gen(6)
+    n = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    w, x = n(4, 6, 8).requires_grad_(), n(4, 6, 8).sigmoid()
+
+    def overwrite(t, call):
+        """call(t) writes to t, which a product with a leaf has saved."""
+        leaf = torch.randn(t.shape, generator=g).to(DEV).requires_grad_()
+        saved = (leaf * t).sum()
+        with torch.no_grad():
+            call(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.backward()
+
+    overwrite(x.clone(), lambda t: rk.linear_recurrence(t, x, out=t))
+    overwrite(n(4, 8), lambda t: rk.linear_recurrence(x, x, state=t, state_out=t))
+    for name in ("dgate", "dx", "dstate"):
+        overwrite(n(4, 8) if name == "dstate" else x.clone(), lambda t: rk.linear_recurrence_backward(x, x, x, x, **{name: t}))
+    overwrite(n(4, 6), lambda t: rk.copy_blocks([t], i32([1, 2])))
+    overwrite(n(2, 3), lambda t: rk.beam_select(n(6, 9), n(2, 3), best=t))
+    overwrite(n(4, 9), lambda t: rk.softmax(t, out=t))
+
+    table, held, ring, state = i32([3, 1], [2, 0]), i32(2, 2), i32(4, 5, 6, 7, 8, 9, 10, 11), torch.tensor([0, 8, 0, 0], device=DEV)
+    outs = dict(table_out=i32([0, 0], [0, 0]), held_out=i32(0, 0), lens_out=i32(0, 0), pairs=i32([0, 0], [0, 0]))
+    every = [ring, state, *outs.values()]
+    before = [t._version for t in every]
+    rk.fork_blocks(i32(0, 0), i32(20, 20), 16, held, table, ring, state, 12, **outs)
+    assert all(t._version > b for t, b in zip(every, before)) and table._version == held._version == 0
+    moves, after = torch.empty(6, 2, dtype=torch.int32, device=DEV), torch.empty(4, dtype=torch.int64, device=DEV)
+    every = [table, moves, after]
+    before = [t._version for t in every]
+    ring12 = i32(*range(12))
+    rk.compact_blocks(held, table, ring12, 12, pairs=moves, state_out=after)
+    assert all(t._version > b for t, b in zip(every, before)) and ring12._version > 0 and held._version == 0
+    every = [table, held, ring, state]
+    before = [t._version for t in every]
+    rk.block_tables(i32(20, 20), 16, held, table, ring, state)
+    assert all(t._version > b for t, b in zip(every, before))
+    outs = rk.slot_map(i32(20, 20), i32(1, 1), 16, table, held, 12, capacity=4)
+    before = [t._version for t in outs]
+    rk.slot_map(i32(20, 20), i32(1, 1), 16, table, held, 12, slots=outs[0], positions=outs[1], requests=outs[2], starts=outs[3])
+    assert all(t._version > b for t, b in zip(outs, before))
+
+    # inputs that are only read, a refused call's buffers, and tensors of inference mode
+    out, _ = rk.linear_recurrence(w, x, kind="sigmoid")
+    with torch.no_grad():
+        rk.linear_recurrence(w, x)
+        with pytest.raises(rk.RkError):
+            rk.linear_recurrence(x, w, out=out[:, :1].expand(4, 6, 8))
+    out.sum().backward()
+    with torch.inference_mode():
+        t = x.clone()
+    with torch.no_grad():
+        rk.linear_recurrence(t, x, out=t)
+
+
 def test_same_bits_every_time():
     rk = _rk()
     g = gen(1)
