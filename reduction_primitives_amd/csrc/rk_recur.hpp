@@ -12,13 +12,17 @@ namespace tune {
 constexpr int kRecurBlock = 256;          // threads
 constexpr int kRecurVec = 4;              // channels of a lane (1 where there are fewer)
 // Most channels of a tile, so that a row of it is a whole 128-byte line of 16-bit
-// elements (32: 65536 x 2048 bf16 forward 272 us against 260, 512 x 64 x 2048
-// backward 250 against 178).
+// elements (32, in an earlier version: 65536 x 2048 bf16 forward 272 us against 260,
+// 512 x 64 x 2048 backward 250 against 178).
 constexpr int kRecurStrip = 64;
 // Sequences of so many tokens, up to so many of them, are columns of their own:
 // the tiles that run at the same time are then mostly other sequences', not the
-// ones a tile waits for (8 x 4096 x 2048 bf16 forward 109 us, one after the other
-// 125).
+// ones a tile waits for.  Apart and one after the other, bf16 forward, us a call: 64 x
+// 512 x 2048 102 and 112, 32 x 1024 x 2048 107 and 117, 1024 x 512 x 128 96 and 119
+// (backward 187 and 193, 192 and 198, 181 and 199); 64 x 256 x 2048 55 and 57, 2 x 256
+// x 2048 12.2 and 11.9.  The borders are rough: sequences that fill a tile together
+// gain nothing (4096 x 512 x 4: 41 and 20), and beyond 4096 of them some still would
+// (8192 x 512 x 32: 171 and 196).
 constexpr int64_t kRecurApart = 512, kRecurApartMost = 4096;
 // Polls of a look-back (a microsecond each) before its block does the work of one
 // that has not been started.
@@ -32,10 +36,10 @@ static_assert(kRecurPatienceAgain <= kRecurPatience, "polls begin at the differe
 }  // namespace tune
 
 // Most tokens of a lane: what leaves the registers for kRecurWaves waves.  The bytes
-// that blocks have on their way bound the rate: with three waves a SIMD 8 x 4096 x
-// 2048 bf16 backward took 219 us, with four 204; forward with 12 tokens, gates
-// computed twice to make room for them, 16 x 4096 x 2048 took 233 us, with 8 and
-// gates kept 207.
+// that blocks have on their way bound the rate: with three waves a SIMD, in an earlier
+// version, 8 x 4096 x 2048 bf16 backward took 219 us, with four 204; forward with 12
+// tokens, gates computed twice to make room for them, 16 x 4096 x 2048 took 233 us,
+// with 8 and gates kept 207.
 constexpr int recur_rows(int x_size, int gate_size, bool backward)
 {
     return backward && gate_size + 3 * x_size > 8 ? 4 : 8;

@@ -28,12 +28,13 @@
 //
 // States, products of gates and sums are float32; outputs are rounded once.
 //
-// Measured, bf16 unless said: 512 x 128 tokens x 2048, where no tile waits, 167 us forward
-// (805 MB, 4.8 TB/s) and 512 x 64 backward 172 (as many bytes); 16 x 4096 203, 1 x 65536
-// 246 (3.3 TB/s), 8 x 4096 backward 195, 20011 x 1001 float32 backward 137.  What the
-// tiles wait for each other is what is left, and 5 us of clearing the records: four
-// blocks a CU hide a load's latency but not that as well, and a fifth has no registers
-// (40 spilled).  (Blocks that go from tile to tile with the next one's inputs loaded
+// Measured, us a call, 2048 channels of bf16 unless said: 512 x 128 tokens, where no tile
+// waits, 167 forward (805 MB, 4.8 TB/s) and 512 x 64 backward 173 (as many bytes); 16 x
+// 4096 forward 207, 4 x 16384 204, 1 x 65536 247 (3.3 TB/s), 8 x 4096 109, 1 x 4096 21, 37
+// sequences packed in 20011 tokens 87; 8 x 4096 backward 197, 20011 x 1001 float32 packed
+// 138.  What the tiles wait for each other is what is left, and 5 to 7 us of clearing the
+// records: four blocks a CU hide a load's latency but not that as well, and a fifth has no
+// registers (40 spilled).  (Blocks that go from tile to tile with the next one's inputs loaded
 // ahead took 337 us for 1 x 65536: three blocks a CU then, and loads that come back in
 // order behind the look-back's.  The other three waves loading the 12 records before the
 // nearest four while the first polls: 258 us, for the traffic.)

@@ -71,7 +71,11 @@ constexpr int kLdsBytes = 160 << 10;      // of a CU
 constexpr int64_t kSlotStreamBytes = int64_t(32) << 20;
 // ---- beam selection
 constexpr int kBeamBlock = 256;
-constexpr int kBeamTile = 2048;           // vocabulary entries of a wave's tile
+// Vocabulary entries of a wave's tile: what suits many lines.  With 1024, 2048 and 4096,
+// us a call: 64 x 8 x 131072 bf16 42.7, 38.6 and 43.4, 64 x 8 x 32768 f32 24.8, 25.2 and
+// 27.2; few lines go either way (1 x 4 x 32768 f32 11.1, 11.4 and 12.0; 1 x 4 x 131072
+// bf16 17.8, 13.3 and 12.0, 16 x 4 18.3, 17.3 and 14.6).
+constexpr int kBeamTile = 2048;
 constexpr int kBeamWavesPerCu = 16;       // waves of the first launch = CUs * this, or a wave a tile
 constexpr int kBeamMost = 64;             // candidates kept of a request: a lane each
 constexpr int kBeamLines = 4096;          // beams of a request, 12 bytes of LDS each
@@ -79,10 +83,17 @@ constexpr int kBeamLines = 4096;          // beams of a request, 12 bytes of LDS
 constexpr int kPageBlock = 256;
 constexpr int kPageSeg = 1024;            // entries of a new row that a wave copies
 constexpr int kPageRows = 8;              // old rows that a wave goes through, 64 entries of each
-constexpr int kPageLdsRows = 4096;        // rows (old and new each) that every block plans for itself in LDS
+// Rows (old and new each) that every block plans for itself in LDS.  So and in launches of
+// their own, us a call, tables of 4 k tokens: 64 rows 18.5 and 24.3, 1024 20.4 and 24.8, 2048
+// 25.5 and 28.1, 2560 27.3 and 29.7; but 4000 rows 50.6 and 36.3 (a thread sums up 16 counts
+// in a row then, 32 lanes in the same LDS bank).
+constexpr int kPageLdsRows = 4096;
 constexpr int kPageBlocksPerCu = 8;       // grid cap = CUs * this
 constexpr int kCompactChunk = 4096;       // ids whose flags a block packs
-constexpr int kCompactOwn = 65536;        // ids of a pool whose flags every block packs for itself
+// Ids of a pool whose flags every block packs for itself.  So and in launches of their own, us
+// a call: 408 ids 12.7 and 17.1, 5030 13.1 and 17.5, 36273 13.5 and 17.8, 45737 13.1 and 17.6,
+// and with 4000 rows (39592 ids) 13.8 and 17.9.
+constexpr int kCompactOwn = 65536;
 constexpr int kCompactSums = 4096;        // chunks that every block sums up for itself
 constexpr int kCopyCaches = 64;           // caches of a launch
 constexpr int kCopyBlocksPerCu = 16;      // blocks of a launch = CUs * this, or one a pair of a chunk

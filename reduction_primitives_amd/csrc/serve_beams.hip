@@ -15,7 +15,7 @@
 // the count-th largest of the lanes' maxima, later also what other waves of the block
 // have for the same line.  (A sorted list across the lanes, each entry put in its
 // place: 50 instructions an entry, more than the exponentials, and 41 us where this
-// takes XX, at 512 lines of 131072 bf16.)  Equal entries without end, as in a line of
+// takes 33, at 512 lines of 131072 bf16.)  Equal entries without end, as in a line of
 // one value, are put into such a list all the same, one after the other.
 //
 // Second launch: a block a request folds its lines' sums, finds a bar the same way,

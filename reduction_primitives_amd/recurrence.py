@@ -57,7 +57,9 @@ def linear_recurrence(gate, x, state=None, kind="value", blend=False, starts=Non
     (sequences, channels), zeros where it is None; with sources (int32),
     sequence b starts from line sources[b] of it.  Returns (out, state_out): every
     token's h, of x's dtype, and the last ones in float32; state_out may be state
-    where there are no sources.
+    where there are no sources.  Up to 2048 gates in a row are folded into one
+    float32 factor: with gates above 1, one that leaves float32's range makes a
+    state infinite or NaN that need not be.
 
     Where gradients are recorded and gate, x or state requires one, the outputs
     have them (of the first order, computed on the stream that was current;
