@@ -565,6 +565,36 @@ def test_blocks_help_in_place(types, channels, cuts):
             assert torch.equal(a[rows] if a.shape == x.shape else a, b[rows] if b.shape == x.shape else b)
 
 
+def test_states_in_place_in_a_captured_graph():
+    """Chunk after chunk through one graph, the last states in the first ones' place: each replay starts from what the one
+    before left, and keeps it apart in the workspace again."""
+    rk = _rk()
+    g = gen(12)
+    chunks = [(gates(g, (3, 900, 70), "sigmoid", BF16).to(DEV), torch.randn(3, 900, 70, generator=g).to(BF16).to(DEV)) for _ in range(4)]
+    first = torch.randn(3, 70, generator=g).to(DEV)
+    want, last = [], first
+    for a, v in chunks:
+        out, last = rk.linear_recurrence(a, v, state=last, kind="sigmoid", blend=True)
+        want.append((out, last))
+    gate, x, state = chunks[0][0].clone(), chunks[0][1].clone(), first.clone()
+    out = torch.empty_like(x)
+    n = rk.rk_linear_recurrence_workspace_size(rk.RK_BF16, rk.RK_BF16, 3, 900, 70, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rk.linear_recurrence(gate, x, state=state, kind="sigmoid", blend=True, out=out, state_out=state, workspace=ws)
+    for _ in range(2):
+        state.copy_(first)
+        for (a, v), (o, s) in zip(chunks, want):
+            gate.copy_(a)
+            x.copy_(v)
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, o) and torch.equal(state, s)
+
+
 def test_no_gradients_are_recorded_in_a_capture():
     """An eager graph of the same leaves is alive; the captured backward call gives what autograd gives."""
     rk = _rk()
